@@ -449,7 +449,8 @@ def work(case):
 # ---- the definitions in 64 bits ---------------------------------------------
 
 def _pow2(e):
-    return torch.ldexp(torch.ones_like(e, dtype=torch.float64), e)
+    """2^e exactly: the exponent field of a double."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
 
 
 def _floor_log2(v):
