@@ -37,18 +37,22 @@ def sources():
     return cu, cpp
 
 
-def _headers_mtime():
-    paths = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    paths.append(os.path.join(ROOT, "include", "gemm.h"))
-    return max(os.path.getmtime(p) for p in paths)
+def _up_to_date(out):
+    """Whether the object is newer than every file its last compilation read
+    (the dependency file the compiler wrote beside it)."""
+    try:
+        built = os.path.getmtime(out)
+        with open(out + ".d") as f:
+            deps = f.read().split(":", 1)[1].replace("\\\n", " ").split()
+        return all(os.path.getmtime(d) <= built for d in deps)
+    except (OSError, IndexError):
+        return False
 
 
-def _compile(cmd, out, src, hdr_mtime, force):
-    if not force and os.path.exists(out):
-        m = os.path.getmtime(out)
-        if m >= os.path.getmtime(src) and m >= hdr_mtime:
-            return None
-    r = subprocess.run(cmd, capture_output=True, text=True)
+def _compile(cmd, out, force):
+    if not force and _up_to_date(out):
+        return None
+    r = subprocess.run(cmd + ["-MD", "-MF", out + ".d"], capture_output=True, text=True)
     if r.returncode != 0:
         return f"{' '.join(cmd)}\n{r.stdout}\n{r.stderr}"
     return None
@@ -62,20 +66,19 @@ def build(force: bool = False, verbose: bool = False, checks: bool = False) -> s
     nvcc = _nvcc()
     inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC] + (["-DQG_DEVICE_CHECKS"] if checks else [])
     cu, cpp = sources()
-    hdr = _headers_mtime()
     jobs = []
     for f in cu:
         out = os.path.join(build_dir, f + ".o")
         cmd = [nvcc, "-gencode", GENCODE, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC",
                "-Xcompiler", "-Wall", *inc, "-c", os.path.join(CSRC, f), "-o", out]
-        jobs.append((cmd, out, os.path.join(CSRC, f)))
+        jobs.append((cmd, out))
     for f in cpp:
         out = os.path.join(build_dir, f + ".o")
         cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", *inc, "-I", _cuda_include(), "-c",
                os.path.join(CSRC, f), "-o", out]
-        jobs.append((cmd, out, os.path.join(CSRC, f)))
+        jobs.append((cmd, out))
     with cf.ThreadPoolExecutor(max_workers=max(2, min(len(jobs), os.cpu_count() or 4))) as ex:
-        errs = [e for e in ex.map(lambda j: _compile(*j, hdr, force), jobs) if e]
+        errs = [e for e in ex.map(lambda j: _compile(*j, force), jobs) if e]
     if errs:
         raise RuntimeError("libqgemm build failed:\n" + "\n".join(errs))
     objs = [j[1] for j in jobs]
