@@ -56,7 +56,8 @@ typedef enum {
     GEMM_F32 = 0, GEMM_F16 = 1, GEMM_BF16 = 2,
     GEMM_S4 = 3,                /* two's-complement nibbles, two per byte        */
     GEMM_S8 = 4,                /* int8 (quantised D)                           */
-    GEMM_E4M3 = 5, GEMM_E5M2 = 6 /* 8-bit floats (1-4-3 bias 7, no infinity; 1-5-2 bias 15) */
+    GEMM_E4M3 = 5, GEMM_E5M2 = 6, /* 8-bit floats (1-4-3 bias 7, no infinity; 1-5-2 bias 15) */
+    GEMM_E2M1 = 7               /* 4-bit floats with block scales (gemm_mx.h only)  */
 } gemm_dtype_t;
 typedef enum { GEMM_ROW_MAJOR = 0, GEMM_COL_MAJOR = 1 } gemm_order_t;
 

@@ -1,7 +1,7 @@
 """Python binding of the GB300 GEMM library (libqgemm.so).
 
 Argument marshalling only: every function here forwards to the C ABI of
-``include/gemm.h`` under the same name; every step of the GEMM runs in the
+``include/gemm.h`` and ``include/gemm_mx.h`` under the same name; every step of the GEMM runs in the
 library's CUDA kernels.  PyTorch is used for device memory and streams in the
 convenience helpers at the bottom (``layout_of``, ``Workspace``, ``run``).
 
@@ -30,7 +30,8 @@ GEMM_ERR_DEVICE_TIMEOUT = 6
 GEMM_ERR_BAD_CACHE = 7
 GEMM_ERR_DEVICE_CHECK = 8
 
-GEMM_F32, GEMM_F16, GEMM_BF16, GEMM_S4, GEMM_S8, GEMM_E4M3, GEMM_E5M2 = 0, 1, 2, 3, 4, 5, 6
+GEMM_F32, GEMM_F16, GEMM_BF16, GEMM_S4, GEMM_S8, GEMM_E4M3, GEMM_E5M2, GEMM_E2M1 = 0, 1, 2, 3, 4, 5, 6, 7
+GEMM_MXFP4, GEMM_NVFP4 = 1, 2  # 4-bit microscaled formats (gemm_mx.h)
 GEMM_ROW_MAJOR, GEMM_COL_MAJOR = 0, 1
 GEMM_DISPATCH_DEFAULT, GEMM_DISPATCH_MEASURE, GEMM_DISPATCH_REUSE = 0, 1, 2
 GEMM_EPILOGUE_DEFAULT, GEMM_EPILOGUE_BIAS, GEMM_EPILOGUE_RELU, GEMM_EPILOGUE_GELU = 0, 1, 2, 4
@@ -45,6 +46,11 @@ SYMBOLS = (
     "gemm_get_tuning_seq", "gemm_cache_size", "gemm_status_string", "gemm_device_status",
     "gemm_selftest_wait_timeout", "gemm_last_choice", "gemm_plan_streamk", "gemm_grouped_block",
     "gemm_run_noalloc", "gemm_heuristic_choice", "gemm_checked_build",
+)
+# ... and of gemm_mx.h.
+MX_SYMBOLS = (
+    "gemm_mx_scale_size", "gemm_mx_quantize", "gemm_mx_dequantize", "gemm_run_mx", "gemm_run_mx_grouped",
+    "gemm_mx_norm_quantize",
 )
 
 
@@ -75,6 +81,13 @@ class gemm_op_t(ctypes.Structure):
 class gemm_workspace_t(ctypes.Structure):
     _fields_ = [("barriers", ctypes.c_void_p), ("barriers_size", ctypes.c_size_t),
                 ("partials", ctypes.c_void_p), ("partials_size", ctypes.c_size_t)]
+
+
+class gemm_mx_norm_t(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("tensor_scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("post_weight", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
+                ("weight_type", ctypes.c_int32), ("gate_type", ctypes.c_int32), ("gate", ctypes.c_void_p),
+                ("gate_ld", ctypes.c_int64)]
 
 
 _lib = None
@@ -115,6 +128,15 @@ def lib():
         "gemm_heuristic_choice": (ctypes.c_int, [I64, I64, I64, I32, I32, I32, I32, I32, I32, I32, ctypes.c_size_t,
                                                  ctypes.c_char_p, ctypes.c_size_t]),
         "gemm_checked_build": (ctypes.c_int, []),
+        "gemm_mx_scale_size": (ctypes.c_int, [I32, I64, I64, I32, ctypes.POINTER(SZ)]),
+        "gemm_mx_quantize": (ctypes.c_int, [P, I32, F, P, LP, P, LP, P, SZ, P, I32, P]),
+        "gemm_mx_dequantize": (ctypes.c_int, [P, I32, F, P, LP, P, SZ, P, LP, P, I32, P]),
+        "gemm_run_mx": (ctypes.c_int, [P, ctypes.POINTER(gemm_op_t), I32, F, P, LP, P, SZ, P, LP, P, SZ, F, P, LP, P,
+                                       LP, P]),
+        "gemm_run_mx_grouped": (ctypes.c_int, [P, ctypes.POINTER(gemm_op_t), I32, F, P, P, LP, P, SZ, P, LP, P, SZ, F,
+                                               P, LP, P, LP, P, I32, P]),
+        "gemm_mx_norm_quantize": (ctypes.c_int, [P, ctypes.POINTER(gemm_mx_norm_t), P, LP, P, LP, P, LP, P, LP, P, SZ,
+                                                 P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -244,6 +266,47 @@ def gemm_grouped_block(sizes, block_m, block):
     return tuple(out)
 
 
+# ---- 4-bit microscaled operators (gemm_mx.h) -----------------------------------------
+
+def gemm_mx_scale_size(format, rows, cols, num_experts=0) -> int:
+    """Bytes of the scales of a rows x cols operand (rows sorted by num_experts
+    experts when that is not 0)."""
+    n = ctypes.c_size_t()
+    rc = lib().gemm_mx_scale_size(int(format), int(rows), int(cols), int(num_experts), ctypes.byref(n))
+    if rc:
+        raise GemmError(rc, "gemm_mx_scale_size")
+    return n.value
+
+
+def gemm_mx_quantize(h, format, tensor_scale, X, Xdesc, Q, Qdesc, S, S_size, expert_offsets_dev, num_experts, stream):
+    return lib().gemm_mx_quantize(h, format, tensor_scale, X, _lp(Xdesc), Q, _lp(Qdesc), S, S_size,
+                                  expert_offsets_dev, num_experts, stream)
+
+
+def gemm_mx_dequantize(h, format, tensor_scale, Q, Qdesc, S, S_size, D, Ddesc, expert_offsets_dev, num_experts,
+                       stream):
+    return lib().gemm_mx_dequantize(h, format, tensor_scale, Q, _lp(Qdesc), S, S_size, D, _lp(Ddesc),
+                                    expert_offsets_dev, num_experts, stream)
+
+
+def gemm_run_mx(h, op, format, alpha, A, Adesc, SA, SA_size, B, Bdesc, SB, SB_size, beta, C, Cdesc, D, Ddesc, stream):
+    """Returns the status code (0 = OK).  Pointers are ints (device addresses)."""
+    return lib().gemm_run_mx(h, ctypes.byref(op), format, alpha, A, _lp(Adesc), SA, SA_size, B, _lp(Bdesc), SB,
+                             SB_size, beta, C, _lp(Cdesc), D, _lp(Ddesc), stream)
+
+
+def gemm_run_mx_grouped(h, op, format, alpha, expert_alpha, A, Adesc, SA, SA_size, B, Bdesc, SB, SB_size, beta, C,
+                        Cdesc, D, Ddesc, expert_offsets_dev, num_experts, stream):
+    return lib().gemm_run_mx_grouped(h, ctypes.byref(op), format, alpha, expert_alpha, A, _lp(Adesc), SA, SA_size, B,
+                                     _lp(Bdesc), SB, SB_size, beta, C, _lp(Cdesc), D, _lp(Ddesc), expert_offsets_dev,
+                                     num_experts, stream)
+
+
+def gemm_mx_norm_quantize(h, op, F, Fdesc, R, Rdesc, O, Odesc, Q, Qdesc, S, S_size, stream):
+    return lib().gemm_mx_norm_quantize(h, ctypes.byref(op), F, _lp(Fdesc), R, _lp(Rdesc), O, _lp(Odesc), Q, _lp(Qdesc),
+                                       S, S_size, stream)
+
+
 # ---- torch convenience (memory and streams only) ------------------------------------
 
 def _dtype_code(t):
@@ -276,6 +339,42 @@ def col_major_from_nk(t, k=None, type_=None):
         return layout(type_, GEMM_COL_MAJOR, kk, t.shape[1], max(t.stride(1) * mult, kk, 1), t.shape[0],
                       t.stride(0) * mult)
     return layout(type_, GEMM_COL_MAJOR, kk, t.shape[0], max(t.stride(0) * mult, kk, 1))
+
+
+def mx_layout(t, k):
+    """Layout of packed E2M1 codes: a uint8 [rows, ld / 2] (or [num, rows,
+    ld / 2]) tensor holding rows of k codes (operand A, or a matrix to quantise
+    to)."""
+    if t.dim() == 3:
+        return layout(GEMM_E2M1, GEMM_ROW_MAJOR, t.shape[1], k, 2 * t.stride(1), t.shape[0], 2 * t.stride(0))
+    return layout(GEMM_E2M1, GEMM_ROW_MAJOR, t.shape[0], k, 2 * t.stride(0))
+
+
+def mx_layout_b(t, k):
+    """Layout of operand B from its packed [N, ld / 2] (or [num, N, ld / 2])
+    codes: a col-major k x N matrix."""
+    if t.dim() == 3:
+        return layout(GEMM_E2M1, GEMM_COL_MAJOR, k, t.shape[1], 2 * t.stride(1), t.shape[0], 2 * t.stride(0))
+    return layout(GEMM_E2M1, GEMM_COL_MAJOR, k, t.shape[0], 2 * t.stride(0))
+
+
+class MxOperand:
+    """Device memory of a rows x k 4-bit operand: packed codes and scales.
+    num_experts: rows sorted by that many experts.  num: that many matrices
+    (the experts' weights)."""
+
+    def __init__(self, format, rows, k, num_experts=0, num=1, device="cuda"):
+        import torch
+        self.format, self.rows, self.k = format, rows, k
+        shape = (rows, -(-k // 32) * 16)
+        self.codes = torch.zeros(shape if num == 1 else (num, *shape), dtype=torch.uint8, device=device)
+        self.scales = torch.zeros(max(num * gemm_mx_scale_size(format, rows, k, num_experts), 16), dtype=torch.uint8,
+                                  device=device)
+
+    def args(self, b=False):
+        """(codes, layout, scales, scale bytes) as the calls take them."""
+        return (self.codes.data_ptr(), (mx_layout_b if b else mx_layout)(self.codes, self.k), self.scales.data_ptr(),
+                self.scales.numel())
 
 
 class Workspace:

@@ -981,6 +981,28 @@ int bind_device(gemm_handle* h) {
 
 }  // namespace
 
+int qg::handle_bind(gemm_handle_t h) { return bind_device(h); }
+bool qg::handle_device_pointer(gemm_handle_t h, const void* p) { return device_pointer(h, p); }
+int qg::handle_encode(gemm_handle_t h, CUtensorMap* m, CUtensorMapDataType type, uint32_t rank, const void* ptr,
+                      const uint64_t* dims, const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
+    cuuint64_t d[5] = {0}, s[5] = {0};
+    cuuint32_t b[5] = {0};
+    for (uint32_t i = 0; i < rank && i < 5; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i + 1 < rank) s[i] = strides[i];
+    }
+    return encode_cached(h, m, type, rank, ptr, d, s, b, swizzle) == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
+}
+int qg::handle_sm_count(gemm_handle_t h) { return h->sm_count; }
+uint32_t* qg::handle_status(gemm_handle_t h) { return h->status; }
+uint64_t qg::handle_timeout_ns(gemm_handle_t h) { return h->timeout_ns; }
+void qg::handle_set_choice(gemm_handle_t h, const char* name, int64_t m, int64_t n, int64_t k) {
+    h->last_choice = name;
+    if (h->log)
+        fprintf(stderr, "qgemm: M=%lld N=%lld K=%lld -> %s\n", (long long)m, (long long)n, (long long)k, name);
+}
+
 extern "C" {
 
 int gemm_run(gemm_handle_t h, const gemm_op_t* op, float alpha, const void* A, const gemm_layout_t* Adesc,

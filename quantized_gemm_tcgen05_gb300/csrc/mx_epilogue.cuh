@@ -1,0 +1,156 @@
+// Epilogue pieces of the 4-bit microscaled products: 32 accumulator columns of
+// one row, held by one thread, to D.
+#pragma once
+#include "common.cuh"
+#include "mx_gemm.h"
+
+namespace qg {
+
+// 32-byte global accesses: a whole sector per lane.
+__device__ __forceinline__ void ld32(const void* p, uint32_t (&w)[8]) {
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p)
+                 : "memory");
+}
+__device__ __forceinline__ void st32(void* p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// Columns n0 .. n0+31 of row m (valid for this lane when `row_ok`), values v
+// before alpha.  Every lane of the warp takes part.  Vector form: every lane
+// moves its own row's 64 or 128 bytes in 32-byte pieces, whole sectors each, so
+// no transposition is needed.  Otherwise (rows not 32-byte aligned, or the
+// tile's last columns) the warp turns the block through `stage` (32 x 33
+// floats) and each lane takes one column, row after row.
+template <int ACT, int DT>
+__device__ __forceinline__ void mx_store_block_t(const EpiParams& ep, bool vec32, float alpha, int64_t m0,
+                                                 int rows, int64_t n0, float (&v)[32], float* stage, int lane) {
+    const EpiParams e = ep;
+    EpiArith ar = epi_arith(e);
+    ar.alpha = alpha;
+    const int64_t m = m0 + lane;
+    const bool use_c = e.beta != 0.0f;
+    if (vec32 && n0 + 32 <= e.N) {
+        const float bl = ACT >= 0 ? bias_at(ar, n0 + lane) : 0.0f;
+        constexpr int ES = DT == DT_F32 ? 4 : 2, PER = 32 / ES;  // elements per piece
+        char* d = static_cast<char*>(e.D) + (m * e.ldd + n0) * ES;
+        const char* c = static_cast<const char*>(e.C) + (m * e.ldc + n0) * ES;
+        const bool ok = lane < rows;
+#pragma unroll
+        for (int q = 0; q < 32 / PER; ++q) {
+            float cv[PER];
+#pragma unroll
+            for (int t = 0; t < PER; ++t) cv[t] = 0.0f;
+            if (use_c && ok) {
+                uint32_t w[8];
+                ld32(c + 32 * q, w);
+#pragma unroll
+                for (int t = 0; t < 8; ++t) {
+                    if constexpr (DT == DT_F32) {
+                        cv[t] = __uint_as_float(w[t]);
+                    } else {
+                        const float2 f = DT == DT_BF16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[t]))
+                                                       : __half22float2(*reinterpret_cast<const __half2*>(&w[t]));
+                        cv[2 * t] = f.x;
+                        cv[2 * t + 1] = f.y;
+                    }
+                }
+            }
+            float x[PER];
+#pragma unroll
+            for (int t = 0; t < PER; ++t) {
+                const float b = ACT >= 0 ? __shfl_sync(0xFFFFFFFFu, bl, PER * q + t) : 0.0f;
+                x[t] = epi_value<ACT>(ar, v[PER * q + t], cv[t], b);
+            }
+            uint32_t w[8];
+#pragma unroll
+            for (int t = 0; t < 8; ++t) {
+                if constexpr (DT == DT_F32) {
+                    w[t] = __float_as_uint(x[t]);
+                } else if constexpr (DT == DT_BF16) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * t], x[2 * t + 1]);
+                    w[t] = *reinterpret_cast<const uint32_t*>(&h);
+                } else {
+                    const __half2 h = __floats2half2_rn(x[2 * t], x[2 * t + 1]);
+                    w[t] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+            }
+            if (ok) st32(d + 32 * q, w);
+        }
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) stage[lane * 33 + j] = v[j];
+    __syncwarp();
+    const int64_t n = n0 + lane;
+    if (n < e.N) {
+        const float b = ACT >= 0 ? bias_at(ar, n) : 0.0f;
+        for (int r = 0; r < rows; ++r) {
+            const int64_t i = (m0 + r) * e.ldd + n;
+            const float c = use_c ? ld_elem(e.C, DT, (m0 + r) * e.ldc + n) : 0.0f;
+            st_elem(e.D, DT, i, epi_value<ACT>(ar, stage[r * 33 + lane], c, b));
+        }
+    }
+    __syncwarp();
+}
+
+template <int DT>
+__device__ __forceinline__ void mx_store_block_dt(const EpiParams& e, bool vec32, float alpha, int64_t m0, int rows,
+                                                  int64_t n0, float (&v)[32], float* stage, int lane) {
+    with_epi_act(e, [&](auto act) {
+        mx_store_block_t<decltype(act)::value, DT>(e, vec32, alpha, m0, rows, n0, v, stage, lane);
+    });
+}
+
+// rows: rows of this warp's 32 that exist (m0 .. m0 + rows - 1).
+__device__ __forceinline__ void mx_store_block(const EpiParams& e, bool vec32, float alpha, int64_t m0, int rows,
+                                               int64_t n0, float (&v)[32], float* stage, int lane) {
+    if (e.d_type == DT_BF16)
+        mx_store_block_dt<DT_BF16>(e, vec32, alpha, m0, rows, n0, v, stage, lane);
+    else if (e.d_type == DT_F16)
+        mx_store_block_dt<DT_F16>(e, vec32, alpha, m0, rows, n0, v, stage, lane);
+    else
+        mx_store_block_dt<DT_F32>(e, vec32, alpha, m0, rows, n0, v, stage, lane);
+}
+
+// Warp-wide: block b (of `bm` rows, a multiple of 128) of rows sorted by
+// expert -> expert, its first row, its rows, and the scale atom row it starts
+// on.  Returns false past the last block.
+__device__ __forceinline__ bool mx_expert_block(const int32_t* off, int32_t E, int bm, int64_t b, int lane,
+                                                int* expert, int64_t* row0, int* rows, int64_t* atom_row) {
+    int64_t blocks = 0, tiles = 0;
+    for (int32_t e0 = 0; e0 < E; e0 += 32) {
+        const int32_t e = e0 + lane;
+        const int64_t lo = e < E ? off[e] : 0, hi = e < E ? off[e + 1] : 0;
+        const int64_t m = hi > lo ? hi - lo : 0;
+        const int nb = (int)((m + bm - 1) / bm), nt = (int)((m + MX_ATOM_ROWS - 1) / MX_ATOM_ROWS);
+        int pb = nb, pt = nt;  // inclusive prefix sums
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int ub = __shfl_up_sync(0xFFFFFFFFu, pb, d), ut = __shfl_up_sync(0xFFFFFFFFu, pt, d);
+            if (lane >= d) {
+                pb += ub;
+                pt += ut;
+            }
+        }
+        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, b < blocks + pb);
+        if (hit) {
+            const int l = __ffs((int)hit) - 1;
+            const int64_t q = b - blocks - __shfl_sync(0xFFFFFFFFu, pb - nb, l);  // block within the expert
+            const int64_t left = __shfl_sync(0xFFFFFFFFu, m, l) - q * bm;
+            *expert = e0 + l;
+            *row0 = __shfl_sync(0xFFFFFFFFu, lo, l) + q * bm;
+            *rows = (int)(left < bm ? left : bm);
+            *atom_row = tiles + __shfl_sync(0xFFFFFFFFu, pt - nt, l) + q * (bm / MX_ATOM_ROWS);
+            return true;
+        }
+        blocks += __shfl_sync(0xFFFFFFFFu, pb, 31);
+        tiles += __shfl_sync(0xFFFFFFFFu, pt, 31);
+    }
+    return false;
+}
+
+}  // namespace qg

@@ -1,0 +1,63 @@
+// Parameter blocks of the 4-bit microscaled kernels (include/gemm_mx.h) and
+// the integer layout rules they share with the host.
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kparams.h"
+
+namespace qg {
+
+enum MxFormat : int32_t { MXF_MXFP4 = 1, MXF_NVFP4 = 2 };
+
+constexpr int MX_ATOM_ROWS = 128;   // rows of a scale atom
+constexpr int MX_ATOM_BYTES = 512;  // 128 rows x 4 blocks
+constexpr int MX_KSTEP = 256;       // codes of one 128-byte swizzle row
+
+QG_HD int32_t mx_block(int32_t format) { return format == MXF_NVFP4 ? 16 : 32; }
+// Atoms along K of one atom row.
+QG_HD int64_t mx_atoms(int32_t format, int64_t cols) { return ceil_div(cols, 4 * (int64_t)mx_block(format)); }
+// Byte of the scale of row r, block b, within a matrix of `atoms` atoms per row.
+QG_HD int64_t mx_scale_at(int64_t r, int64_t b, int64_t atoms) {
+    return ((r / MX_ATOM_ROWS) * atoms + b / 4) * MX_ATOM_BYTES + (r % 32) * 16 + (r % MX_ATOM_ROWS) / 32 * 4 + b % 4;
+}
+
+// Quantisation and its inverse: one matrix of `rows` x `cols`, or `num` of them.
+struct MxQuantParams {
+    const void* X;  // values in (quantise); codes in (dequantise)
+    void* Y;        // codes out; values out
+    uint8_t* S;     // scales
+    int64_t rows, cols;
+    int64_t ldx, x_bstride;  // of the values, elements
+    int64_t ldq, q_bstride;  // of the codes, bytes
+    int64_t s_bstride;       // bytes
+    int32_t num;
+    int32_t type;            // of the values (DType)
+    int32_t format;
+    int32_t vec;             // values: base and rows 16-byte aligned
+    float tensor_scale;      // g
+    float six_g;             // RN(6 g)
+    const int32_t* offsets;  // rows sorted by expert: device int32[num_experts + 1], or null
+    int32_t num_experts;
+};
+
+struct MxNormParams {
+    const void *F, *R;
+    void* O;
+    uint8_t *Q, *S;
+    int64_t rows, cols, ldf, ldr, ldo, ldq;  // ldq in bytes
+    int32_t type, format;
+    int32_t vec;  // F, R, O: bases and rows 16-byte aligned
+    float eps, residual_scale, tensor_scale, six_g;
+    const void *post, *pre, *gate;
+    int32_t weight_type, gate_type;
+    int64_t gate_ld;
+    int32_t wvec, gvec;  // weights / gate 16-byte aligned
+};
+
+cudaError_t launch_mx_quantize(const MxQuantParams& p, cudaStream_t st);
+cudaError_t launch_mx_dequantize(const MxQuantParams& p, cudaStream_t st);
+cudaError_t launch_mx_norm(const MxNormParams& p, cudaStream_t st);
+
+}  // namespace qg
