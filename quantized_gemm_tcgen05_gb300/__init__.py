@@ -278,33 +278,36 @@ def gemm_mx_scale_size(format, rows, cols, num_experts=0) -> int:
     return n.value
 
 
+# The calls below hand their layouts and op structs over as they are (None for a
+# null pointer): ctypes takes a structure's address itself where the signature
+# wants a pointer to it, which costs the host less than one byref() each.
+
 def gemm_mx_quantize(h, format, tensor_scale, X, Xdesc, Q, Qdesc, S, S_size, expert_offsets_dev, num_experts, stream):
-    return lib().gemm_mx_quantize(h, format, tensor_scale, X, _lp(Xdesc), Q, _lp(Qdesc), S, S_size,
-                                  expert_offsets_dev, num_experts, stream)
+    return (_lib or lib()).gemm_mx_quantize(h, format, tensor_scale, X, Xdesc, Q, Qdesc, S, S_size,
+                                            expert_offsets_dev, num_experts, stream)
 
 
 def gemm_mx_dequantize(h, format, tensor_scale, Q, Qdesc, S, S_size, D, Ddesc, expert_offsets_dev, num_experts,
                        stream):
-    return lib().gemm_mx_dequantize(h, format, tensor_scale, Q, _lp(Qdesc), S, S_size, D, _lp(Ddesc),
-                                    expert_offsets_dev, num_experts, stream)
+    return (_lib or lib()).gemm_mx_dequantize(h, format, tensor_scale, Q, Qdesc, S, S_size, D, Ddesc,
+                                              expert_offsets_dev, num_experts, stream)
 
 
 def gemm_run_mx(h, op, format, alpha, A, Adesc, SA, SA_size, B, Bdesc, SB, SB_size, beta, C, Cdesc, D, Ddesc, stream):
     """Returns the status code (0 = OK).  Pointers are ints (device addresses)."""
-    return lib().gemm_run_mx(h, ctypes.byref(op), format, alpha, A, _lp(Adesc), SA, SA_size, B, _lp(Bdesc), SB,
-                             SB_size, beta, C, _lp(Cdesc), D, _lp(Ddesc), stream)
+    return (_lib or lib()).gemm_run_mx(h, op, format, alpha, A, Adesc, SA, SA_size, B, Bdesc, SB, SB_size, beta, C,
+                                       Cdesc, D, Ddesc, stream)
 
 
 def gemm_run_mx_grouped(h, op, format, alpha, expert_alpha, A, Adesc, SA, SA_size, B, Bdesc, SB, SB_size, beta, C,
                         Cdesc, D, Ddesc, expert_offsets_dev, num_experts, stream):
-    return lib().gemm_run_mx_grouped(h, ctypes.byref(op), format, alpha, expert_alpha, A, _lp(Adesc), SA, SA_size, B,
-                                     _lp(Bdesc), SB, SB_size, beta, C, _lp(Cdesc), D, _lp(Ddesc), expert_offsets_dev,
-                                     num_experts, stream)
+    return (_lib or lib()).gemm_run_mx_grouped(h, op, format, alpha, expert_alpha, A, Adesc, SA, SA_size, B, Bdesc, SB,
+                                               SB_size, beta, C, Cdesc, D, Ddesc, expert_offsets_dev, num_experts,
+                                               stream)
 
 
 def gemm_mx_norm_quantize(h, op, F, Fdesc, R, Rdesc, O, Odesc, Q, Qdesc, S, S_size, stream):
-    return lib().gemm_mx_norm_quantize(h, ctypes.byref(op), F, _lp(Fdesc), R, _lp(Rdesc), O, _lp(Odesc), Q, _lp(Qdesc),
-                                       S, S_size, stream)
+    return (_lib or lib()).gemm_mx_norm_quantize(h, op, F, Fdesc, R, Rdesc, O, Odesc, Q, Qdesc, S, S_size, stream)
 
 
 # ---- torch convenience (memory and streams only) ------------------------------------
@@ -388,8 +391,12 @@ class Workspace:
 
 
 def current_stream():
+    """The handle of torch's current stream on the current device."""
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None or not torch.cuda.is_initialized():
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    return ctypes.c_void_p(raw(torch.cuda.current_device()))  # without a Stream object: a third of the time
 
 
 def ptr(t):

@@ -98,6 +98,23 @@ __device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, const G
     }
 }
 
+// The same with cluster scope: for phases that the peer CTA completes.
+__device__ __forceinline__ bool wait_bar_cluster(uint64_t* bar, uint32_t parity, const Guard& g, uint32_t site) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (*g.abort) return false;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t n = 1;; ++n) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if ((n & 31u) == 0) {
+            if (*g.abort) return false;
+            if (globaltimer_ns() - t0 > g.limit_ns) {
+                record_timeout(g, site);
+                return false;
+            }
+        }
+    }
+}
+
 // Wait used when a role drains its own in-flight work before exit: bounded,
 // and it does not stop early on abort.
 __device__ __forceinline__ bool wait_bar_drain(uint64_t* bar, uint32_t parity, const Guard& g) {

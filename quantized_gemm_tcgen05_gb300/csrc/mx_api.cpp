@@ -5,7 +5,11 @@
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdio.h>
+#include <stdlib.h>
 #include <string.h>
+
+#include <algorithm>
+#include <atomic>
 
 #include "handle_internal.h"
 #include "mx_gemm.h"
@@ -237,14 +241,44 @@ int64_t tiles_along_m(const MxProduct& p, int bm) {
 }
 
 struct MxChoice {
-    int bn, splits;
+    int bn, splits, pair;
 };
 
-MxChoice choose(const MxProduct& p, int sm_count, int forced_split) {
-    MxChoice c{128, 1};
+// Clusters of two that the CTA-pair kernel keeps resident (asked once per device).
+int pair_clusters(gemm_handle_t h, int32_t format) {
+    static std::atomic<int> known[64][2];
+    std::atomic<int>& k = known[handle_device(h) & 63][format == GEMM_NVFP4];
+    int n = k.load();
+    if (n == 0) {
+        n = std::max(0, std::min(mx_pair_max_clusters(format), handle_sm_count(h) / 2)) + 1;
+        k.store(n);
+    }
+    return n - 1;
+}
+
+// GEMM_FORCE_KERNEL=mx_bn64 / mx_bn128 / mx2_bn256 (the names gemm_last_choice
+// prints, up to the slash) pins the kernel, for tests and sweeps.
+bool forced_kernel(MxChoice* c) {
+    const char* f = getenv("GEMM_FORCE_KERNEL");
+    if (!f || strncmp(f, "mx", 2)) return false;
+    c->pair = strncmp(f, "mx2_bn256", 9) == 0;
+    c->bn = c->pair ? 256 : strncmp(f, "mx_bn64", 7) == 0 ? 64 : 128;
+    return true;
+}
+
+MxChoice choose(const MxProduct& p, int sm_count, int clusters, int forced_split) {
+    MxChoice c{128, 1, 0};
+    const bool forced = forced_kernel(&c);
+    if (!forced && !forced_split && p.M > 128 && clusters > 0 &&
+        tiles_along_m(p, 256) * ceil_div(p.N, 256) * 2 >= clusters)
+        c.pair = 1;
+    if (c.pair) {
+        c.bn = 256;
+        return c;
+    }
     const int64_t steps = ceil_div(p.K, MX_KSTEP);
     const int64_t slots = 2 * (int64_t)sm_count;  // CTAs resident at once
-    if (tiles_along_m(p, 128) * ceil_div(p.N, 128) * 8 <= slots || p.N <= 64) c.bn = 64;
+    if (!forced && (tiles_along_m(p, 128) * ceil_div(p.N, 128) * 8 <= slots || p.N <= 64)) c.bn = 64;
     const int64_t tiles = tiles_along_m(p, 128) * ceil_div(p.N, c.bn);
     const int want = forced_split ? forced_split : 8;
     while (c.splits * 2 <= want && c.splits * 2 <= steps && (forced_split || tiles * c.splits * 2 <= slots)) c.splits *= 2;
@@ -260,24 +294,26 @@ int run_product(gemm_handle_t h, const gemm_op_t* op, MxProduct& p, cudaStream_t
         handle_set_choice(h, "scale_c", p.M, p.N, p.K);
         return status_of(launch_scale_c(p.epi, 1, st));
     }
-    const MxChoice c = choose(p, handle_sm_count(h), op->splitk);
+    const int clusters = pair_clusters(h, p.format);
+    const MxChoice c = choose(p, handle_sm_count(h), clusters, op->splitk);
+    if (c.pair && clusters < 1) return GEMM_ERR_NO_KERNEL;
     MxGemmParams k;
     memset(&k, 0, sizeof k);
     k.epi = p.epi;
     k.expert_alpha = p.expert_alpha;
     k.offsets = p.offsets;
     k.num_experts = p.experts;
-    const int64_t tm = tiles_along_m(p, 128), tn = ceil_div(p.N, c.bn);
+    const int64_t tm = tiles_along_m(p, c.pair ? 256 : 128), tn = ceil_div(p.N, c.bn);
     if (tm * tn * c.splits > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
     k.tiles_m = (int32_t)tm;
     k.tiles_n = (int32_t)tn;
     k.k_steps = (int32_t)ceil_div(p.K, MX_KSTEP);
     k.k_atoms = (int32_t)ceil_div(p.K, 64);
     k.splits = c.splits;
-    k.a_rows = (int32_t)(p.M < 128 ? ceil_div(p.M, 8) * 8 : 128);
-    k.stages = mx_gemm_stages(c.bn, p.format, k.a_rows);
+    k.a_rows = (int32_t)(p.M < 128 && !c.pair ? ceil_div(p.M, 8) * 8 : 128);
+    k.stages = c.pair ? 0 : mx_gemm_stages(c.bn, p.format, k.a_rows);
     k.b3d = p.experts > 1;
-    k.idesc = make_idesc_mx(p.format == GEMM_NVFP4, 128, c.bn);
+    k.idesc = make_idesc_mx(p.format == GEMM_NVFP4, c.pair ? 256 : 128, c.bn);
     const int64_t ds = float_size(p.epi.d_type);
     k.vec32 = aligned(p.epi.D, 32) && p.epi.ldd * ds % 32 == 0 &&
               (!p.epi.C || (aligned(p.epi.C, 32) && p.epi.ldc * ds % 32 == 0));
@@ -288,13 +324,20 @@ int run_product(gemm_handle_t h, const gemm_op_t* op, MxProduct& p, cudaStream_t
     const int32_t nb = p.experts > 1 ? p.experts : 1;
     const int64_t a_atom_rows = p.experts ? p.M / MX_ATOM_ROWS + p.experts : ceil_div(p.M, MX_ATOM_ROWS);
     int rc = map_codes(h, &m.a, p.A, p.K, p.M, p.lda, 1, 0, k.a_rows);
-    if (rc == GEMM_OK) rc = map_codes(h, &m.b, p.B, p.K, p.N, p.ldb, nb, p.b_bs, c.bn);
+    if (rc == GEMM_OK) rc = map_codes(h, &m.b, p.B, p.K, p.N, p.ldb, nb, p.b_bs, c.pair ? 128 : c.bn);
     if (rc == GEMM_OK) rc = map_scales(h, &m.sa, p.SA, p.format, p.K, a_atom_rows, 1, 1);
-    if (rc == GEMM_OK) rc = map_scales(h, &m.sb, p.SB, p.format, p.K, ceil_div(p.N, MX_ATOM_ROWS), nb, 1);
+    if (rc == GEMM_OK) rc = map_scales(h, &m.sb, p.SB, p.format, p.K, ceil_div(p.N, MX_ATOM_ROWS), nb, c.pair ? 2 : 1);
     if (rc != GEMM_OK) return rc;
     char name[64];
-    snprintf(name, sizeof name, "mx%s_bn%d/%s%d", p.experts ? "_grouped" : "", c.bn, "splitk", c.splits);
+    if (c.pair || c.splits == 1)
+        snprintf(name, sizeof name, "mx%s%s_bn%d/dp", c.pair ? "2" : "", p.experts ? "_grouped" : "", c.bn);
+    else
+        snprintf(name, sizeof name, "mx%s_bn%d/splitk%d", p.experts ? "_grouped" : "", c.bn, c.splits);
     handle_set_choice(h, name, p.M, p.N, p.K);
+    if (c.pair) {
+        k.programs = (int32_t)std::min<int64_t>(clusters, tm * tn);
+        return status_of(launch_mx_pair(p.format, m, k, k.programs, st));
+    }
     return status_of(launch_mx_gemm(c.bn, p.format, m, k, (int)(tm * tn * c.splits), st));
 }
 

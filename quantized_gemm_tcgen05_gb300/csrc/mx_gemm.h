@@ -40,4 +40,10 @@ cudaError_t launch_mx_gemm(int bn, int format, const MxMaps& m, const MxGemmPara
 // Stages of the ring for a tile of a_rows x bn.
 int mx_gemm_stages(int bn, int format, int a_rows);
 
+
+// The CTA-pair kernel: 256 x 256 tiles, persistent clusters of two.
+cudaError_t launch_mx_pair(int format, const MxMaps& m, const MxGemmParams& p, int clusters, cudaStream_t st);
+// Clusters that can be resident at once.
+int mx_pair_max_clusters(int format);
+
 }  // namespace qg

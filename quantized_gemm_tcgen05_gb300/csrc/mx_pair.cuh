@@ -1,0 +1,321 @@
+// Product of two 4-bit microscaled operands on CTA pairs: persistent clusters
+// of two, one 256 x 256 tile at a time (tcgen05.mma.cta_group::2).
+//
+// Per 256-wide K-step an SM takes in its 128 rows of A, its half of the 256 rows
+// of B, the scale atom of its A rows and both atoms of B (a pair's MMA wants all
+// of B's scales in both CTAs' TMEM): 38 KB for 128 x 256 x 256 products, the
+// least per product that the accumulator's size allows.  That ingest, about 57
+// bytes a clock and SM, is what bounds large products; the tensor core alone
+// would need 512 clocks a step.
+//
+// TMEM: 256 accumulator columns and as many scale buffers as the ring has
+// stages, so a buffer is free whenever its stage is (the stage was refilled
+// after the MMAs that read both had completed).
+//
+//   warp 0     TMA producer (both CTAs; all bytes complete on the leader's full[s])
+//   warp 1     leader: scale copies and MMAs
+//   warps 2-9  epilogue: a warp takes 32 rows x 128 columns into registers, gives
+//              the accumulator back, then stores; so the next tile's main loop
+//              waits for eight warps' TMEM loads only, not for their stores.
+//
+// Grouped problems: 256-row blocks of one expert's rows; the blocks that exist
+// are counted on the device and shared out, so none is assigned in vain.
+#pragma once
+#include <atomic>
+
+#include "mx_epilogue.cuh"
+
+namespace qg {
+
+template <bool NVF4>
+struct MxPairCfg {
+    static constexpr int BN = 256;
+    static constexpr uint32_t A_BYTES = 128 * 128, B_BYTES = 128 * 128;
+    static constexpr uint32_t SA_BYTES = NVF4 ? 2048 : 1024, SB_BYTES = 2 * SA_BYTES;
+    static constexpr int S_ATOMS = NVF4 ? 4 : 2;
+    static constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES + SA_BYTES + SB_BYTES;
+    static constexpr int STAGES = 5;
+    static constexpr uint32_t SCALE_COLS = 12 * S_ATOMS;  // A 4, B 8 a K-atom
+    static_assert(STAGE_BYTES % 1024 == 0 && BN + STAGES * SCALE_COLS <= 512, "");
+    static constexpr uint32_t EPI_BYTES = 8 * 32 * 33 * 4;
+    static constexpr uint32_t AUX_BYTES = (2 * STAGES + 3) * 8 + 16;
+    static constexpr uint32_t SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + AUX_BYTES;
+    static_assert(SMEM_BYTES <= 232448, "");
+};
+
+struct MxTile {
+    int64_t n0, row0, atom_row;
+    int expert, rows;  // rows of the 256 that exist
+};
+
+// Blocks of bm rows that rows sorted by expert make (every lane gets it).
+__device__ __forceinline__ int64_t mx_expert_blocks(const int32_t* off, int32_t E, int bm, int lane) {
+    int n = 0;
+    for (int32_t e = lane; e < E; e += 32) {
+        const int64_t m = (int64_t)off[e + 1] - off[e];
+        n += m > 0 ? (int)((m + bm - 1) / bm) : 0;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
+    return n;
+}
+
+// Tile t of the launch (warp-wide): M blocks vary fastest.  False past the end.
+__device__ __forceinline__ bool mx_pair_tile(const MxGemmParams& P, int64_t blocks, int64_t t, int lane, MxTile& o) {
+    if (t >= blocks * P.tiles_n) return false;
+    const int64_t b = t % blocks;
+    o.n0 = t / blocks * 256;
+    o.expert = 0;
+    if (P.offsets) return mx_expert_block(P.offsets, P.num_experts, 256, b, lane, &o.expert, &o.row0, &o.rows, &o.atom_row);
+    o.row0 = b * 256;
+    o.rows = (int)(P.epi.M - o.row0 < 256 ? P.epi.M - o.row0 : 256);
+    o.atom_row = 2 * b;
+    return true;
+}
+
+template <bool NVF4>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
+    mx_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                   const __grid_constant__ MxGemmParams P) {
+    using Cfg = MxPairCfg<NVF4>;
+    constexpr int S = Cfg::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    float* stage_all = reinterpret_cast<float*>(smem + S * Cfg::STAGE_BYTES);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * Cfg::STAGE_BYTES + Cfg::EPI_BYTES);
+    uint64_t* empty = full + S;
+    uint64_t* tfull = empty + S;
+    uint64_t* tempty = tfull + 1;  // leader: 16 epilogue warps of the pair
+    uint64_t* done = tempty + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(tfull, 1);
+        mbar_init(tempty, 16);
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmSA);
+        tma_prefetch_desc(&tmSB);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrive
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    griddep_launch_dependents();
+    griddep_wait();
+    const Guard g{P.status, P.timeout_ns, abort_flag};
+    const int64_t pid = blockIdx.x >> 1;
+    const int64_t blocks = P.offsets ? mx_expert_blocks(P.offsets, P.num_experts, 256, lane) : P.tiles_m;
+
+    if (warp == 0) {
+        // ---------------- TMA producer (both CTAs) ----------------
+        int s = 0;
+        uint32_t ph = 0, armed = 0, armed_par = 0;
+        bool ok = true;
+        MxTile t;
+        for (int64_t i = pid; ok && mx_pair_tile(P, blocks, i, lane, t); i += P.programs) {
+            if (lane == 0) {
+                const int32_t a0 = (int32_t)(t.row0 + 128 * rank), b0 = (int32_t)(t.n0 + 128 * rank);
+                const int32_t sa0 = (int32_t)(t.atom_row + rank), sb0 = (int32_t)(t.n0 / 128);
+                for (int k = 0; k < P.k_steps; ++k) {
+                    if (!wait_bar_cluster(&empty[s], ph ^ 1, g, SITE_PRODUCER_EMPTY)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* a = smem + s * Cfg::STAGE_BYTES;
+                    uint8_t* b = a + Cfg::A_BYTES;
+                    uint8_t* sa = b + Cfg::B_BYTES;
+                    uint8_t* sb = sa + Cfg::SA_BYTES;
+                    const int32_t kx = k * 128, sx = k * (int32_t)(Cfg::SA_BYTES / 8);
+                    const uint32_t bar = leader ? smem_u32(&full[s]) : mapa_shared(smem_u32(&full[s]), 0);
+                    if (leader) {
+                        mbar_arrive_expect_tx(&full[s], 2 * Cfg::STAGE_BYTES);
+                        armed |= 1u << s;
+                        armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                    }
+                    tma_load_2d_pair(a, &tmA, bar, kx, a0);
+                    tma_load_2d_pair(sa, &tmSA, bar, sx, sa0);
+                    if (P.b3d) {
+                        tma_load_3d_pair(b, &tmB, bar, kx, b0, t.expert);
+                        tma_load_3d_pair(sb, &tmSB, bar, sx, sb0, t.expert);
+                    } else {
+                        tma_load_2d_pair(b, &tmB, bar, kx, b0);
+                        tma_load_2d_pair(sb, &tmSB, bar, sx, sb0);
+                    }
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+        }
+        if (lane == 0) {
+            // never leave with copies in flight into this CTA's shared memory
+            if (leader) {
+                for (int i = 0; i < S; ++i)
+                    if (armed & (1u << i)) wait_bar_drain(&full[i], (armed_par >> i) & 1u, g);
+            } else if (!ok) {
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 200000ull) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1 && leader) {
+        // ---------------- scale copies and MMAs (even CTA) ----------------
+        int s = 0;
+        uint32_t ph = 0, it = 0;
+        bool ok = true, issued = false;
+        MxTile t;
+        for (int64_t i = pid; ok && mx_pair_tile(P, blocks, i, lane, t); i += P.programs, ++it) {
+            if (lane == 0) {
+                // the accumulator's previous tile is in the epilogue's registers
+                ok = wait_bar_cluster(tempty, (it & 1) ^ 1, g, SITE_MMA_TMEM_EMPTY);
+                tc_fence_after_sync();
+                for (int k = 0; ok && k < P.k_steps; ++k) {
+                    if (!wait_bar_cluster(&full[s], ph, g, SITE_MMA_FULL)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t a = smem_u32(smem + s * Cfg::STAGE_BYTES);
+                    const uint32_t b = a + Cfg::A_BYTES, sa = b + Cfg::B_BYTES, sb = sa + Cfg::SA_BYTES;
+                    const uint32_t ta = tmem + Cfg::BN + s * Cfg::SCALE_COLS, tb = ta + 4 * Cfg::S_ATOMS;
+                    const int na = P.k_atoms - 4 * k < 4 ? P.k_atoms - 4 * k : 4;
+                    const uint64_t ad = make_sw128_kmajor_desc(a), bd = make_sw128_kmajor_desc(b);
+#pragma unroll
+                    for (int q = 0; q < Cfg::S_ATOMS; ++q) {
+                        tmem_cp_scales_pair(ta + 4 * q, make_scale_desc(sa + MX_ATOM_BYTES * q));
+                        tmem_cp_scales_pair(tb + 8 * q, make_scale_desc(sb + MX_ATOM_BYTES * q));
+                        tmem_cp_scales_pair(tb + 8 * q + 4, make_scale_desc(sb + Cfg::SA_BYTES + MX_ATOM_BYTES * q));
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        if (q >= na) break;
+                        const uint32_t acc = (k > 0 || q > 0) ? 1u : 0u;
+                        if constexpr (NVF4) {
+                            umma_mx_ss_pair<true>(tmem, ad + 2 * q, bd + 2 * q, P.idesc, ta + 4 * q, tb + 8 * q, acc);
+                        } else {
+                            const uint32_t id = (q & 1) * 2u;
+                            umma_mx_ss_pair<false>(tmem, ad + 2 * q, bd + 2 * q, P.idesc | (id << 29) | (id << 4),
+                                                   ta + 4 * (q / 2), tb + 8 * (q / 2), acc);
+                        }
+                    }
+                    issued = true;
+                    umma_commit_pair_mc(&empty[s], 0x3);
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+                if (ok) umma_commit_pair_mc(tfull, 0x3);
+            }
+            ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
+        }
+        if (lane == 0 && issued) {  // every issued MMA has finished before TMEM is freed
+            umma_commit_pair_mc(done, 0x1);
+            wait_bar_drain(done, 0, g);
+        }
+        __syncwarp();
+    } else if (warp >= 2) {
+        // ---------------- epilogue ----------------
+        const int ew = warp % 4, half = (warp - 2) / 4;
+        float* stage = stage_all + (warp - 2) * (32 * 33);
+        const uint32_t l_tempty = mapa_shared(smem_u32(tempty), 0);
+        uint32_t it = 0;
+        MxTile t;
+        for (int64_t i = pid; mx_pair_tile(P, blocks, i, lane, t); i += P.programs, ++it) {
+            float alpha = P.epi.alpha;
+            if (P.expert_alpha) alpha *= P.expert_alpha[t.expert];
+            int rows = t.rows - 128 * (int)rank - 32 * ew;
+            rows = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
+            const int64_t m0 = t.row0 + 128 * rank + 32 * ew, n0 = t.n0 + 128 * half;
+            if (!__all_sync(0xFFFFFFFFu, wait_bar_cluster(tfull, it & 1, g, SITE_EPI_TMEM_FULL))) break;
+            tc_fence_after_sync();
+            const uint32_t ta = tmem + 128 * half + ((uint32_t)(ew * 32) << 16);
+            float v[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_load_chunk<32>(ta + 32 * c, v[c]);
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(l_tempty);
+            if (rows > 0) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (n0 + 32 * c < P.epi.N)
+                        mx_store_block(P.epi, P.vec32, alpha, m0, rows, n0 + 32 * c, v[c], stage, lane);
+            }
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // the leader's MMAs and all cross-CTA arrivals are done
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+template <bool NVF4>
+cudaError_t mx_pair_configure() {
+    static std::atomic<uint64_t> configured{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(configured.load() & bit)) {
+        e = cudaFuncSetAttribute(mx_pair_kernel<NVF4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)MxPairCfg<NVF4>::SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit);
+    }
+    return cudaSuccess;
+}
+
+template <bool NVF4>
+cudaError_t launch_mx_pair_t(const MxMaps& m, const MxGemmParams& p, int clusters, cudaStream_t st) {
+    const cudaError_t e = mx_pair_configure<NVF4>();
+    if (e != cudaSuccess) return e;
+    return launch_pdl(mx_pair_kernel<NVF4>, 2 * clusters, 320, MxPairCfg<NVF4>::SMEM_BYTES, st, m.a, m.b, m.sa, m.sb, p);
+}
+
+template <bool NVF4>
+int mx_pair_clusters_t() {
+    if (mx_pair_configure<NVF4>() != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(320, 1, 1);
+    cfg.dynamicSmemBytes = MxPairCfg<NVF4>::SMEM_BYTES;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel<NVF4>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
+}  // namespace qg

@@ -53,22 +53,6 @@ struct PairCfg {
     }
 };
 
-__device__ __forceinline__ bool wait_bar_cluster(uint64_t* bar, uint32_t parity, const Guard& g, uint32_t site) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if (*g.abort) return false;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t n = 1;; ++n) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if ((n & 31u) == 0) {
-            if (*g.abort) return false;
-            if (globaltimer_ns() - t0 > g.limit_ns) {
-                record_timeout(g, site);
-                return false;
-            }
-        }
-    }
-}
-
 template <int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(192, 1)
     umma_pair_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmY,

@@ -26,6 +26,14 @@ def h():
     qg.gemm_destroy(h)
 
 
+@pytest.fixture(params=["", "mx_bn64", "mx_bn128", "mx2_bn256"])
+def kernel(request, monkeypatch):
+    """The automatic choice, then each kernel pinned."""
+    if request.param:
+        monkeypatch.setenv("GEMM_FORCE_KERNEL", request.param)
+    return request.param
+
+
 def dev(a):
     return torch.from_numpy(np.ascontiguousarray(a)).cuda()
 
@@ -71,10 +79,12 @@ def check(got, ref, bound, d, what=""):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-@pytest.mark.parametrize("splits", [1, 2])
-def test_one_hot_placement(h, fmt, splits):
+@pytest.mark.parametrize("splits", [0, 1, 2])
+def test_one_hot_placement(h, monkeypatch, fmt, splits):
     # A has one code per row (1.0, scale 1) at k = 37 i % K: D[i][j] is exactly
     # B's value there, so a misplaced code, scale row or scale column shows
+    if splits == 0:
+        monkeypatch.setenv("GEMM_FORCE_KERNEL", "mx2_bn256")
     m, n, k = 256, 320, 1088
     rng = np.random.default_rng(5)
     code = np.zeros((m, k), np.uint8)
@@ -93,13 +103,13 @@ def test_one_hot_placement(h, fmt, splits):
 
 SHAPES = [(1, 1, 1), (1, 4096, 512), (3, 130, 95), (17, 64, 256), (64, 1000, 4096), (127, 129, 33), (128, 128, 257),
           (129, 257, 700), (200, 328, 1031), (300, 1002, 2080), (520, 700, 31), (1, 8, 14336), (256, 512, 64),
-          (640, 1280, 768), (1000, 2056, 1280)]
+          (640, 1280, 768), (1000, 2056, 1280), (257, 300, 1600)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("d", OUTS)
 @pytest.mark.parametrize("shape", SHAPES)
-def test_shapes(h, fmt, d, shape):
+def test_shapes(h, kernel, fmt, d, shape):
     m, n, k = shape
     rng = np.random.default_rng(m * 7 + n * 3 + k)
     a, b = Operand(rng, m, k, fmt), Operand(rng, n, k, fmt)
@@ -128,8 +138,11 @@ def test_k_slices(h, fmt, splits, shape):
 
 @pytest.mark.parametrize("d", OUTS)
 @pytest.mark.parametrize("act", ["", "bias", "relu", "gelu"])
-@pytest.mark.parametrize("shape,splits", [((70, 264, 600), 1), ((70, 264, 600), 2), ((300, 517, 512), 1), ((600, 1100, 512), 1)])
-def test_epilogue(h, d, act, shape, splits):
+@pytest.mark.parametrize("shape,splits,pin", [((70, 264, 600), 1, ""), ((70, 264, 600), 2, ""), ((300, 517, 512), 1, ""),
+                                              ((600, 1100, 512), 1, "mx2_bn256"), ((260, 520, 300), 0, "mx2_bn256")])
+def test_epilogue(h, monkeypatch, d, act, shape, splits, pin):
+    if pin:
+        monkeypatch.setenv("GEMM_FORCE_KERNEL", pin)
     fmt = qg.GEMM_NVFP4
     m, n, k = shape
     rng = np.random.default_rng(11)
@@ -160,7 +173,7 @@ def test_epilogue(h, d, act, shape, splits):
 
 @pytest.mark.parametrize("d", OUTS)
 @pytest.mark.parametrize("ldd", [200, 208, 217, 256])
-def test_strides_and_nothing_else_written(h, d, ldd):
+def test_strides_and_nothing_else_written(h, kernel, d, ldd):
     fmt = qg.GEMM_MXFP4
     m, n, k = 150, 199, 320
     rng = np.random.default_rng(ldd)
@@ -173,7 +186,7 @@ def test_strides_and_nothing_else_written(h, d, ldd):
     assert bool((buf[0] == 7).all()) and bool((buf[-1] == 7).all()) and bool((buf[:, n:] == 7).all())
 
 
-def test_element_aligned_output(h):
+def test_element_aligned_output(h, kernel):
     # D starts one element into its buffer: no vector access may be used
     fmt, m, n, k = qg.GEMM_NVFP4, 66, 128, 128
     rng = np.random.default_rng(1)
@@ -186,7 +199,7 @@ def test_element_aligned_output(h):
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
-def test_nan_scale_reaches_its_row_and_column_only(h, fmt):
+def test_nan_scale_reaches_its_row_and_column_only(h, kernel, fmt):
     m, n, k = 40, 140, 512
     rng = np.random.default_rng(3)
     a, b = Operand(rng, m, k, fmt), Operand(rng, n, k, fmt)
@@ -214,6 +227,18 @@ def test_no_k(h, beta, act):
     assert rc == 0
     want = beta * c
     assert torch.equal(out, torch.relu(want) if act else want)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_many_tiles_per_program(h, fmt):
+    # every cluster of the CTA-pair kernel runs several tiles, ragged ones last
+    m, n, k = 2600, 5000, 320
+    rng = np.random.default_rng(21)
+    a, b = Operand(rng, m, k, fmt), Operand(rng, n, k, fmt)
+    got = product(h, a, b, fmt, synth.BF16, alpha=0.5)
+    assert qg.gemm_last_choice(h).startswith("mx2_")
+    check(got, 0.5 * a.values @ b.values.T, 0.5 * np.abs(a.values) @ np.abs(b.values).T, synth.BF16)
+    assert torch.equal(got, product(h, a, b, fmt, synth.BF16, alpha=0.5))
 
 
 # ---- grouped -----------------------------------------------------------------
@@ -260,12 +285,12 @@ COUNTS = [[1], [5, 0, 3], [0, 0, 0, 130], [128, 128, 1], [127, 129, 0, 256, 2], 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("counts", COUNTS, ids=[str(i) for i in range(len(COUNTS))])
 @pytest.mark.parametrize("n,k", [(192, 512), (137, 97)])
-def test_grouped(h, fmt, counts, n, k):
+def test_grouped(h, kernel, fmt, counts, n, k):
     grouped(h, counts, n, k, fmt, synth.BF16, seed=len(counts) + n, alpha=0.125)
 
 
 @pytest.mark.parametrize("d", OUTS)
-def test_grouped_types_c_and_rows_past_the_experts(h, d):
+def test_grouped_types_c_and_rows_past_the_experts(h, kernel, d):
     grouped(h, [200, 0, 57, 300], 300, 640, qg.GEMM_NVFP4, d, seed=4, alpha=2.0 ** -8, beta=0.5)
     grouped(h, [20, 0, 57], 128, 1500, qg.GEMM_MXFP4, d, seed=5, alpha=2.0 ** -8, with_expert_alpha=False, extra=9)
 
@@ -275,7 +300,7 @@ def test_grouped_k_slices(h, splits):
     grouped(h, [3, 150, 0, 20], 256, 2048, qg.GEMM_NVFP4, synth.F32, seed=6, op=qg.gemm_op_t(splitk=splits))
 
 
-def test_grouped_no_rows_at_all(h):
+def test_grouped_no_rows_at_all(h, kernel):
     grouped(h, [0, 0], 64, 64, qg.GEMM_NVFP4, synth.BF16, seed=7, extra=4)
 
 
