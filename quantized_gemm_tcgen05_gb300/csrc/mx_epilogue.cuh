@@ -19,6 +19,60 @@ __device__ __forceinline__ void st32(void* p, const uint32_t (&w)[8]) {
                  : "memory");
 }
 
+// 64 accumulator columns (TMEM address ta, this warp's 32 rows, a row per lane)
+// as finished 16-bit values: w[j] holds columns 2 j and 2 j + 1.
+template <int ACT, int DT>
+__device__ __forceinline__ void mx_pack64(const EpiParams& e, float alpha, uint32_t ta, int64_t n0, uint32_t (&w)[32],
+                                          int lane) {
+    EpiArith ar = epi_arith(e);
+    ar.alpha = alpha;
+    ar.beta = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        float v[32];
+        tmem_load_chunk<32>(ta + 32 * c, v);
+        const float bl = ACT >= 0 ? bias_at(ar, n0 + 32 * c + lane) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            float b0 = 0.0f, b1 = 0.0f;
+            if constexpr (ACT >= 0) {
+                b0 = __shfl_sync(0xFFFFFFFFu, bl, 2 * j);
+                b1 = __shfl_sync(0xFFFFFFFFu, bl, 2 * j + 1);
+            }
+            const float x0 = epi_value<ACT>(ar, v[2 * j], 0.0f, b0), x1 = epi_value<ACT>(ar, v[2 * j + 1], 0.0f, b1);
+            if constexpr (DT == DT_BF16) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
+                w[16 * c + j] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                const __half2 h = __floats2half2_rn(x0, x1);
+                w[16 * c + j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+    }
+}
+
+// The 64 packed columns through `stage` (32 rows of 128 bytes, 16-byte chunks
+// XOR-permuted by the row): in, a row per lane; out, four lanes to a row, so
+// every global request is a whole 128-byte line.  Storing the rows a lane each
+// instead sends four times the requests, which cost 4096x14336x4096 19 us of
+// 110.  d: row 0's first column; ld in elements; rows: rows that exist.
+__device__ __forceinline__ void mx_stage64(uint8_t* stage, const uint32_t (&w)[32], int lane) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) =
+            make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+}
+__device__ __forceinline__ void mx_store64(const uint8_t* stage, uint16_t* d, int64_t ld, int rows, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + lane / 4, part = lane % 4;
+        const uint4 a = *reinterpret_cast<const uint4*>(stage + r * 128 + (((2 * part) ^ (r & 7)) << 4));
+        const uint4 b = *reinterpret_cast<const uint4*>(stage + r * 128 + (((2 * part + 1) ^ (r & 7)) << 4));
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if (r < rows) st32(d + r * ld + 16 * part, w);
+    }
+}
+
 // Columns n0 .. n0+31 of row m (valid for this lane when `row_ok`), values v
 // before alpha.  Every lane of the warp takes part.  Vector form: every lane
 // moves its own row's 64 or 128 bytes in 32-byte pieces, whole sectors each, so

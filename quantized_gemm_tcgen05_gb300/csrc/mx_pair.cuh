@@ -9,14 +9,18 @@
 // would need 512 clocks a step.
 //
 // TMEM: 256 accumulator columns and as many scale buffers as the ring has
-// stages, so a buffer is free whenever its stage is (the stage was refilled
-// after the MMAs that read both had completed).
+// stages.  Scales go from shared memory to TMEM through the registers of four
+// warps, one per 32-lane quarter (every quarter holds all scales).  Copies by the
+// tensor core's own queue (tcgen05.cp) are simpler but stand in line with the
+// MMAs: twelve a K-step took 4096^3 from 38 to 58 us.
 //
-//   warp 0     TMA producer (both CTAs; all bytes complete on the leader's full[s])
-//   warp 1     leader: scale copies and MMAs
-//   warps 2-9  epilogue: a warp takes 32 rows x 128 columns into registers, gives
-//              the accumulator back, then stores; so the next tile's main loop
-//              waits for eight warps' TMEM loads only, not for their stores.
+//   warp 0      TMA producer (both CTAs; the operands' bytes complete on the
+//               leader's full[s], each CTA's scales on its own sfull[s])
+//   warp 1      leader: MMAs
+//   warps 2-9   epilogue: a warp takes 32 rows x 128 columns into registers, gives
+//               the accumulator back, then stores; so the next tile's main loop
+//               waits for eight warps' TMEM loads only, not for their stores
+//   warps 10-13 scales: shared memory -> TMEM, then arrive on the leader's sready[s]
 //
 // Grouped problems: 256-row blocks of one expert's rows; the blocks that exist
 // are counted on the device and shared out, so none is assigned in vain.
@@ -26,6 +30,8 @@
 #include "mx_epilogue.cuh"
 
 namespace qg {
+
+constexpr int MX_PAIR_THREADS = 448;
 
 template <bool NVF4>
 struct MxPairCfg {
@@ -37,8 +43,8 @@ struct MxPairCfg {
     static constexpr int STAGES = 5;
     static constexpr uint32_t SCALE_COLS = 12 * S_ATOMS;  // A 4, B 8 a K-atom
     static_assert(STAGE_BYTES % 1024 == 0 && BN + STAGES * SCALE_COLS <= 512, "");
-    static constexpr uint32_t EPI_BYTES = 8 * 32 * 33 * 4;
-    static constexpr uint32_t AUX_BYTES = (2 * STAGES + 3) * 8 + 16;
+    static constexpr uint32_t EPI_BYTES = 8 * (32 * 33 + 12) * 4;
+    static constexpr uint32_t AUX_BYTES = (4 * STAGES + 3) * 8 + 16;
     static constexpr uint32_t SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + EPI_BYTES + AUX_BYTES;
     static_assert(SMEM_BYTES <= 232448, "");
 };
@@ -74,7 +80,7 @@ __device__ __forceinline__ bool mx_pair_tile(const MxGemmParams& P, int64_t bloc
 }
 
 template <bool NVF4>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_PAIR_THREADS, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                    const __grid_constant__ MxGemmParams P) {
@@ -85,7 +91,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
     float* stage_all = reinterpret_cast<float*>(smem + S * Cfg::STAGE_BYTES);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + S * Cfg::STAGE_BYTES + Cfg::EPI_BYTES);
     uint64_t* empty = full + S;
-    uint64_t* tfull = empty + S;
+    uint64_t* sfull = empty + S;    // this CTA's scales are in shared memory
+    uint64_t* sready = sfull + S;   // leader: both CTAs' scales are in TMEM (8 warps)
+    uint64_t* tfull = sready + S;
     uint64_t* tempty = tfull + 1;  // leader: 16 epilogue warps of the pair
     uint64_t* done = tempty + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -98,6 +106,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+            mbar_init(&sfull[s], 1);
+            mbar_init(&sready[s], 8);
         }
         mbar_init(tfull, 1);
         mbar_init(tempty, 16);
@@ -137,7 +147,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
                 const int32_t a0 = (int32_t)(t.row0 + 128 * rank), b0 = (int32_t)(t.n0 + 128 * rank);
                 const int32_t sa0 = (int32_t)(t.atom_row + rank), sb0 = (int32_t)(t.n0 / 128);
                 for (int k = 0; k < P.k_steps; ++k) {
-                    if (!wait_bar_cluster(&empty[s], ph ^ 1, g, SITE_PRODUCER_EMPTY)) {
+                    if (!wait_bar(&empty[s], ph ^ 1, g, SITE_PRODUCER_EMPTY)) {
                         ok = false;
                         break;
                     }
@@ -147,20 +157,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
                     uint8_t* sb = sa + Cfg::SA_BYTES;
                     const int32_t kx = k * 128, sx = k * (int32_t)(Cfg::SA_BYTES / 8);
                     const uint32_t bar = leader ? smem_u32(&full[s]) : mapa_shared(smem_u32(&full[s]), 0);
-                    if (leader) {
-                        mbar_arrive_expect_tx(&full[s], 2 * Cfg::STAGE_BYTES);
-                        armed |= 1u << s;
-                        armed_par = (armed_par & ~(1u << s)) | (ph << s);
-                    }
+                    if (leader) mbar_arrive_expect_tx(&full[s], 2 * (Cfg::A_BYTES + Cfg::B_BYTES));
+                    mbar_arrive_expect_tx(&sfull[s], Cfg::SA_BYTES + Cfg::SB_BYTES);
+                    armed |= 1u << s;
+                    armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                    tma_load_2d(sa, &tmSA, &sfull[s], sx, sa0);
+                    if (P.b3d)
+                        tma_load_3d(sb, &tmSB, &sfull[s], sx, sb0, t.expert);
+                    else
+                        tma_load_2d(sb, &tmSB, &sfull[s], sx, sb0);
                     tma_load_2d_pair(a, &tmA, bar, kx, a0);
-                    tma_load_2d_pair(sa, &tmSA, bar, sx, sa0);
-                    if (P.b3d) {
+                    if (P.b3d)
                         tma_load_3d_pair(b, &tmB, bar, kx, b0, t.expert);
-                        tma_load_3d_pair(sb, &tmSB, bar, sx, sb0, t.expert);
-                    } else {
+                    else
                         tma_load_2d_pair(b, &tmB, bar, kx, b0);
-                        tma_load_2d_pair(sb, &tmSB, bar, sx, sb0);
-                    }
                     if (++s == S) {
                         s = 0;
                         ph ^= 1;
@@ -171,10 +181,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
         }
         if (lane == 0) {
             // never leave with copies in flight into this CTA's shared memory
-            if (leader) {
-                for (int i = 0; i < S; ++i)
-                    if (armed & (1u << i)) wait_bar_drain(&full[i], (armed_par >> i) & 1u, g);
-            } else if (!ok) {
+            for (int i = 0; i < S; ++i)
+                if (armed & (1u << i)) {
+                    wait_bar_drain(&sfull[i], (armed_par >> i) & 1u, g);
+                    if (leader) wait_bar_drain(&full[i], (armed_par >> i) & 1u, g);
+                }
+            if (!leader && !ok) {
+                // the odd CTA cannot see its operand copies complete (they land on
+                // the leader's barriers); after an abort give them time to land
                 const uint64_t t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 200000ull) {
                 }
@@ -182,7 +196,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
         }
         __syncwarp();
     } else if (warp == 1 && leader) {
-        // ---------------- scale copies and MMAs (even CTA) ----------------
+        // ---------------- MMAs (even CTA) ----------------
         int s = 0;
         uint32_t ph = 0, it = 0;
         bool ok = true, issued = false;
@@ -193,25 +207,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
                 ok = wait_bar_cluster(tempty, (it & 1) ^ 1, g, SITE_MMA_TMEM_EMPTY);
                 tc_fence_after_sync();
                 for (int k = 0; ok && k < P.k_steps; ++k) {
-                    if (!wait_bar_cluster(&full[s], ph, g, SITE_MMA_FULL)) {
+                    if (!wait_bar(&full[s], ph, g, SITE_MMA_FULL) ||
+                        !wait_bar_cluster(&sready[s], ph, g, SITE_MMA_OPERAND)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after_sync();
                     const uint32_t a = smem_u32(smem + s * Cfg::STAGE_BYTES);
-                    const uint32_t b = a + Cfg::A_BYTES, sa = b + Cfg::B_BYTES, sb = sa + Cfg::SA_BYTES;
+                    const uint32_t b = a + Cfg::A_BYTES;
                     const uint32_t ta = tmem + Cfg::BN + s * Cfg::SCALE_COLS, tb = ta + 4 * Cfg::S_ATOMS;
-                    const int na = P.k_atoms - 4 * k < 4 ? P.k_atoms - 4 * k : 4;
+                    // always four: past K's end codes and scales are zeros (a bound
+                    // tested per instruction cost the issuing thread 8% of the loop)
                     const uint64_t ad = make_sw128_kmajor_desc(a), bd = make_sw128_kmajor_desc(b);
 #pragma unroll
-                    for (int q = 0; q < Cfg::S_ATOMS; ++q) {
-                        tmem_cp_scales_pair(ta + 4 * q, make_scale_desc(sa + MX_ATOM_BYTES * q));
-                        tmem_cp_scales_pair(tb + 8 * q, make_scale_desc(sb + MX_ATOM_BYTES * q));
-                        tmem_cp_scales_pair(tb + 8 * q + 4, make_scale_desc(sb + Cfg::SA_BYTES + MX_ATOM_BYTES * q));
-                    }
-#pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        if (q >= na) break;
                         const uint32_t acc = (k > 0 || q > 0) ? 1u : 0u;
                         if constexpr (NVF4) {
                             umma_mx_ss_pair<true>(tmem, ad + 2 * q, bd + 2 * q, P.idesc, ta + 4 * q, tb + 8 * q, acc);
@@ -237,10 +246,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
             wait_bar_drain(done, 0, g);
         }
         __syncwarp();
+    } else if (warp >= 10) {
+        // ---------------- scales: shared memory -> TMEM ----------------
+        const uint32_t quarter = (uint32_t)(warp % 4 * 32) << 16;
+        const uint32_t l_sready = mapa_shared(smem_u32(sready), 0);
+        int s = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        MxTile t;
+        for (int64_t i = pid; ok && mx_pair_tile(P, blocks, i, lane, t); i += P.programs) {
+            for (int k = 0; k < P.k_steps; ++k) {
+                // the scales are there; the buffer's previous readers are done (the
+                // producer has waited for the same phase of empty[s])
+                ok = __all_sync(0xFFFFFFFFu, wait_bar(&sfull[s], ph, g, SITE_DQ_RAW) &&
+                                                 wait_bar(&empty[s], ph ^ 1, g, SITE_DQ_EMPTY));
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint8_t* sa = smem + s * Cfg::STAGE_BYTES + Cfg::A_BYTES + Cfg::B_BYTES + lane * 16;
+                const uint32_t ta = tmem + Cfg::BN + s * Cfg::SCALE_COLS + quarter;
+                uint32_t ra[4 * Cfg::S_ATOMS], rb[8 * Cfg::S_ATOMS];
+#pragma unroll
+                for (int q = 0; q < 3 * Cfg::S_ATOMS; ++q) {
+                    // A's atoms, then B's first 128 rows', then its second
+                    const uint4 w = *reinterpret_cast<const uint4*>(sa + MX_ATOM_BYTES * q);
+                    uint32_t* r = q < Cfg::S_ATOMS ? ra + 4 * q
+                                                   : rb + 8 * (q % Cfg::S_ATOMS) + (q < 2 * Cfg::S_ATOMS ? 0 : 4);
+                    r[0] = w.x;
+                    r[1] = w.y;
+                    r[2] = w.z;
+                    r[3] = w.w;
+                }
+                tmem_st_32x32b(ta, ra);
+                tmem_st_32x32b(ta + 4 * Cfg::S_ATOMS, rb);
+                tmem_st_wait();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote_tmem(l_sready + 8u * s);
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1;
+                }
+            }
+        }
     } else if (warp >= 2) {
         // ---------------- epilogue ----------------
         const int ew = warp % 4, half = (warp - 2) / 4;
-        float* stage = stage_all + (warp - 2) * (32 * 33);
+        float* stage = stage_all + (warp - 2) * (32 * 33 + 12);  // 16-byte aligned for the packed form
         const uint32_t l_tempty = mapa_shared(smem_u32(tempty), 0);
         uint32_t it = 0;
         MxTile t;
@@ -250,21 +301,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(320, 1)
             int rows = t.rows - 128 * (int)rank - 32 * ew;
             rows = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
             const int64_t m0 = t.row0 + 128 * rank + 32 * ew, n0 = t.n0 + 128 * half;
-            if (!__all_sync(0xFFFFFFFFu, wait_bar_cluster(tfull, it & 1, g, SITE_EPI_TMEM_FULL))) break;
+            if (!__all_sync(0xFFFFFFFFu, wait_bar(tfull, it & 1, g, SITE_EPI_TMEM_FULL))) break;
             tc_fence_after_sync();
             const uint32_t ta = tmem + 128 * half + ((uint32_t)(ew * 32) << 16);
-            float v[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_load_chunk<32>(ta + 32 * c, v[c]);
+            const bool packed = P.vec32 && P.epi.d_type != DT_F32 && P.epi.beta == 0.0f && n0 + 128 <= P.epi.N;
+            if (packed && rows > 0) {
+                // a 16-bit D without C: half of the finished values wait in shared
+                // memory, half in registers, so the accumulator is given back
+                // before the first store
+                uint32_t w[32];
+                uint8_t* buf = reinterpret_cast<uint8_t*>(stage);
+                with_epi_act(P.epi, [&](auto act) {
+                    constexpr int ACT = decltype(act)::value;
+                    if (P.epi.d_type == DT_BF16) {
+                        mx_pack64<ACT, DT_BF16>(P.epi, alpha, ta, n0, w, lane);
+                        mx_stage64(buf, w, lane);
+                        mx_pack64<ACT, DT_BF16>(P.epi, alpha, ta + 64, n0 + 64, w, lane);
+                    } else {
+                        mx_pack64<ACT, DT_F16>(P.epi, alpha, ta, n0, w, lane);
+                        mx_stage64(buf, w, lane);
+                        mx_pack64<ACT, DT_F16>(P.epi, alpha, ta + 64, n0 + 64, w, lane);
+                    }
+                });
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote_tmem(l_tempty);
+                uint16_t* d = static_cast<uint16_t*>(P.epi.D) + m0 * P.epi.ldd + n0;
+                mx_store64(buf, d, P.epi.ldd, rows, lane);
+                __syncwarp();
+                mx_stage64(buf, w, lane);
+                __syncwarp();
+                mx_store64(buf, d + 64, P.epi.ldd, rows, lane);
+                __syncwarp();
+                continue;
+            }
+            if (rows > 0) {
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    if (n0 + 32 * c >= P.epi.N) break;
+                    float v[32];
+                    tmem_load_chunk<32>(ta + 32 * c, v);
+                    mx_store_block(P.epi, P.vec32, alpha, m0, rows, n0 + 32 * c, v, stage, lane);
+                }
+            }
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(l_tempty);
-            if (rows > 0) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    if (n0 + 32 * c < P.epi.N)
-                        mx_store_block(P.epi, P.vec32, alpha, m0, rows, n0 + 32 * c, v[c], stage, lane);
-            }
+            if (lane == 0) mbar_arrive_remote_tmem(l_tempty);
         }
     }
     tc_fence_before_sync();
@@ -297,7 +379,7 @@ template <bool NVF4>
 cudaError_t launch_mx_pair_t(const MxMaps& m, const MxGemmParams& p, int clusters, cudaStream_t st) {
     const cudaError_t e = mx_pair_configure<NVF4>();
     if (e != cudaSuccess) return e;
-    return launch_pdl(mx_pair_kernel<NVF4>, 2 * clusters, 320, MxPairCfg<NVF4>::SMEM_BYTES, st, m.a, m.b, m.sa, m.sb, p);
+    return launch_pdl(mx_pair_kernel<NVF4>, 2 * clusters, MX_PAIR_THREADS, MxPairCfg<NVF4>::SMEM_BYTES, st, m.a, m.b, m.sa, m.sb, p);
 }
 
 template <bool NVF4>
@@ -308,7 +390,7 @@ int mx_pair_clusters_t() {
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2, 1, 1);
-    cfg.blockDim = dim3(320, 1, 1);
+    cfg.blockDim = dim3(MX_PAIR_THREADS, 1, 1);
     cfg.dynamicSmemBytes = MxPairCfg<NVF4>::SMEM_BYTES;
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel<NVF4>, &cfg) != cudaSuccess) {
