@@ -244,6 +244,9 @@ struct MxChoice {
     int bn, splits, pair;
 };
 
+// Rows of A that a stage of the one-tile kernel holds.
+int rows_staged(const MxProduct& p) { return (int)(p.M < 128 ? ceil_div(p.M, 8) * 8 : 128); }
+
 // Clusters of two that the CTA-pair kernel keeps resident (asked once per device).
 int pair_clusters(gemm_handle_t h, int32_t format) {
     static std::atomic<int> known[64][2];
@@ -282,6 +285,13 @@ MxChoice choose(const MxProduct& p, int sm_count, int clusters, int forced_split
     const int64_t tiles = tiles_along_m(p, 128) * ceil_div(p.N, c.bn);
     const int want = forced_split ? forced_split : 8;
     while (c.splits * 2 <= want && c.splits * 2 <= steps && (forced_split || tiles * c.splits * 2 <= slots)) c.splits *= 2;
+    const int a_rows = rows_staged(p);
+    while (c.splits > 1 && !mx_gemm_stages(c.bn, p.format, a_rows, c.splits)) {
+        if (c.bn == 128 && !forced)
+            c.bn = 64;
+        else
+            c.splits /= 2;
+    }
     return c;
 }
 
@@ -310,8 +320,8 @@ int run_product(gemm_handle_t h, const gemm_op_t* op, MxProduct& p, cudaStream_t
     k.k_steps = (int32_t)ceil_div(p.K, MX_KSTEP);
     k.k_atoms = (int32_t)ceil_div(p.K, 64);
     k.splits = c.splits;
-    k.a_rows = (int32_t)(p.M < 128 && !c.pair ? ceil_div(p.M, 8) * 8 : 128);
-    k.stages = c.pair ? 0 : mx_gemm_stages(c.bn, p.format, k.a_rows);
+    k.a_rows = c.pair ? 128 : rows_staged(p);
+    k.stages = c.pair ? 0 : mx_gemm_stages(c.bn, p.format, k.a_rows, c.splits);
     k.b3d = p.experts > 1;
     k.idesc = make_idesc_mx(p.format == GEMM_NVFP4, c.pair ? 256 : 128, c.bn);
     const int64_t ds = float_size(p.epi.d_type);

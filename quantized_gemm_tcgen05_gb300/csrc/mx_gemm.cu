@@ -12,10 +12,10 @@ cudaError_t launch_mx_gemm(int bn, int format, const MxMaps& m, const MxGemmPara
     }
 }
 
-int mx_gemm_stages(int bn, int format, int a_rows) {
+int mx_gemm_stages(int bn, int format, int a_rows, int splits) {
     const bool nv = format == MXF_NVFP4;
-    if (bn == 64) return nv ? MxCfg<64, true>::max_stages(a_rows) : MxCfg<64, false>::max_stages(a_rows);
-    return nv ? MxCfg<128, true>::max_stages(a_rows) : MxCfg<128, false>::max_stages(a_rows);
+    if (bn == 64) return nv ? MxCfg<64, true>::max_stages(a_rows, splits) : MxCfg<64, false>::max_stages(a_rows, splits);
+    return nv ? MxCfg<128, true>::max_stages(a_rows, splits) : MxCfg<128, false>::max_stages(a_rows, splits);
 }
 
 }  // namespace qg

@@ -4,19 +4,23 @@
 // multiplies the scales in (tcgen05.mma with block scales), fp32 accumulator in
 // TMEM.  A stage holds one K-step of 256 codes: the 128-byte swizzled rows of A
 // (up to 128) and of B (BN), and the scale atoms of both (128 rows x 256 codes
-// each).  The MMA thread copies the atoms from shared memory to TMEM columns
-// (tcgen05.cp, executed in order before the MMAs issued after it) and issues
-// four MMAs of K = 64.  The scale columns are double-buffered: before step i
-// overwrites a buffer, the MMAs of step i - 2 that read it have been waited for.
+// each).  Four warps move the scales from shared memory to TMEM, one per
+// 32-lane quarter (every quarter holds all of them); there are as many scale
+// buffers as stages, so a buffer is free whenever its stage is.
 //
-// The tile's K-steps are shared out over the `splits` CTAs of a cluster; their
-// fp32 partial tiles are added in rank order through distributed shared
-// memory, each CTA finishing its share of the columns.  Nothing goes through
-// global memory but operands and D, and no workspace is needed.
+// The tile's K-steps are shared out over the `splits` CTAs of a cluster.  When
+// all of them are through, each sends every other its share of the columns of
+// its fp32 partial tile (bulk copies into the idle ring, counted by the
+// receiver's barrier), adds what it received in rank order and finishes its
+// columns.  Nothing goes through global memory but operands and D, and no
+// workspace is needed.  Bulk copies carry their own completion: cluster
+// barriers and remote loads in their place took 4 us of a 9 us launch.
 //
-// 128 threads: warp 0's first lane issues the copies, warp 1's the MMAs, then
-// all four warps run the epilogue.  Two CTAs fit an SM (shared memory and TMEM
-// both), so one's set-up and epilogue overlap the other's main loop.
+//   warp 0     TMA producer          warps 4-7  scales
+//   warp 1     MMAs                  all        epilogue
+//
+// Two CTAs fit an SM (shared memory and TMEM both), so one's set-up and
+// epilogue overlap the other's main loop.
 //
 // Only the rows of A that exist are copied (a_rows): with few rows the MMAs read
 // whatever shared memory holds below them, which reaches only accumulator rows
@@ -28,49 +32,52 @@
 
 namespace qg {
 
+constexpr int MX_THREADS = 256;
+
 template <int BN, bool NVF4>
 struct MxCfg {
     static constexpr uint32_t B_BYTES = BN * 128;
     static constexpr uint32_t S_BYTES = NVF4 ? 2048 : 1024;  // one operand's scale atoms of a K-step
     static constexpr int S_ATOMS = NVF4 ? 4 : 2;
-    static constexpr int MAX_STAGES = 8;
-    static constexpr uint32_t TMEM_COLS = tmem_cols_for(BN + 64);
-    static constexpr uint32_t AUX_BYTES = (2 * MAX_STAGES + 2) * 8 + 16;
-    static constexpr uint32_t PART_PITCH = 129 * 16;  // a quad of columns x 128 rows, padded
-    static constexpr uint32_t EPI_BYTES = BN / 4 * PART_PITCH;  // partial tile; also the 4 warps' 32 x 33 floats
-    static uint32_t stage_bytes(int a_rows) { return a_rows * 128u + B_BYTES + 2 * S_BYTES; }
-    // the ring, with room below the last stage for the rows of A an MMA reads beyond a_rows
-    static uint32_t ring_bytes(int a_rows, int stages) {
-        const uint32_t sb = stage_bytes(a_rows);
-        uint32_t n = sb * stages;
-        const uint32_t reach = sb * (stages - 1) + 128 * 128;
-        if (n < reach) n = reach;
-        return n < EPI_BYTES ? EPI_BYTES : n;
-    }
+    static constexpr uint32_t TMEM_COLS = 256;
+    static constexpr uint32_t SCALE_COLS = 8 * S_ATOMS;  // A 4, B 4 a K-atom
+    static constexpr int MAX_STAGES = (TMEM_COLS - BN) / SCALE_COLS < 8 ? (TMEM_COLS - BN) / SCALE_COLS : 8;
+    static constexpr uint32_t AUX_BYTES = (3 * MAX_STAGES + 3) * 8 + 16;
+    static constexpr uint32_t WARP_STAGE = (32 * 33 + 12) * 4;  // an epilogue warp's buffer
     // two CTAs an SM: at most half of its 228 KB, a kilobyte each reserved
     static constexpr uint32_t BUDGET = 113 * 1024;
-    static uint32_t smem_bytes(int a_rows, int stages) {
-        const uint32_t n = 1024 + ring_bytes(a_rows, stages) + AUX_BYTES;
+    QG_HD static uint32_t stage_bytes(int a_rows) { return a_rows * 128u + B_BYTES + 2 * S_BYTES; }
+    // the ring, with room below the last stage for the rows of A an MMA reads
+    // beyond a_rows, and for what the epilogue keeps there: its warps' buffers,
+    // or the partial tile sent and the shares received (rows of an odd pitch)
+    QG_HD static uint32_t ring_bytes(int a_rows, int stages, int splits) {
+        const uint32_t sb = stage_bytes(a_rows);
+        uint32_t n = sb * (stages - 1) + (sb > 16384u ? sb : 16384u);
+        const uint32_t epi = splits > 1 ? 2 * (BN / 4) * (a_rows + 1) * 16 : 8 * WARP_STAGE;
+        return ((n > epi ? n : epi) + 1023) / 1024 * 1024;
+    }
+    static uint32_t smem_bytes(int a_rows, int stages, int splits) {
+        const uint32_t n = 1024 + ring_bytes(a_rows, stages, splits) + AUX_BYTES;
         return n < 80 * 1024 ? 80 * 1024 : n;  // never three an SM: TMEM holds two
     }
-    static int max_stages(int a_rows) {
+    // 0: the partial tiles do not fit
+    static int max_stages(int a_rows, int splits) {
         int s = MAX_STAGES;
-        while (s > 2 && smem_bytes(a_rows, s) > BUDGET) --s;
-        return s;
+        while (s > 0 && smem_bytes(a_rows, s, splits) > BUDGET) --s;
+        return s < 2 ? 0 : s;
     }
 };
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
+// Bulk copy from this CTA's shared memory to another CTA's (cluster addresses),
+// completing its bytes on a barrier there.
+__device__ __forceinline__ void bulk_s2cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "r"(src), "r"(bytes), "r"(bar)
                  : "memory");
-    return v;
 }
 
 template <int BN, bool NVF4>
-__global__ void __launch_bounds__(128, 2)
+__global__ void __launch_bounds__(MX_THREADS, 2)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                    const __grid_constant__ MxGemmParams P) {
@@ -79,24 +86,33 @@ __global__ void __launch_bounds__(128, 2)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int S = P.stages;
     const uint32_t a_bytes = (uint32_t)P.a_rows * 128u;
-    const uint32_t stage_bytes = a_bytes + Cfg::B_BYTES + 2 * Cfg::S_BYTES;
-    uint32_t ring_bytes = stage_bytes * (S - 1) + (stage_bytes > 16384u ? stage_bytes : 16384u);
-    if (ring_bytes < Cfg::EPI_BYTES) ring_bytes = Cfg::EPI_BYTES;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes);
+    const uint32_t stage_bytes = Cfg::stage_bytes(P.a_rows);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + Cfg::ring_bytes(P.a_rows, S, P.splits));
     uint64_t* empty = full + Cfg::MAX_STAGES;
-    uint64_t* tfull = empty + Cfg::MAX_STAGES;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tfull + 2);
+    uint64_t* sready = empty + Cfg::MAX_STAGES;  // the stage has landed and its scales are in TMEM (4 warps)
+    uint64_t* tfull = sready + Cfg::MAX_STAGES;  // the accumulator is complete
+    uint64_t* idle = tfull + 1;                  // every CTA of the cluster is through with its ring
+    uint64_t* part = idle + 1;                   // the partial tiles' shares have arrived
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(part + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int splits = P.splits;
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
+            mbar_init(&sready[s], 4);
         }
         mbar_init(tfull, 1);
+        mbar_init(idle, (uint32_t)splits);
+        mbar_init(part, 1);
         *abort_flag = 0;
         fence_barrier_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        tma_prefetch_desc(&tmSA);
+        tma_prefetch_desc(&tmSB);
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, Cfg::TMEM_COLS);
@@ -104,15 +120,25 @@ __global__ void __launch_bounds__(128, 2)
     }
     tc_fence_before_sync();
     __syncthreads();
+    if (splits > 1) cluster_sync();  // every CTA's barriers exist before another's copies complete on them
     tc_fence_after_sync();
     const uint32_t tmem = *tmem_slot;
     griddep_launch_dependents();
 
-    const int rank = P.splits > 1 ? (int)cluster_ctarank() : 0;
-    const int64_t tile = blockIdx.x / P.splits;
+    const int rank = splits > 1 ? (int)cluster_ctarank() : 0;
+    const int64_t tile = blockIdx.x / splits;
     const int64_t tm = tile % P.tiles_m, tn = tile / P.tiles_m;
-    const int k0 = (int)((int64_t)P.k_steps * rank / P.splits), k1 = (int)((int64_t)P.k_steps * (rank + 1) / P.splits);
+    const int k0 = (int)((int64_t)P.k_steps * rank / splits), k1 = (int)((int64_t)P.k_steps * (rank + 1) / splits);
+    const int64_t n0 = tn * BN;
     const Guard g{P.status, P.timeout_ns, abort_flag};
+    if (!P.offsets && warp == 0 && lane == 0) {
+        // warm L2 with the first stages of the weights while the previous kernel
+        // in the stream finishes (a hint: L2 is where memory is coherent)
+        for (int k = k0; k < k1 && k < k0 + S; ++k) {
+            tma_prefetch_l2_2d(&tmB, k * 128, (int32_t)n0);
+            tma_prefetch_l2_2d(&tmSB, k * (int)(Cfg::S_BYTES / 8), (int32_t)(n0 / 128));
+        }
+    }
 
     griddep_wait();
     int expert = 0, rows = 0;
@@ -127,128 +153,210 @@ __global__ void __launch_bounds__(128, 2)
         rows = (int)(P.epi.M - row0 < 128 ? P.epi.M - row0 : 128);
         atom_row = tm;
     }
-    const int64_t n0 = tn * BN;
 
     bool ok = live;
     if (live && warp == 0) {
-        if (lane == 0) {
-            for (int k = k0; k < k1; ++k) {
-                const int i = k - k0, s = i % S;
-                if (!wait_bar(&empty[s], ((i / S) & 1) ^ 1, g, SITE_PRODUCER_EMPTY)) break;
-                uint8_t* a = smem + (size_t)s * stage_bytes;
-                uint8_t* b = a + a_bytes;
-                uint8_t* sa = b + Cfg::B_BYTES;
-                mbar_arrive_expect_tx(&full[s], stage_bytes);
-                tma_load_2d(a, &tmA, &full[s], k * 128, (int32_t)row0);
-                tma_load_2d(sa, &tmSA, &full[s], k * (int)(Cfg::S_BYTES / 8), (int32_t)atom_row);
+        int s = 0;
+        uint32_t ph = 1;
+        const uint32_t stage_tx = stage_bytes;
+        int kx = k0 * 128, sx = k0 * (int)(Cfg::S_BYTES / 8);
+        for (int k = k0; k < k1; ++k) {
+            if (!__all_sync(0xFFFFFFFFu, wait_bar(&empty[s], ph, g, SITE_PRODUCER_EMPTY))) break;
+            uint8_t* a = smem + (uint32_t)s * stage_bytes;
+            uint8_t* b = a + a_bytes;
+            uint8_t* sa = b + Cfg::B_BYTES;
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&full[s], stage_tx);
+                tma_load_2d(sa, &tmSA, &full[s], sx, (int32_t)atom_row);
                 if (P.b3d) {
-                    tma_load_3d(b, &tmB, &full[s], k * 128, (int32_t)n0, expert);
-                    tma_load_3d(sa + Cfg::S_BYTES, &tmSB, &full[s], k * (int)(Cfg::S_BYTES / 8), (int32_t)(n0 / 128), expert);
+                    tma_load_3d(sa + Cfg::S_BYTES, &tmSB, &full[s], sx, (int32_t)(n0 / 128), expert);
+                    tma_load_3d(b, &tmB, &full[s], kx, (int32_t)n0, expert);
                 } else {
-                    tma_load_2d(b, &tmB, &full[s], k * 128, (int32_t)n0);
-                    tma_load_2d(sa + Cfg::S_BYTES, &tmSB, &full[s], k * (int)(Cfg::S_BYTES / 8), (int32_t)(n0 / 128));
+                    tma_load_2d(sa + Cfg::S_BYTES, &tmSB, &full[s], sx, (int32_t)(n0 / 128));
+                    tma_load_2d(b, &tmB, &full[s], kx, (int32_t)n0);
                 }
+                tma_load_2d(a, &tmA, &full[s], kx, (int32_t)row0);
+            }
+            __syncwarp();
+            kx += 128;
+            sx += (int)(Cfg::S_BYTES / 8);
+            if (++s == S) {
+                s = 0;
+                ph ^= 1;
             }
         }
-        __syncwarp();
     } else if (live && warp == 1) {
-        if (lane == 0) {
-            const uint32_t sfa = tmem + BN, sfb = tmem + BN + 32;  // two buffers of 16 columns each
-            const uint32_t sfb_off = (uint32_t)(n0 % 128) / 32;
-            for (int k = k0; k < k1; ++k) {
-                const int i = k - k0, s = i % S;
-                if (!wait_bar(&full[s], (i / S) & 1, g, SITE_MMA_FULL)) {
-                    ok = false;
-                    break;
-                }
-                // the scale buffer's previous readers, the MMAs of step i - 2
-                if (i >= 2 && !wait_bar(&empty[(i - 2) % S], ((i - 2) / S) & 1, g, SITE_MMA_OPERAND)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after_sync();
-                const uint32_t a = smem_u32(smem + (size_t)s * stage_bytes);
-                const uint32_t b = a + a_bytes, sa = b + Cfg::B_BYTES, sb = sa + Cfg::S_BYTES;
-                const uint32_t ta = sfa + (i & 1) * 16, tb = sfb + (i & 1) * 16;
-                const int na = P.k_atoms - 4 * k < 4 ? P.k_atoms - 4 * k : 4;  // 64-wide steps that exist
-#pragma unroll
-                for (int q = 0; q < Cfg::S_ATOMS; ++q) {
-                    tmem_cp_scales(ta + 4 * q, make_scale_desc(sa + MX_ATOM_BYTES * q));
-                    tmem_cp_scales(tb + 4 * q, make_scale_desc(sb + MX_ATOM_BYTES * q));
-                }
-                const uint64_t ad = make_sw128_kmajor_desc(a), bd = make_sw128_kmajor_desc(b);
+        const uint32_t sfb_off = 4 * Cfg::S_ATOMS + (uint32_t)(n0 % 128) / 32;
+        const uint64_t ad0 = make_sw128_kmajor_desc(smem_u32(smem)), bd0 = make_sw128_kmajor_desc(smem_u32(smem) + a_bytes);
+        uint64_t ad = ad0, bd = bd0;
+        uint32_t ta = tmem + BN, acc = 0, ph = 0;
+        int s = 0;
+        for (int k = k0; k < k1; ++k) {
+            // the scale warps have seen the whole stage land before they arrive here
+            if (!__all_sync(0xFFFFFFFFu, wait_bar(&sready[s], ph, g, SITE_MMA_OPERAND))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after_sync();
+            const uint32_t tb = ta + sfb_off;
+            if (elect_one()) {
+                // always four: past K's end codes and scales are zeros
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    if (q >= na) break;
-                    const uint32_t acc = (i > 0 || q > 0) ? 1u : 0u;
-                    if constexpr (NVF4)
-                        umma_mx_ss<true>(tmem, ad + 2 * q, bd + 2 * q, P.idesc, ta + 4 * q, tb + 4 * q + sfb_off, acc);
-                    else {
+                    if constexpr (NVF4) {
+                        umma_mx_ss<true>(tmem, ad + 2 * q, bd + 2 * q, P.idesc, ta + 4 * q, tb + 4 * q, q ? 1u : acc);
+                    } else {
                         // an atom's four scales cover two instructions: bytes 0-1, then 2-3
                         const uint32_t id = (q & 1) * 2u;
                         umma_mx_ss<false>(tmem, ad + 2 * q, bd + 2 * q, P.idesc | (id << 29) | (id << 4),
-                                          ta + 4 * (q / 2), tb + 4 * (q / 2) + sfb_off, acc);
+                                          ta + 4 * (q / 2), tb + 4 * (q / 2), q ? 1u : acc);
                     }
                 }
                 umma_commit(&empty[s]);
+                if (k == k1 - 1) umma_commit(tfull);
             }
-            if (ok) umma_commit(tfull);
+            __syncwarp();
+            acc = 1;
+            ad += stage_bytes / 16;
+            bd += stage_bytes / 16;
+            ta += Cfg::SCALE_COLS;
+            if (++s == S) {
+                s = 0;
+                ph ^= 1;
+                ad = ad0;
+                bd = bd0;
+                ta = tmem + BN;
+            }
         }
-        __syncwarp();
+    } else if (live && warp >= 4) {
+        const uint32_t quarter = (uint32_t)(warp % 4 * 32) << 16;
+        int s = 0;
+        uint32_t ph = 0;
+        for (int k = k0; k < k1; ++k) {
+            // the stage is there; the scale buffer's previous readers are done: the
+            // producer has waited for that phase of empty[s]
+            ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[s], ph, g, SITE_DQ_RAW));
+            if (!ok) break;
+            tc_fence_after_sync();
+            const uint8_t* sa = smem + (uint32_t)s * stage_bytes + a_bytes + Cfg::B_BYTES + lane * 16;
+            uint32_t r[8 * Cfg::S_ATOMS];
+#pragma unroll
+            for (int q = 0; q < 2 * Cfg::S_ATOMS; ++q) {
+                const uint4 w = *reinterpret_cast<const uint4*>(sa + MX_ATOM_BYTES * q);
+                r[4 * q] = w.x;
+                r[4 * q + 1] = w.y;
+                r[4 * q + 2] = w.z;
+                r[4 * q + 3] = w.w;
+            }
+            tmem_st_32x32b(tmem + BN + (uint32_t)s * Cfg::SCALE_COLS + quarter, r);
+            tmem_st_wait();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sready[s]);
+            if (++s == S) {
+                s = 0;
+                ph ^= 1;
+            }
+        }
     }
     // every thread learns whether the accumulator is complete
     if (live) {
-        ok = wait_bar(tfull, 0, g, SITE_EPI_TMEM_FULL);
+        ok = ok && wait_bar(tfull, 0, g, SITE_EPI_TMEM_FULL);
         tc_fence_after_sync();
     }
-    const bool all_ok = __syncthreads_and(ok ? 1 : 0) != 0;
+    bool all_ok = __syncthreads_and(ok ? 1 : 0) != 0;
     if (live && !all_ok) {
         // gave up: let copies in flight land and issued MMAs finish before shared memory and TMEM go
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 200000ull) {
         }
     }
-    const uint32_t tb = tmem + ((uint32_t)(warp * 32) << 16);
-    const int wrows = rows - warp * 32 < 0 ? 0 : (rows - warp * 32 < 32 ? rows - warp * 32 : 32);
-    if (P.splits == 1) {
+    const int ew = warp % 4, half = warp / 4;
+    const uint32_t tb = tmem + half * (BN / 2) + ((uint32_t)(ew * 32) << 16);
+    const int wrows = rows - ew * 32 < 0 ? 0 : (rows - ew * 32 < 32 ? rows - ew * 32 : 32);
+    if (splits == 1) {
         if (all_ok && wrows > 0) {
-            float* stage = reinterpret_cast<float*>(smem) + warp * (32 * 33);
+            uint8_t* buf = smem + warp * Cfg::WARP_STAGE;
+            float* stage = reinterpret_cast<float*>(buf);
+            const int64_t m0 = row0 + ew * 32, nh = n0 + half * (BN / 2);
+            bool done = false;
+            if constexpr (BN == 128) {
+                if (P.vec32 && P.epi.d_type != DT_F32 && P.epi.beta == 0.0f && nh + 64 <= P.epi.N) {
+                    uint32_t w[32];
+                    with_epi_act(P.epi, [&](auto act) {
+                        if (P.epi.d_type == DT_BF16)
+                            mx_pack64<decltype(act)::value, DT_BF16>(P.epi, alpha, tb, nh, w, lane);
+                        else
+                            mx_pack64<decltype(act)::value, DT_F16>(P.epi, alpha, tb, nh, w, lane);
+                    });
+                    mx_stage64(buf, w, lane);
+                    __syncwarp();
+                    mx_store64(buf, static_cast<uint16_t*>(P.epi.D) + m0 * P.epi.ldd + nh, P.epi.ldd, wrows, lane);
+                    done = true;
+                }
+            }
+            if (!done) {
 #pragma unroll 1
-            for (int c = 0; c < BN / 32; ++c) {
-                if (n0 + 32 * c >= P.epi.N) break;
-                float v[32];
-                tmem_load_chunk<32>(tb + 32 * c, v);
-                mx_store_block(P.epi, P.vec32, alpha, row0 + warp * 32, wrows, n0 + 32 * c, v, stage, lane);
+                for (int c = 0; c < BN / 64; ++c) {
+                    if (nh + 32 * c >= P.epi.N) break;
+                    float v[32];
+                    tmem_load_chunk<32>(tb + 32 * c, v);
+                    mx_store_block(P.epi, P.vec32, alpha, m0, wrows, nh + 32 * c, v, stage, lane);
+                }
             }
         }
     } else {
-        // partial tile -> shared memory, [quad of columns][row]
+        // partial tile -> shared memory, [quad of columns][row], rows at an odd pitch
+        constexpr int QUADS = BN / 4;
+        const uint32_t pitch = (uint32_t)(rows | 1) * 16u;
+        const int nq = QUADS / splits;  // quads of this CTA's columns
+        uint8_t* recv = smem + (size_t)QUADS * pitch;
         if (all_ok && wrows > 0) {
 #pragma unroll 1
-            for (int c = 0; c < BN / 32; ++c) {
+            for (int c = 0; c < BN / 64; ++c) {
                 float v[32];
                 tmem_load_chunk<32>(tb + 32 * c, v);
+                if (lane < wrows) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<float4*>(smem + (8 * c + j) * Cfg::PART_PITCH + (warp * 32 + lane) * 16) =
-                        make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<float4*>(smem + (half * (BN / 8) + 8 * c + j) * pitch + (ew * 32 + lane) * 16) =
+                            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                }
             }
         }
-        cluster_sync();
+        fence_proxy_async_smem();  // ... visible to the bulk copies
+        __syncthreads();
+        if (live && threadIdx.x == 0) {
+            // this CTA's ring is idle (its accumulator is complete): tell everyone,
+            // and wait until theirs are.  Nothing is published, so the arrivals are relaxed
+            mbar_arrive_expect_tx(part, (uint32_t)splits * nq * pitch);
+            for (int z = 0; z < splits; ++z) mbar_arrive_remote_relaxed(mapa_shared(smem_u32(idle), z));
+            if (wait_bar_cluster(idle, 0, g, SITE_DRAIN)) {
+                // bytes are sent even after a failure, so that no receiver waits in vain
+                for (int z = 0; z < splits; ++z)
+                    bulk_s2cluster(mapa_shared(smem_u32(recv) + (uint32_t)(rank * nq) * pitch, z),
+                                   smem_u32(smem) + (uint32_t)(z * nq) * pitch, (uint32_t)nq * pitch,
+                                   mapa_shared(smem_u32(part), z));
+            }
+        }
+        if (live) {
+            ok = wait_bar_cluster(part, 0, g, SITE_DRAIN);
+            all_ok = __syncthreads_and(all_ok && ok ? 1 : 0) != 0;
+            // everyone's copies to this CTA have landed: their senders may leave
+            if (threadIdx.x == 0)
+                for (int z = 0; z < splits; ++z) mbar_arrive_remote_relaxed(mapa_shared(smem_u32(idle), z));
+        }
         if (all_ok) {
-            constexpr int QUADS = BN / 4;
-            const int q0 = QUADS * rank / P.splits, nq = QUADS * (rank + 1) / P.splits - q0;
             const EpiParams& e = P.epi;
             EpiArith ar = epi_arith(e);
             ar.alpha = alpha;
-            const uint32_t base = smem_u32(smem);
-            for (int t = threadIdx.x; t < rows * nq; t += 128) {
-                const int q = q0 + t % nq, r = t / nq;
-                const int64_t n = n0 + 4 * q, m = row0 + r;
+            for (int t = threadIdx.x; t < rows * nq; t += MX_THREADS) {
+                const int q = t % nq, r = t / nq;
+                const int64_t n = n0 + 4 * (rank * nq + q), m = row0 + r;
                 if (n >= e.N) continue;
                 float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int z = 0; z < P.splits; ++z) {  // in K order
-                    const float4 p = ld_cluster_f4(mapa_shared(base + q * Cfg::PART_PITCH + r * 16, z));
+                for (int z = 0; z < splits; ++z) {  // in K order
+                    const float4 p = *reinterpret_cast<const float4*>(recv + (uint32_t)(z * nq + q) * pitch + r * 16);
                     sum.x += p.x;
                     sum.y += p.y;
                     sum.z += p.z;
@@ -274,7 +382,8 @@ __global__ void __launch_bounds__(128, 2)
                 }
             }
         }
-        cluster_sync();  // no CTA leaves while another reads its partial tile
+        // shared memory goes only when every peer has this CTA's share
+        if (live && threadIdx.x == 0) wait_bar_cluster(idle, 1, g, SITE_DRAIN);
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -301,8 +410,8 @@ cudaError_t launch_mx_bn(const MxMaps& m, const MxGemmParams& p, int grid, cudaS
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = Cfg::smem_bytes(p.a_rows, p.stages);
+    cfg.blockDim = dim3(MX_THREADS);
+    cfg.dynamicSmemBytes = Cfg::smem_bytes(p.a_rows, p.stages, p.splits);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     int n = 0;

@@ -37,8 +37,8 @@ QG_HD uint32_t make_idesc_mx(int nvf4, int m, int n) {
 }
 
 cudaError_t launch_mx_gemm(int bn, int format, const MxMaps& m, const MxGemmParams& p, int grid, cudaStream_t st);
-// Stages of the ring for a tile of a_rows x bn.
-int mx_gemm_stages(int bn, int format, int a_rows);
+// Stages of the ring for a tile of a_rows x bn; 0: its partial tiles do not fit.
+int mx_gemm_stages(int bn, int format, int a_rows, int splits);
 
 
 // The CTA-pair kernel: 256 x 256 tiles, persistent clusters of two.

@@ -142,42 +142,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_PAIR_THREADS, 1)
         uint32_t ph = 0, armed = 0, armed_par = 0;
         bool ok = true;
         MxTile t;
+        const uint32_t l_full = mapa_shared(smem_u32(full), 0);
         for (int64_t i = pid; ok && mx_pair_tile(P, blocks, i, lane, t); i += P.programs) {
-            if (lane == 0) {
-                const int32_t a0 = (int32_t)(t.row0 + 128 * rank), b0 = (int32_t)(t.n0 + 128 * rank);
-                const int32_t sa0 = (int32_t)(t.atom_row + rank), sb0 = (int32_t)(t.n0 / 128);
-                for (int k = 0; k < P.k_steps; ++k) {
-                    if (!wait_bar(&empty[s], ph ^ 1, g, SITE_PRODUCER_EMPTY)) {
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* a = smem + s * Cfg::STAGE_BYTES;
-                    uint8_t* b = a + Cfg::A_BYTES;
-                    uint8_t* sa = b + Cfg::B_BYTES;
-                    uint8_t* sb = sa + Cfg::SA_BYTES;
-                    const int32_t kx = k * 128, sx = k * (int32_t)(Cfg::SA_BYTES / 8);
-                    const uint32_t bar = leader ? smem_u32(&full[s]) : mapa_shared(smem_u32(&full[s]), 0);
+            const int32_t a0 = (int32_t)(t.row0 + 128 * rank), b0 = (int32_t)(t.n0 + 128 * rank);
+            const int32_t sa0 = (int32_t)(t.atom_row + rank), sb0 = (int32_t)(t.n0 / 128);
+            int32_t kx = 0, sx = 0;
+            for (int k = 0; k < P.k_steps; ++k) {
+                ok = __all_sync(0xFFFFFFFFu, wait_bar(&empty[s], ph ^ 1, g, SITE_PRODUCER_EMPTY));
+                if (!ok) break;
+                uint8_t* a = smem + (uint32_t)s * Cfg::STAGE_BYTES;
+                uint8_t* b = a + Cfg::A_BYTES;
+                uint8_t* sa = b + Cfg::B_BYTES;
+                uint8_t* sb = sa + Cfg::SA_BYTES;
+                const uint32_t bar = l_full + 8u * s;
+                armed |= 1u << s;
+                armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                if (elect_one()) {
                     if (leader) mbar_arrive_expect_tx(&full[s], 2 * (Cfg::A_BYTES + Cfg::B_BYTES));
                     mbar_arrive_expect_tx(&sfull[s], Cfg::SA_BYTES + Cfg::SB_BYTES);
-                    armed |= 1u << s;
-                    armed_par = (armed_par & ~(1u << s)) | (ph << s);
                     tma_load_2d(sa, &tmSA, &sfull[s], sx, sa0);
-                    if (P.b3d)
+                    if (P.b3d) {
                         tma_load_3d(sb, &tmSB, &sfull[s], sx, sb0, t.expert);
-                    else
-                        tma_load_2d(sb, &tmSB, &sfull[s], sx, sb0);
-                    tma_load_2d_pair(a, &tmA, bar, kx, a0);
-                    if (P.b3d)
                         tma_load_3d_pair(b, &tmB, bar, kx, b0, t.expert);
-                    else
+                    } else {
+                        tma_load_2d(sb, &tmSB, &sfull[s], sx, sb0);
                         tma_load_2d_pair(b, &tmB, bar, kx, b0);
-                    if (++s == S) {
-                        s = 0;
-                        ph ^= 1;
                     }
+                    tma_load_2d_pair(a, &tmA, bar, kx, a0);
+                }
+                __syncwarp();
+                kx += 128;
+                sx += (int32_t)(Cfg::SA_BYTES / 8);
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1;
                 }
             }
-            ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
         }
         if (lane == 0) {
             // never leave with copies in flight into this CTA's shared memory
@@ -197,52 +197,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_PAIR_THREADS, 1)
         __syncwarp();
     } else if (warp == 1 && leader) {
         // ---------------- MMAs (even CTA) ----------------
+        const uint64_t ad0 = make_sw128_kmajor_desc(smem_u32(smem));
+        const uint64_t bd0 = make_sw128_kmajor_desc(smem_u32(smem) + Cfg::A_BYTES);
         int s = 0;
         uint32_t ph = 0, it = 0;
         bool ok = true, issued = false;
         MxTile t;
         for (int64_t i = pid; ok && mx_pair_tile(P, blocks, i, lane, t); i += P.programs, ++it) {
-            if (lane == 0) {
-                // the accumulator's previous tile is in the epilogue's registers
-                ok = wait_bar_cluster(tempty, (it & 1) ^ 1, g, SITE_MMA_TMEM_EMPTY);
+            // the accumulator's previous tile is in the epilogue's registers
+            ok = __all_sync(0xFFFFFFFFu, wait_bar_cluster(tempty, (it & 1) ^ 1, g, SITE_MMA_TMEM_EMPTY));
+            tc_fence_after_sync();
+            for (int k = 0; ok && k < P.k_steps; ++k) {
+                // the leader's scale warps have seen both CTAs' operands land before they arrive
+                ok = __all_sync(0xFFFFFFFFu, wait_bar_cluster(&sready[s], ph, g, SITE_MMA_OPERAND));
+                if (!ok) break;
                 tc_fence_after_sync();
-                for (int k = 0; ok && k < P.k_steps; ++k) {
-                    if (!wait_bar(&full[s], ph, g, SITE_MMA_FULL) ||
-                        !wait_bar_cluster(&sready[s], ph, g, SITE_MMA_OPERAND)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after_sync();
-                    const uint32_t a = smem_u32(smem + s * Cfg::STAGE_BYTES);
-                    const uint32_t b = a + Cfg::A_BYTES;
-                    const uint32_t ta = tmem + Cfg::BN + s * Cfg::SCALE_COLS, tb = ta + 4 * Cfg::S_ATOMS;
-                    // always four: past K's end codes and scales are zeros (a bound
-                    // tested per instruction cost the issuing thread 8% of the loop)
-                    const uint64_t ad = make_sw128_kmajor_desc(a), bd = make_sw128_kmajor_desc(b);
+                const uint64_t ad = ad0 + (uint64_t)((uint32_t)s * (Cfg::STAGE_BYTES / 16));
+                const uint64_t bd = bd0 + (uint64_t)((uint32_t)s * (Cfg::STAGE_BYTES / 16));
+                const uint32_t ta = tmem + Cfg::BN + (uint32_t)s * Cfg::SCALE_COLS, tb = ta + 4 * Cfg::S_ATOMS;
+                const uint32_t acc = k > 0 ? 1u : 0u;
+                if (elect_one()) {
+                    // always four: past K's end codes and scales are zeros
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const uint32_t acc = (k > 0 || q > 0) ? 1u : 0u;
                         if constexpr (NVF4) {
-                            umma_mx_ss_pair<true>(tmem, ad + 2 * q, bd + 2 * q, P.idesc, ta + 4 * q, tb + 8 * q, acc);
+                            umma_mx_ss_pair<true>(tmem, ad + 2 * q, bd + 2 * q, P.idesc, ta + 4 * q, tb + 8 * q, q ? 1u : acc);
                         } else {
                             const uint32_t id = (q & 1) * 2u;
                             umma_mx_ss_pair<false>(tmem, ad + 2 * q, bd + 2 * q, P.idesc | (id << 29) | (id << 4),
-                                                   ta + 4 * (q / 2), tb + 8 * (q / 2), acc);
+                                                   ta + 4 * (q / 2), tb + 8 * (q / 2), q ? 1u : acc);
                         }
                     }
-                    issued = true;
                     umma_commit_pair_mc(&empty[s], 0x3);
-                    if (++s == S) {
-                        s = 0;
-                        ph ^= 1;
-                    }
+                    if (k == P.k_steps - 1) umma_commit_pair_mc(tfull, 0x3);
                 }
-                if (ok) umma_commit_pair_mc(tfull, 0x3);
+                __syncwarp();
+                issued = true;
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1;
+                }
             }
-            ok = __shfl_sync(0xFFFFFFFFu, ok ? 1 : 0, 0) != 0;
         }
-        if (lane == 0 && issued) {  // every issued MMA has finished before TMEM is freed
-            umma_commit_pair_mc(done, 0x1);
+        if (issued) {  // every issued MMA has finished before TMEM is freed
+            if (elect_one()) umma_commit_pair_mc(done, 0x1);
+            __syncwarp();
             wait_bar_drain(done, 0, g);
         }
         __syncwarp();
@@ -258,8 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_PAIR_THREADS, 1)
             for (int k = 0; k < P.k_steps; ++k) {
                 // the scales are there; the buffer's previous readers are done (the
                 // producer has waited for the same phase of empty[s])
-                ok = __all_sync(0xFFFFFFFFu, wait_bar(&sfull[s], ph, g, SITE_DQ_RAW) &&
-                                                 wait_bar(&empty[s], ph ^ 1, g, SITE_DQ_EMPTY));
+                ok = __all_sync(0xFFFFFFFFu, wait_bar(&sfull[s], ph, g, SITE_DQ_RAW));
                 if (!ok) break;
                 tc_fence_after_sync();
                 const uint8_t* sa = smem + s * Cfg::STAGE_BYTES + Cfg::A_BYTES + Cfg::B_BYTES + lane * 16;
@@ -279,9 +277,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_PAIR_THREADS, 1)
                 tmem_st_32x32b(ta, ra);
                 tmem_st_32x32b(ta + 4 * Cfg::S_ATOMS, rb);
                 tmem_st_wait();
+                if (leader) {
+                    ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[s], ph, g, SITE_MMA_FULL));
+                    if (!ok) break;
+                }
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote_tmem(l_sready + 8u * s);
+                if (lane == 0) {
+                    if (leader)
+                        mbar_arrive(&sready[s]);  // (a release: what full[s] showed this warp, the MMA thread sees)
+                    else
+                        mbar_arrive_remote_relaxed(l_sready + 8u * s);
+                }
                 if (++s == S) {
                     s = 0;
                     ph ^= 1;
@@ -325,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_PAIR_THREADS, 1)
                 });
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote_tmem(l_tempty);
+                if (lane == 0) mbar_arrive_remote_relaxed(l_tempty);
                 uint16_t* d = static_cast<uint16_t*>(P.epi.D) + m0 * P.epi.ldd + n0;
                 mx_store64(buf, d, P.epi.ldd, rows, lane);
                 __syncwarp();
@@ -346,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_PAIR_THREADS, 1)
             }
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote_tmem(l_tempty);
+            if (lane == 0) mbar_arrive_remote_relaxed(l_tempty);
         }
     }
     tc_fence_before_sync();

@@ -24,6 +24,16 @@ __device__ __forceinline__ uint32_t lane_id() {
     return l;
 }
 
+// True in one lane of a converged warp.  Loops that issue copies or MMAs run in
+// the whole warp and elect a lane around the instructions themselves: addresses
+// and descriptors then stay in uniform registers, which those instructions
+// read, where a lane of its own would move them there one by one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+    return p != 0;
+}
+
 // ---- mbarrier ----------------------------------------------------------------
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
@@ -267,12 +277,6 @@ __device__ __forceinline__ void umma_mx_ss(uint32_t d_tmem, uint64_t a_desc, uin
             : "memory");
 }
 
-// Copy one scale atom (32 rows of 16 bytes, 512 bytes of shared memory) into
-// four TMEM columns, repeated in each of the four 32-lane quarters.
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
-
 // Arrive once on `bar` when every tcgen05 operation issued so far by this
 // thread has completed.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
@@ -352,11 +356,11 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// The same without the release: for handing over TMEM, whose accesses the
-// caller has completed (tcgen05.wait) and fenced (tc_fence_before_sync), when no
-// other memory is published.  The release at cluster scope costs about a
-// microsecond per arrival.
-__device__ __forceinline__ void mbar_arrive_remote_tmem(uint32_t cluster_addr) {
+// The same without the release, for arrivals that publish no ordinary memory:
+// TMEM handed over (its accesses completed by tcgen05.wait and fenced by
+// tc_fence_before_sync), or shared memory that the caller has done with.  The
+// release at cluster scope costs about a microsecond per arrival.
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
@@ -457,16 +461,6 @@ __device__ __forceinline__ uint64_t make_sw128_kmajor_desc(uint32_t smem_addr) {
     d |= (uint64_t)(1024u >> 4) << 32;
     d |= (uint64_t)1u << 46;
     d |= (uint64_t)2u << 61;
-    return d;
-}
-
-// Descriptor of one scale atom for tmem_cp_scales: 8-row groups of 16-byte
-// rows (128 bytes) one after another, no swizzle.
-__device__ __forceinline__ uint64_t make_scale_desc(uint32_t smem_addr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(128u >> 4) << 32;
-    d |= (uint64_t)1u << 46;
     return d;
 }
 
