@@ -16,11 +16,17 @@
 
 using namespace qg;
 
-static_assert(GEMM_MXFP4 == MXF_MXFP4 && GEMM_NVFP4 == MXF_NVFP4, "the C ABI's format codes are the kernels' codes");
+static_assert((int)GEMM_MXFP4 == (int)MXF_MXFP4 && (int)GEMM_NVFP4 == (int)MXF_NVFP4,
+              "the C ABI's format codes are the kernels' codes");
 
 namespace {
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+// How rows may be moved: 2 in 32-byte pieces, 1 in 16-byte ones, 0 by element.
+int row_alignment(const void* p, int64_t ld, int64_t element) {
+    if (!p) return 2;
+    return aligned(p, 32) && ld * element % 32 == 0 ? 2 : aligned(p, 16) && ld * element % 16 == 0 ? 1 : 0;
+}
 bool known_format(int32_t f) { return f == GEMM_MXFP4 || f == GEMM_NVFP4; }
 int64_t float_size(int32_t t) { return t == GEMM_F32 ? 4 : (t == GEMM_F16 || t == GEMM_BF16) ? 2 : 0; }
 
@@ -84,7 +90,7 @@ int quant_params(gemm_handle_t h, int32_t format, float g, const gemm_layout_t* 
     if (!tensor_scale_ok(format, g)) return GEMM_ERR_INVALID_ARG;
     if ((rc = check_experts(h, offsets, experts))) return rc;
     if (experts && v->num != 1) return GEMM_ERR_INVALID_ARG;
-    if (v->cols > QUANT_MAX_COLS || v->num > 65535) return GEMM_ERR_UNSUPPORTED;
+    if (v->rows > INT32_MAX - 64 || v->cols > QUANT_MAX_COLS || v->num > 65535) return GEMM_ERR_UNSUPPORTED;
     const int64_t need = scale_bytes(format, v->rows, v->cols, experts);
     memset(p, 0, sizeof *p);
     p->rows = v->rows;
@@ -103,9 +109,9 @@ int quant_params(gemm_handle_t h, int32_t format, float g, const gemm_layout_t* 
     p->num = v->num;
     p->type = v->type;
     p->format = format;
-    p->vec = aligned(vals, 16) && v->ld * es % 16 == 0 && p->x_bstride * es % 16 == 0;
-    p->tensor_scale = g;
-    p->six_g = 6.0f * g;
+    p->vec = std::min(row_alignment(vals, v->ld, es), row_alignment(vals, p->x_bstride, es));
+    p->atoms = (int32_t)mx_atoms(format, v->cols);
+    p->c = mx_scale_const(g);
     p->offsets = offsets;
     p->num_experts = experts;
     return GEMM_OK;
@@ -269,30 +275,69 @@ bool forced_kernel(MxChoice* c) {
     return true;
 }
 
-MxChoice choose(const MxProduct& p, int sm_count, int clusters, int forced_split) {
-    MxChoice c{128, 1, 0};
-    const bool forced = forced_kernel(&c);
-    if (!forced && !forced_split && p.M > 128 && clusters > 0 &&
-        tiles_along_m(p, 256) * ceil_div(p.N, 256) * 2 >= clusters)
-        c.pair = 1;
-    if (c.pair) {
-        c.bn = 256;
-        return c;
-    }
+// Estimated time of a choice, microseconds.  Measured on GB300 (152 SMs),
+// back-to-back launches:
+//   one-tile kernel  2.5 us for launch, first data and exit (1x64x64), 0.30 us (64
+//     columns) or 0.33 (128) a K-step of 256 while the issuing warp is the bound, else the bytes of the
+//     stages of the CTAs that share an SM at 132 bytes a nanosecond; 1.2 us for
+//     every further wave of CTAs, 0.25 us for every CTA on an SM; K slices: 1.4 us
+//     and 0.025 us a row of a 64-column tile (1x4096x4096: 7.5 us whole, 6.3 in
+//     two, 5.9 in four; 128x4096x4096: 8.0 whole, 9.6 in two)
+//   CTA pair         3.9 us, 0.37 us a K-step, 0.42 when every cluster is busy
+//     (512x4096x4096: 10.5 us against 9.4 in 64-column tiles; 1024x4096x4096:
+//     11.3 against 18; 4096^3: 32 against 65)
+// No choice takes less than its operands at 6.5 TB/s; among choices that memory
+// bounds, the one with less else to do is ahead.
+double estimate(const MxProduct& p, int sm_count, int clusters, const MxChoice& c) {
     const int64_t steps = ceil_div(p.K, MX_KSTEP);
-    const int64_t slots = 2 * (int64_t)sm_count;  // CTAs resident at once
-    if (!forced && (tiles_along_m(p, 128) * ceil_div(p.N, 128) * 8 <= slots || p.N <= 64)) c.bn = 64;
-    const int64_t tiles = tiles_along_m(p, 128) * ceil_div(p.N, c.bn);
-    const int want = forced_split ? forced_split : 8;
-    while (c.splits * 2 <= want && c.splits * 2 <= steps && (forced_split || tiles * c.splits * 2 <= slots)) c.splits *= 2;
-    const int a_rows = rows_staged(p);
-    while (c.splits > 1 && !mx_gemm_stages(c.bn, p.format, a_rows, c.splits)) {
-        if (c.bn == 128 && !forced)
-            c.bn = 64;
-        else
-            c.splits /= 2;
+    const double bytes = 0.56 * (double)p.K * ((double)p.M + (double)p.N * (p.experts ? std::min<int64_t>(p.experts, p.M) : 1));
+    const double memory = 2.5 + bytes / 6.5e6;
+    if (c.pair) {
+        const int64_t tiles = tiles_along_m(p, 256) * ceil_div(p.N, 256);
+        const double waves = (double)ceil_div(tiles, clusters);
+        const double own = 3.9 + waves * steps * (tiles < clusters ? 0.37 : 0.42);
+        return std::max(memory, own) + 0.2 * own;
     }
-    return c;
+    const int a_rows = rows_staged(p);
+    const int64_t ctas = tiles_along_m(p, 128) * ceil_div(p.N, c.bn) * c.splits;
+    const double stage = 128.0 * (a_rows + c.bn) + (p.format == GEMM_NVFP4 ? 4096 : 2048);
+    const double step = std::max(c.bn == 64 ? 0.30 : 0.33, (ctas > sm_count ? 2 : 1) * stage / 132e3);
+    const double waves = (double)ceil_div(ctas, 2 * (int64_t)sm_count);
+    const double rows = (double)std::min<int64_t>(p.M, 128);
+    const double tail = (c.splits > 1 ? 1.4 + 0.025 * rows * c.bn / 64 : 0.0) + 0.25 * ceil_div(ctas, sm_count);
+    const double own = 1.3 + waves * (1.2 + ceil_div(steps, c.splits) * step);
+    return std::max(memory, own) + 0.2 * own + tail;
+}
+
+MxChoice choose(const MxProduct& p, int sm_count, int clusters, int forced_split) {
+    const int64_t steps = ceil_div(p.K, MX_KSTEP);
+    const int a_rows = rows_staged(p);
+    MxChoice forced{0, 1, 0}, best{64, 1, 0};
+    const bool pinned = forced_kernel(&forced);
+    double best_us = -1.0;
+    for (int bn : {64, 128}) {
+        if (pinned && (forced.pair || forced.bn != bn)) continue;
+        for (int splits : {1, 2, 4, 8}) {
+            if (forced_split && splits != std::min(forced_split, 8)) {
+                // a forced count is cut down to what K and shared memory allow
+                const bool cut = splits < forced_split &&
+                                 (2 * splits > steps || !mx_gemm_stages(bn, p.format, a_rows, 2 * splits));
+                if (!cut) continue;
+            }
+            if (splits > steps || !mx_gemm_stages(bn, p.format, a_rows, splits)) continue;
+            const MxChoice c{bn, splits, 0};
+            const double us = estimate(p, sm_count, clusters, c);
+            if (best_us < 0 || us < best_us) {
+                best_us = us;
+                best = c;
+            }
+        }
+    }
+    if (clusters > 0 && (pinned ? forced.pair != 0 : !forced_split && p.M > 128)) {
+        const MxChoice c{256, 1, 1};
+        if (pinned || estimate(p, sm_count, clusters, c) < best_us) best = c;
+    }
+    return best;
 }
 
 int run_product(gemm_handle_t h, const gemm_op_t* op, MxProduct& p, cudaStream_t st) {
@@ -306,7 +351,6 @@ int run_product(gemm_handle_t h, const gemm_op_t* op, MxProduct& p, cudaStream_t
     }
     const int clusters = pair_clusters(h, p.format);
     const MxChoice c = choose(p, handle_sm_count(h), clusters, op->splitk);
-    if (c.pair && clusters < 1) return GEMM_ERR_NO_KERNEL;
     MxGemmParams k;
     memset(&k, 0, sizeof k);
     k.epi = p.epi;
@@ -480,14 +524,13 @@ int gemm_mx_norm_quantize(gemm_handle_t h, const gemm_mx_norm_t* op, const void*
         p.ldq = Qdesc->ld / 2;
         p.type = Rdesc->type;
         p.format = op->format;
-        auto rows16 = [&](const void* ptr, int64_t ld, int64_t n) { return !ptr || (aligned(ptr, 16) && ld * n % 16 == 0); };
-        p.vec = rows16(F, p.ldf, es) && rows16(R, p.ldr, es) && rows16(O, p.ldo, es);
-        p.wvec = rows16(op->post_weight, 0, ws) && rows16(op->pre_weight, 0, ws);
-        p.gvec = rows16(op->gate, op->gate_ld, gs);
+        p.vec = std::min({row_alignment(F, p.ldf, es), row_alignment(R, p.ldr, es), row_alignment(O, p.ldo, es)});
+        p.wvec = std::min(row_alignment(op->post_weight, 0, ws), row_alignment(op->pre_weight, 0, ws));
+        p.gvec = row_alignment(op->gate, op->gate_ld, gs);
+        p.atoms = (int32_t)mx_atoms(op->format, cols);
         p.eps = op->eps;
         p.residual_scale = op->residual_scale;
-        p.tensor_scale = op->tensor_scale;
-        p.six_g = 6.0f * op->tensor_scale;
+        p.c = mx_scale_const(op->tensor_scale);
         p.post = op->post_weight;
         p.pre = op->pre_weight;
         p.gate = op->gate;

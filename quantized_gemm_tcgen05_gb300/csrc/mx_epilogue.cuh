@@ -142,10 +142,15 @@ __device__ __forceinline__ void mx_store_block_t(const EpiParams& ep, bool vec32
     const int64_t n = n0 + lane;
     if (n < e.N) {
         const float b = ACT >= 0 ? bias_at(ar, n) : 0.0f;
-        for (int r = 0; r < rows; ++r) {
-            const int64_t i = (m0 + r) * e.ldd + n;
-            const float c = use_c ? ld_elem(e.C, DT, (m0 + r) * e.ldc + n) : 0.0f;
-            st_elem(e.D, DT, i, epi_value<ACT>(ar, stage[r * 33 + lane], c, b));
+        for (int r0 = 0; r0 < rows; r0 += 8) {  // eight rows' C in flight together
+            float c[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                c[j] = use_c && r0 + j < rows ? ld_elem(e.C, DT, (m0 + r0 + j) * e.ldc + n) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (r0 + j < rows)
+                    st_elem(e.D, DT, (m0 + r0 + j) * e.ldd + n, epi_value<ACT>(ar, stage[(r0 + j) * 33 + lane], c[j], b));
         }
     }
     __syncwarp();

@@ -23,6 +23,12 @@ QG_HD int64_t mx_scale_at(int64_t r, int64_t b, int64_t atoms) {
     return ((r / MX_ATOM_ROWS) * atoms + b / 4) * MX_ATOM_BYTES + (r % 32) * 16 + (r % MX_ATOM_ROWS) / 32 * 4 + b % 4;
 }
 
+// Constants of a launch: g, RN(6 g) and its reciprocal, rounded.
+struct MxScaleConst {
+    float g, six_g, inv_six_g;
+};
+inline MxScaleConst mx_scale_const(float g) { return MxScaleConst{g, 6.0f * g, 1.0f / (6.0f * g)}; }
+
 // Quantisation and its inverse: one matrix of `rows` x `cols`, or `num` of them.
 struct MxQuantParams {
     const void* X;  // values in (quantise); codes in (dequantise)
@@ -35,9 +41,9 @@ struct MxQuantParams {
     int32_t num;
     int32_t type;            // of the values (DType)
     int32_t format;
-    int32_t vec;             // values: base and rows 16-byte aligned
-    float tensor_scale;      // g
-    float six_g;             // RN(6 g)
+    int32_t vec;             // values: base and rows 32-byte (2) or 16-byte (1) aligned, or neither (0)
+    int32_t atoms;           // scale atoms of a row
+    MxScaleConst c;
     const int32_t* offsets;  // rows sorted by expert: device int32[num_experts + 1], or null
     int32_t num_experts;
 };
@@ -48,12 +54,14 @@ struct MxNormParams {
     uint8_t *Q, *S;
     int64_t rows, cols, ldf, ldr, ldo, ldq;  // ldq in bytes
     int32_t type, format;
-    int32_t vec;  // F, R, O: bases and rows 16-byte aligned
-    float eps, residual_scale, tensor_scale, six_g;
+    int32_t vec;    // F, R, O: as in MxQuantParams
+    int32_t atoms;  // scale atoms of a row
+    float eps, residual_scale;
+    MxScaleConst c;
     const void *post, *pre, *gate;
     int32_t weight_type, gate_type;
     int64_t gate_ld;
-    int32_t wvec, gvec;  // weights / gate 16-byte aligned
+    int32_t wvec, gvec;  // weights, gate: likewise
 };
 
 cudaError_t launch_mx_quantize(const MxQuantParams& p, cudaStream_t st);

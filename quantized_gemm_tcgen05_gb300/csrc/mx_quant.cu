@@ -13,29 +13,36 @@ namespace qg {
 
 namespace {
 
-constexpr int QWARPS = 8;  // rows per block
+constexpr int QWARPS = 8;  // warps of a block
+constexpr int QROWS = 2;   // rows a warp takes, so that its address arithmetic and
+                           // its launch are paid for twice as many bytes
 
 template <typename T, bool NVF4>
 __global__ void __launch_bounds__(32 * QWARPS) mx_quantize_kernel(const __grid_constant__ MxQuantParams p) {
     griddep_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t r = (int64_t)blockIdx.x * QWARPS + warp;
-    if (r >= p.rows) return;
-    const int64_t chunk = (int64_t)blockIdx.y * 32 + lane;
-    const int64_t atoms = mx_atoms(NVF4 ? MXF_NVFP4 : MXF_MXFP4, p.cols);
-    const int64_t chunk_end = atoms * (NVF4 ? 4 : 8);
+    const int r0 = (int)blockIdx.x * (QWARPS * QROWS) + warp;  // then QWARPS further
+    const int chunk = (int)blockIdx.y * 32 + lane, cols = (int)p.cols;
+    const int chunk_end = p.atoms * (NVF4 ? 4 : 8);
+    if (r0 >= p.rows) return;
     griddep_wait();
-    const int64_t srow = p.offsets ? mx_expert_row(p.offsets, p.num_experts, r, lane) : r;
-    if (srow < 0) return;
-    const T* row = static_cast<const T*>(p.X) + blockIdx.z * p.x_bstride + r * p.ldx;
-    float v[16];
-    mx_load16(row, chunk * 16, p.cols, p.vec, v);
-    uint2 codes;
-    const uint32_t byte = mx_quantize16<NVF4>(v, p.tensor_scale, p.six_g, codes);
-    mx_store_codes(static_cast<uint8_t*>(p.Y) + blockIdx.z * p.q_bstride + r * p.ldq, chunk * 16, p.cols, codes);
-    // blocks past the row's end are padding: zero, whatever an empty block's scale would be
-    const bool pad = (NVF4 ? chunk * 16 : chunk / 2 * 32) >= p.cols;
-    mx_store_scales<NVF4>(p.S + blockIdx.z * p.s_bstride, srow, chunk, chunk_end, atoms, pad ? 0u : byte, lane);
+    Raw16<T> raw[QROWS];
+#pragma unroll
+    for (int j = 0; j < QROWS; ++j)
+        if (r0 + j * QWARPS < p.rows)
+            raw[j] = mx_load16(static_cast<const T*>(p.X) + blockIdx.z * p.x_bstride + (r0 + j * QWARPS) * p.ldx, chunk * 16,
+                               cols, p.vec);
+#pragma unroll
+    for (int j = 0; j < QROWS; ++j) {
+        const int r = r0 + j * QWARPS;
+        if (r >= p.rows) break;
+        const int64_t srow = p.offsets ? mx_expert_row(p.offsets, p.num_experts, r, lane) : r;
+        if (srow < 0) continue;
+        uint2 codes;
+        const uint32_t byte = mx_quantize16<NVF4>(mx_values<T>(raw[j]), p.c, codes);
+        mx_store_codes(static_cast<uint8_t*>(p.Y) + blockIdx.z * p.q_bstride + r * p.ldq, chunk * 16, cols, codes);
+        mx_store_scales<NVF4>(p.S + blockIdx.z * p.s_bstride + mx_scale_row_at(srow, p.atoms), chunk, chunk_end, cols, byte, lane);
+    }
 }
 
 // E2M1 codes as E4M3 bytes: the magnitude by a byte permute over the eight of
@@ -54,55 +61,81 @@ __device__ __forceinline__ float2 mx_code_pair(uint32_t byte) {
 
 struct E4M3Out {};  // the codes' own values
 
+// 16 bytes of codes a thread: 32 values.
 template <typename T, bool NVF4>
 __global__ void __launch_bounds__(32 * QWARPS) mx_dequantize_kernel(const __grid_constant__ MxQuantParams p) {
     griddep_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t r = (int64_t)blockIdx.x * QWARPS + warp;
-    if (r >= p.rows) return;
-    const int64_t c0 = ((int64_t)blockIdx.y * 32 + lane) * 16;
+    const int r0 = (int)blockIdx.x * (QWARPS * QROWS) + warp;
+    const int c0 = ((int)blockIdx.y * 32 + lane) * 32, cols = (int)p.cols;
+    if (r0 >= p.rows) return;
     griddep_wait();
-    const int64_t srow = p.offsets ? mx_expert_row(p.offsets, p.num_experts, r, lane) : r;
-    if (srow < 0 || c0 >= p.cols) return;
-    const uint8_t* q = static_cast<const uint8_t*>(p.X) + blockIdx.z * p.q_bstride + r * p.ldq + c0 / 2;
-    uint2 codes = make_uint2(0, 0);
-    if (c0 + 16 <= p.cols) {
-        codes = __ldg(reinterpret_cast<const uint2*>(q));
-    } else {
-        const int64_t n = (p.cols - c0 + 1) / 2;
-        for (int i = 0; i < 8; ++i)
-            if (i < n) (i < 4 ? codes.x : codes.y) |= (uint32_t)q[i] << (8 * (i % 4));
-    }
-    if constexpr (std::is_same<T, E4M3Out>::value) {
-        uint8_t* out = static_cast<uint8_t*>(p.Y) + blockIdx.z * p.x_bstride + r * p.ldx + c0;
-        const uint32_t w[4] = {mx_codes_e4m3(codes.x), mx_codes_e4m3(codes.x >> 16), mx_codes_e4m3(codes.y),
-                               mx_codes_e4m3(codes.y >> 16)};
-        if (p.vec && c0 + 16 <= p.cols) {
-            *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+    uint32_t w[QROWS][4];
+#pragma unroll
+    for (int j = 0; j < QROWS; ++j) {
+        const uint8_t* q = static_cast<const uint8_t*>(p.X) + blockIdx.z * p.q_bstride + (r0 + j * QWARPS) * p.ldq + c0 / 2;
+        w[j][0] = w[j][1] = w[j][2] = w[j][3] = 0;
+        if (r0 + j * QWARPS >= p.rows) continue;
+        if (c0 + 32 <= cols) {
+            const uint4 u = *reinterpret_cast<const uint4*>(q);
+            w[j][0] = u.x;
+            w[j][1] = u.y;
+            w[j][2] = u.z;
+            w[j][3] = u.w;
         } else {
+            const int n = (cols - c0 + 1) / 2;
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                if (c0 + i < p.cols) out[i] = (uint8_t)(w[i / 4] >> (8 * (i % 4)));
+                if (i < n) w[j][i / 4] |= (uint32_t)q[i] << (8 * (i % 4));
         }
-    } else {
-        const int64_t atoms = mx_atoms(NVF4 ? MXF_NVFP4 : MXF_MXFP4, p.cols);
-        const float s = mx_scale_value<NVF4>(
-            p.S[blockIdx.z * p.s_bstride + mx_scale_at(srow, c0 / (NVF4 ? 16 : 32), atoms)]);
-        float v[16];
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 f = mx_code_pair(((i < 4 ? codes.x : codes.y) >> (8 * (i % 4))) & 0xFFu);
-            // code * scale is exact (2 + 4 significant bits); the product with g is rounded, then D
-            v[2 * i] = f.x * s * p.tensor_scale;
-            v[2 * i + 1] = f.y * s * p.tensor_scale;
+    for (int j = 0; j < QROWS; ++j) {
+        const int r = r0 + j * QWARPS;
+        if (r >= p.rows) break;
+        const int64_t srow = p.offsets ? mx_expert_row(p.offsets, p.num_experts, r, lane) : r;
+        if (srow < 0 || c0 >= cols) continue;
+        if constexpr (std::is_same<T, E4M3Out>::value) {
+            uint8_t* out = static_cast<uint8_t*>(p.Y) + blockIdx.z * p.x_bstride + r * p.ldx + c0;
+            uint32_t v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = mx_codes_e4m3(w[j][i / 2] >> (16 * (i % 2)));
+            if (p.vec == 2 && c0 + 32 <= cols) {
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "r"(v[0]), "r"(v[1]),
+                             "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                             : "memory");
+            } else if (p.vec && c0 + 32 <= cols) {
+                *reinterpret_cast<uint4*>(out) = make_uint4(v[0], v[1], v[2], v[3]);
+                *reinterpret_cast<uint4*>(out + 16) = make_uint4(v[4], v[5], v[6], v[7]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (c0 + i < cols) out[i] = (uint8_t)(v[i / 4] >> (8 * (i % 4)));
+            }
+        } else {
+            const uint8_t* sp = p.S + blockIdx.z * p.s_bstride + mx_scale_row_at(srow, p.atoms);
+            T* out = static_cast<T*>(p.Y) + blockIdx.z * p.x_bstride + r * p.ldx;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int ch = c0 + 16 * h;
+                if (ch >= cols) break;
+                const float s = mx_scale_value<NVF4>(sp[mx_block_at(ch / (NVF4 ? 16 : 32))]);
+                Row16 v;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float2 f = mx_code_pair((w[j][2 * h + i / 4] >> (8 * (i % 4))) & 0xFFu);
+                    // code * scale is exact (2 + 4 significant bits); the product with g is rounded, then D
+                    v.p[i] = pack2(f.x * s * p.c.g, f.y * s * p.c.g);
+                }
+                mx_store16(out, ch, cols, p.vec, mx_round<T>(v));
+            }
         }
-        mx_store16(static_cast<T*>(p.Y) + blockIdx.z * p.x_bstride + r * p.ldx, c0, p.cols, p.vec, v);
     }
 }
 
 template <typename F>
 cudaError_t mx_launch(F kernel, const MxQuantParams& p, int64_t chunks, cudaStream_t st) {
-    const int64_t gx = ceil_div(p.rows, QWARPS), gy = ceil_div(chunks, 32);
+    const int64_t gx = ceil_div(p.rows, QWARPS * QROWS), gy = ceil_div(chunks, 32);
     if (gx > INT32_MAX || gy > 65535 || p.num > 65535) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
@@ -121,7 +154,7 @@ cudaError_t mx_launch(F kernel, const MxQuantParams& p, int64_t chunks, cudaStre
 
 cudaError_t launch_mx_quantize(const MxQuantParams& p, cudaStream_t st) {
     const bool nv = p.format == MXF_NVFP4;
-    const int64_t chunks = mx_atoms(p.format, p.cols) * (nv ? 4 : 8);
+    const int64_t chunks = (int64_t)p.atoms * (nv ? 4 : 8);
     switch (p.type) {
         case DT_F32: return nv ? mx_launch(mx_quantize_kernel<float, true>, p, chunks, st) : mx_launch(mx_quantize_kernel<float, false>, p, chunks, st);
         case DT_F16: return nv ? mx_launch(mx_quantize_kernel<__half, true>, p, chunks, st) : mx_launch(mx_quantize_kernel<__half, false>, p, chunks, st);
@@ -132,7 +165,7 @@ cudaError_t launch_mx_quantize(const MxQuantParams& p, cudaStream_t st) {
 
 cudaError_t launch_mx_dequantize(const MxQuantParams& p, cudaStream_t st) {
     const bool nv = p.format == MXF_NVFP4;
-    const int64_t chunks = ceil_div(p.cols, 16);
+    const int64_t chunks = ceil_div(p.cols, 32);
     switch (p.type) {
         case DT_F32: return nv ? mx_launch(mx_dequantize_kernel<float, true>, p, chunks, st) : mx_launch(mx_dequantize_kernel<float, false>, p, chunks, st);
         case DT_F16: return nv ? mx_launch(mx_dequantize_kernel<__half, true>, p, chunks, st) : mx_launch(mx_dequantize_kernel<__half, false>, p, chunks, st);
@@ -161,14 +194,19 @@ __device__ __forceinline__ float mx_block_sum(float x, float* red) {
     return s;
 }
 
-__device__ __forceinline__ void mx_load16_any(const void* p, int32_t type, int64_t at, int64_t c0, int64_t cols,
-                                              bool vec, float (&v)[16]) {
-    if (type == DT_F32)
-        mx_load16(static_cast<const float*>(p) + at, c0, cols, vec, v);
-    else if (type == DT_F16)
-        mx_load16(static_cast<const __half*>(p) + at, c0, cols, vec, v);
-    else
-        mx_load16(static_cast<const __nv_bfloat16*>(p) + at, c0, cols, vec, v);
+__device__ __forceinline__ Row16 mx_load16_any(const void* p, int32_t type, int64_t at, int c0, int cols, int vec) {
+    if (type == DT_F32) return mx_values<float>(mx_load16(static_cast<const float*>(p) + at, c0, cols, vec));
+    if (type == DT_F16) return mx_values<__half>(mx_load16(static_cast<const __half*>(p) + at, c0, cols, vec));
+    return mx_values<__nv_bfloat16>(mx_load16(static_cast<const __nv_bfloat16*>(p) + at, c0, cols, vec));
+}
+
+__device__ __forceinline__ float mx_sum_squares(const Row16& v, float ss) {
+    uint64_t a = pack2(ss, 0.0f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) a = fma2(v.p[j], v.p[j], a);
+    float x, y;
+    unpack2(a, x, y);
+    return x + y;
 }
 
 // A block per row; the row stays in registers between the two norms, NC
@@ -177,79 +215,95 @@ __device__ __forceinline__ void mx_load16_any(const void* p, int32_t type, int64
 // over the block.  Bounded by HBM when there are many rows, by the two block
 // sums' latency when there are few.
 template <typename T, bool NVF4, int NC>
-__global__ void __launch_bounds__(NC == 1 ? 256 : 512) mx_norm_kernel(const __grid_constant__ MxNormParams p) {
+__global__ void __launch_bounds__(NC == 1 ? 256 : 512, NC == 1 ? 4 : 1) mx_norm_kernel(const __grid_constant__ MxNormParams p) {
     __shared__ float red[32];
     griddep_launch_dependents();
     const int64_t r = blockIdx.x;
-    const int lane = threadIdx.x % 32;
-    const float inv = 1.0f / (float)p.cols;
+    const int lane = threadIdx.x % 32, cols = (int)p.cols;
+    const float inv = 1.0f / (float)cols;
     griddep_wait();
-    float v[NC][16];
-    if (p.F) {
-        const T* frow = static_cast<const T*>(p.F) + r * p.ldf;
-        float ss = 0.0f;
+    // both inputs are requested before the first sum is waited for, where
+    // registers hold them (64 values of a thread in fp32 are too many)
+    constexpr bool EARLY = NC * MxIn<T>::LOADS <= 8;
+    const T* frow = static_cast<const T*>(p.F) + r * p.ldf;
+    const T* rrow = static_cast<const T*>(p.R) + r * p.ldr;
+    Row16 v[NC];
+    Raw16<T> raw[EARLY ? NC : 1];
+    {
+        Raw16<T> f[NC];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            mx_load16(frow, ((int64_t)i * blockDim.x + threadIdx.x) * 16, p.cols, p.vec, v[i]);
-            if (p.post) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) ss = fmaf(v[i][j], v[i][j], ss);
-            }
+            const int c0 = (i * (int)blockDim.x + (int)threadIdx.x) * 16;
+            if (p.F) f[i] = mx_load16(frow, c0, cols, p.vec);
+            if constexpr (EARLY) raw[i] = mx_load16(rrow, c0, cols, p.vec);
         }
-        const float rs = p.post ? rsqrtf(fmaf(mx_block_sum(ss, red), inv, p.eps)) : 1.0f;
+        if (p.F) {
+#pragma unroll
+            for (int i = 0; i < NC; ++i) v[i] = mx_values<T>(f[i]);
+        }
+    }
+    if (p.F) {
+        float rs = 1.0f;
+        if (p.post) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NC; ++i) ss = mx_sum_squares(v[i], ss);
+            rs = rsqrtf(fmaf(mx_block_sum(ss, red), inv, p.eps));
+        }
+        const uint64_t rs2 = pack2(rs, rs);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int64_t c0 = ((int64_t)i * blockDim.x + threadIdx.x) * 16;
+            const int c0 = (i * (int)blockDim.x + (int)threadIdx.x) * 16;
             if (p.post) {
-                float w[16];
-                mx_load16_any(p.post, p.weight_type, 0, c0, p.cols, p.wvec, w);
+                const Row16 w = mx_load16_any(p.post, p.weight_type, 0, c0, cols, p.wvec);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[i][j] = v[i][j] * rs * w[j];
+                for (int j = 0; j < 8; ++j) v[i].p[j] = mul2(mul2(v[i].p[j], rs2), w.p[j]);
             }
             if (p.gate) {
-                float w[16];
-                mx_load16_any(p.gate, p.gate_type, r * p.gate_ld, c0, p.cols, p.gvec, w);
+                const Row16 w = mx_load16_any(p.gate, p.gate_type, r * p.gate_ld, c0, cols, p.gvec);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) v[i][j] *= w[j];
+                for (int j = 0; j < 8; ++j) v[i].p[j] = mul2(v[i].p[j], w.p[j]);
             }
         }
     }
-    const T* rrow = static_cast<const T*>(p.R) + r * p.ldr;
+    const uint64_t sc2 = pack2(p.residual_scale, p.residual_scale);
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-        const int64_t c0 = ((int64_t)i * blockDim.x + threadIdx.x) * 16;
-        float x[16];
-        mx_load16(rrow, c0, p.cols, p.vec, x);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
+        const int c0 = (i * (int)blockDim.x + (int)threadIdx.x) * 16;
+        Raw16<T>& x = raw[EARLY ? i : 0];
+        if constexpr (!EARLY) x = mx_load16(rrow, c0, cols, p.vec);
+        Row16 s = mx_values<T>(x);
+        if (p.F) {
             // the sum is rounded to the residual's type before it is normed, so
             // y is the norm of what O holds
-            v[i][j] = p.F ? MxIn<T>::round(fmaf(p.residual_scale, v[i][j], x[j])) : x[j];
-            ss = fmaf(v[i][j], v[i][j], ss);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s.p[j] = fma2(sc2, v[i].p[j], s.p[j]);
+            x = mx_round<T>(s);
+            s = mx_values<T>(x);
         }
-        if (p.O) mx_store16(static_cast<T*>(p.O) + r * p.ldo, c0, p.cols, p.vec, v[i]);
+        v[i] = s;
+        ss = mx_sum_squares(s, ss);
+        if (p.O) mx_store16(static_cast<T*>(p.O) + r * p.ldo, c0, cols, p.vec, x);
     }
     const float rs = rsqrtf(fmaf(mx_block_sum(ss, red), inv, p.eps));
-    const int64_t atoms = mx_atoms(NVF4 ? MXF_NVFP4 : MXF_MXFP4, p.cols);
-    const int64_t chunk_end = atoms * (NVF4 ? 4 : 8);
+    const uint64_t rs2 = pack2(rs, rs);
+    const int chunk_end = p.atoms * (NVF4 ? 4 : 8);
+    uint8_t* srow = p.S + mx_scale_row_at(r, p.atoms);
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
-        const int64_t chunk = (int64_t)i * blockDim.x + threadIdx.x, c0 = chunk * 16;
+        const int chunk = i * (int)blockDim.x + (int)threadIdx.x;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i].p[j] = mul2(v[i].p[j], rs2);
         if (p.pre) {
-            float w[16];
-            mx_load16_any(p.pre, p.weight_type, 0, c0, p.cols, p.wvec, w);
+            const Row16 w = mx_load16_any(p.pre, p.weight_type, 0, chunk * 16, cols, p.wvec);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[i][j] = v[i][j] * rs * w[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) v[i][j] *= rs;
+            for (int j = 0; j < 8; ++j) v[i].p[j] = mul2(v[i].p[j], w.p[j]);
         }
         uint2 codes;
-        const uint32_t byte = mx_quantize16<NVF4>(v[i], p.tensor_scale, p.six_g, codes);
-        mx_store_codes(p.Q + r * p.ldq, c0, p.cols, codes);
-        const bool pad = (NVF4 ? c0 : chunk / 2 * 32) >= p.cols;
-        mx_store_scales<NVF4>(p.S, r, chunk, chunk_end, atoms, pad ? 0u : byte, lane);
+        const uint32_t byte = mx_quantize16<NVF4>(v[i], p.c, codes);
+        mx_store_codes(p.Q + r * p.ldq, chunk * 16, cols, codes);
+        mx_store_scales<NVF4>(srow, chunk, chunk_end, cols, byte, lane);
     }
 }
 
@@ -260,7 +314,7 @@ cudaError_t mx_norm_launch(const MxNormParams& p, int threads, cudaStream_t st) 
 
 template <typename T, bool NVF4>
 cudaError_t mx_norm_pick(const MxNormParams& p, cudaStream_t st) {
-    const int64_t chunks = mx_atoms(p.format, p.cols) * (NVF4 ? 4 : 8);
+    const int64_t chunks = (int64_t)p.atoms * (NVF4 ? 4 : 8);
     // one chunk a thread up to 256 threads, then two, then four
     const int nc = chunks <= 256 ? 1 : (chunks <= 1024 ? 2 : 4);
     const int64_t threads = ceil_div(ceil_div(chunks, nc), 32) * 32;

@@ -8,45 +8,70 @@
 
 namespace qg {
 
-// 16 bytes of T per load.
+// Two fp32 operations in one instruction, each rounded to nearest.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t d, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// Sixteen values as eight packed pairs.
+struct Row16 {
+    uint64_t p[8];
+};
+
+// 16 bytes of T: 16 / sizeof(T) values, as pairs.
 template <typename T>
 struct MxIn;
 template <>
 struct MxIn<float> {
     static constexpr int LOADS = 4;
     static __device__ __forceinline__ float one(const float* p) { return *p; }
-    static __device__ __forceinline__ void unpack(const uint4& w, float* v) {
-        v[0] = __uint_as_float(w.x);
-        v[1] = __uint_as_float(w.y);
-        v[2] = __uint_as_float(w.z);
-        v[3] = __uint_as_float(w.w);
-    }
-    static __device__ __forceinline__ float round(float x) { return x; }
     static __device__ __forceinline__ void st(float* p, float x) { *p = x; }
-    static __device__ __forceinline__ uint4 pack(const float* v) {
-        return make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    static __device__ __forceinline__ void unpack(const uint4& w, uint64_t* v) {
+        v[0] = pack2(__uint_as_float(w.x), __uint_as_float(w.y));
+        v[1] = pack2(__uint_as_float(w.z), __uint_as_float(w.w));
+    }
+    static __device__ __forceinline__ uint4 pack(const uint64_t* v) {
+        float f[4];
+        unpack2(v[0], f[0], f[1]);
+        unpack2(v[1], f[2], f[3]);
+        return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
     }
 };
 template <>
 struct MxIn<__half> {
     static constexpr int LOADS = 2;
     static __device__ __forceinline__ float one(const __half* p) { return __half2float(*p); }
-    static __device__ __forceinline__ void unpack(const uint4& w, float* v) {
+    static __device__ __forceinline__ void st(__half* p, float x) { *p = __float2half_rn(x); }
+    static __device__ __forceinline__ void unpack(const uint4& w, uint64_t* v) {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
+            v[i] = pack2(f.x, f.y);
         }
     }
-    static __device__ __forceinline__ float round(float x) { return __half2float(__float2half_rn(x)); }
-    static __device__ __forceinline__ void st(__half* p, float x) { *p = __float2half_rn(x); }
-    static __device__ __forceinline__ uint4 pack(const float* v) {
+    static __device__ __forceinline__ uint4 pack(const uint64_t* v) {
         uint32_t u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+            float a, b;
+            unpack2(v[i], a, b);
+            const __half2 h = __floats2half2_rn(a, b);
             u[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
         return make_uint4(u[0], u[1], u[2], u[3]);
@@ -56,53 +81,106 @@ template <>
 struct MxIn<__nv_bfloat16> {
     static constexpr int LOADS = 2;
     static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-    static __device__ __forceinline__ void unpack(const uint4& w, float* v) {
+    static __device__ __forceinline__ void st(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+    static __device__ __forceinline__ void unpack(const uint4& w, uint64_t* v) {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(u[i] << 16);
-            v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-        }
+        for (int i = 0; i < 4; ++i) v[i] = pack2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
     }
-    static __device__ __forceinline__ float round(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
-    static __device__ __forceinline__ void st(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
-    static __device__ __forceinline__ uint4 pack(const float* v) {
+    static __device__ __forceinline__ uint4 pack(const uint64_t* v) {
         uint32_t u[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            float a, b;
+            unpack2(v[i], a, b);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
             u[i] = *reinterpret_cast<const uint32_t*>(&h);
         }
         return make_uint4(u[0], u[1], u[2], u[3]);
     }
 };
 
-// Sixteen values of a row from column c0 on; zero past `cols`.  Plain loads:
-// the residual norm may write where it read.
+// The bits of sixteen values of a row, as 16-byte words.
 template <typename T>
-__device__ __forceinline__ void mx_load16(const T* row, int64_t c0, int64_t cols, bool vec, float (&v)[16]) {
+struct Raw16 {
+    uint4 w[MxIn<T>::LOADS];
+};
+
+// Sixteen values of a row from column c0 on; zero past `cols`.  Plain loads:
+// the residual norm may write where it read.  vec: 2 rows 32-byte aligned, one
+// 32-byte load a half of two (every request then covers whole sectors), 1 rows
+// 16-byte aligned, 0 neither.
+template <typename T>
+__device__ __forceinline__ Raw16<T> mx_load16(const T* row, int c0, int cols, int vec) {
+    Raw16<T> r;
     if (vec && c0 + 16 <= cols) {
-        uint4 w[MxIn<T>::LOADS];
+        if (vec == 2) {
 #pragma unroll
-        for (int i = 0; i < MxIn<T>::LOADS; ++i) w[i] = *(reinterpret_cast<const uint4*>(row + c0) + i);
+            for (int i = 0; i < MxIn<T>::LOADS; i += 2) {
+                uint4 &a = r.w[i], &b = r.w[i + 1];
+                asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                             : "l"(reinterpret_cast<const uint4*>(row + c0) + i)
+                             : "memory");
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < MxIn<T>::LOADS; ++i) MxIn<T>::unpack(w[i], v + i * (16 / MxIn<T>::LOADS));
+            for (int i = 0; i < MxIn<T>::LOADS; ++i) r.w[i] = *(reinterpret_cast<const uint4*>(row + c0) + i);
+        }
     } else {
+        uint64_t v[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = c0 + i < cols ? MxIn<T>::one(row + c0 + i) : 0.0f;
+        for (int i = 0; i < 8; ++i)
+            v[i] = pack2(c0 + 2 * i < cols ? MxIn<T>::one(row + c0 + 2 * i) : 0.0f,
+                         c0 + 2 * i + 1 < cols ? MxIn<T>::one(row + c0 + 2 * i + 1) : 0.0f);
+#pragma unroll
+        for (int i = 0; i < MxIn<T>::LOADS; ++i) r.w[i] = MxIn<T>::pack(v + i * (8 / MxIn<T>::LOADS));
     }
+    return r;
 }
 
 template <typename T>
-__device__ __forceinline__ void mx_store16(T* row, int64_t c0, int64_t cols, bool vec, const float (&v)[16]) {
+__device__ __forceinline__ Row16 mx_values(const Raw16<T>& r) {
+    Row16 v;
+#pragma unroll
+    for (int i = 0; i < MxIn<T>::LOADS; ++i) MxIn<T>::unpack(r.w[i], v.p + i * (8 / MxIn<T>::LOADS));
+    return v;
+}
+
+// Rounded to T.
+template <typename T>
+__device__ __forceinline__ Raw16<T> mx_round(const Row16& v) {
+    Raw16<T> r;
+#pragma unroll
+    for (int i = 0; i < MxIn<T>::LOADS; ++i) r.w[i] = MxIn<T>::pack(v.p + i * (8 / MxIn<T>::LOADS));
+    return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void mx_store16(T* row, int c0, int cols, int vec, const Raw16<T>& r) {
     if (vec && c0 + 16 <= cols) {
+        if (vec == 2) {
 #pragma unroll
-        for (int i = 0; i < MxIn<T>::LOADS; ++i)
-            *(reinterpret_cast<uint4*>(row + c0) + i) = MxIn<T>::pack(v + i * (16 / MxIn<T>::LOADS));
+            for (int i = 0; i < MxIn<T>::LOADS; i += 2) {
+                const uint4 &a = r.w[i], &b = r.w[i + 1];
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                                 reinterpret_cast<uint4*>(row + c0) + i),
+                             "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                             : "memory");
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < MxIn<T>::LOADS; ++i) *(reinterpret_cast<uint4*>(row + c0) + i) = r.w[i];
+        }
     } else {
+        const Row16 v = mx_values<T>(r);
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (c0 + i < cols) MxIn<T>::st(row + c0 + i, v[i]);
+        for (int i = 0; i < 8; ++i) {
+            float a, b;
+            unpack2(v.p[i], a, b);
+            if (c0 + 2 * i < cols) MxIn<T>::st(row + c0 + 2 * i, a);
+            if (c0 + 2 * i + 1 < cols) MxIn<T>::st(row + c0 + 2 * i + 1, b);
+        }
     }
 }
 
@@ -140,82 +218,110 @@ __device__ __forceinline__ float mx_scale_value(uint32_t byte) {
     return byte == 0xFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte ? byte << 23 : 1u << 22);
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN when either is
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// Largest magnitude of 16 values; NaN when one of them is.
+__device__ __forceinline__ float mx_amax16(const Row16& v) {
+    float m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float a, b;
+        unpack2(v.p[i], a, b);
+        m[i] = max_nan(fabsf(a), fabsf(b));
+    }
+    return max_nan(max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3])), max_nan(max_nan(m[4], m[5]), max_nan(m[6], m[7])));
+}
+
 // One thread's 16 values to codes; returns the block's scale byte.  Every lane
 // of the warp takes part (MXFP4 blocks span an even lane and the next one).
-// NVFP4's quotient x / u, u = s g: with r = RN(1/u), q0 = RN(x r) and the exact
-// remainder q0 u - x, RN(q0 - remainder * r) is the correctly rounded quotient
-// (Markstein's theorem), so a quotient that lies on a tie of the 4-bit grid is
-// found there (and -0 stays -0 with these signs).  MXFP4's is a product with a power of two, exact.
+//
+// NVFP4's quotients x / u, u = s g, and amax / (6 g): with r = RN(1/u), q0 = RN(x r)
+// and the exact remainder e = u q0 - x, RN(q0 - e r) is the correctly rounded
+// quotient (Markstein's theorem), so a quotient that lies on a tie of the 4-bit
+// grid is found there.  Here x is -v and the codes' signs are turned at the end:
+// no operand has to be negated, three packed operations do two values, and a
+// zero keeps its sign.  MXFP4's quotient is a product with a power of two.
 template <bool NVF4>
-__device__ __forceinline__ uint32_t mx_quantize16(const float (&v)[16], float g, float six_g, uint2& codes) {
-    uint32_t amax = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {  // magnitudes order as integers, NaN above infinity
-        const uint32_t a = __float_as_uint(v[i]) & 0x7FFFFFFFu;
-        amax = a > amax ? a : amax;
-    }
-    if constexpr (!NVF4) {
-        const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, amax, 1);
-        amax = o > amax ? o : amax;
-    }
-    const bool fine = amax < 0x7F800000u;
+__device__ __forceinline__ uint32_t mx_quantize16(const Row16& v, const MxScaleConst& c, uint2& codes) {
+    float amax = mx_amax16(v);
+    if constexpr (!NVF4) amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    const bool fine = amax < __uint_as_float(0x7F800000u);  // false for NaN
     float w[16];
-    uint32_t byte;
     if constexpr (NVF4) {
-        byte = mx_e4m3_byte(fminf(__fdiv_rn(__uint_as_float(amax), six_g), 448.0f));
-        const float u = mx_e4m3_value(byte) * g;
-        const bool live = fine && u > 0.0f;
-        const float r = live ? __frcp_rn(u) : 0.0f;
-        const float m = live ? u : 0.0f;
+        const float t0 = amax * c.inv_six_g;
+        // far above the largest scale the quotient's last bit does not matter
+        // (and its remainder may overflow)
+        const float t = t0 < 1024.0f ? fmaf(fmaf(t0, c.six_g, -amax), -c.inv_six_g, t0) : 448.0f;
+        const uint32_t byte = mx_e4m3_byte(fminf(t, 448.0f));
+        const float u = mx_e4m3_value(byte) * c.g;
+        const float nr = -__frcp_rn(u);
         if (byte == 0x7Eu) {  // the scale stands at its largest: the quotient may be anything, up to infinity
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = live ? __fdiv_rn(v[i], u) : 0.0f;
+            for (int i = 0; i < 8; ++i) {
+                float a, b;
+                unpack2(v.p[i], a, b);
+                w[2 * i] = __fdiv_rn(-a, u);
+                w[2 * i + 1] = __fdiv_rn(-b, u);
+            }
         } else {
+            const uint64_t nr2 = pack2(nr, nr), u2 = pack2(u, u);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float x = live ? v[i] : 0.0f;
-                const float q0 = x * r;
-                w[i] = fmaf(fmaf(q0, m, -x), -r, q0);
+            for (int i = 0; i < 8; ++i) {
+                const uint64_t q0 = mul2(v.p[i], nr2);
+                unpack2(fma2(fma2(q0, u2, v.p[i]), nr2, q0), w[2 * i], w[2 * i + 1]);
             }
         }
-        if (!fine) byte = 0x7Fu;
+        const bool live = fine && byte != 0;  // u = 0: no reciprocal, no codes
+        codes = make_uint2(live ? mx_codes8(w) ^ 0x88888888u : 0u, live ? mx_codes8(w + 8) ^ 0x88888888u : 0u);
+        return fine ? byte : 0x7Fu;
     } else {
-        const int e = (int)(amax >> 23) - 2;
-        byte = e > 0 ? (uint32_t)e : 0u;
+        const int e = (int)(__float_as_uint(amax) >> 23) - 2;
+        const uint32_t byte = e > 0 ? (uint32_t)e : 0u;
         const float r = __uint_as_float((254u - byte) << 23);  // 2^(127 - byte)
+        const uint64_t r2 = pack2(r, r);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = fine ? v[i] * r : 0.0f;
-        if (!fine) byte = 0xFFu;
+        for (int i = 0; i < 8; ++i) unpack2(mul2(v.p[i], r2), w[2 * i], w[2 * i + 1]);
+        codes = make_uint2(fine ? mx_codes8(w) : 0u, fine ? mx_codes8(w + 8) : 0u);
+        return fine ? byte : 0xFFu;
     }
-    codes = make_uint2(mx_codes8(w), mx_codes8(w + 8));
-    return byte;
 }
 
 // Store a thread's codes: 8 bytes, or what of them lies before the row's end.
-__device__ __forceinline__ void mx_store_codes(uint8_t* row, int64_t c0, int64_t cols, const uint2& codes) {
+__device__ __forceinline__ void mx_store_codes(uint8_t* row, int c0, int cols, const uint2& codes) {
     if (c0 + 16 <= cols) {
         *reinterpret_cast<uint2*>(row + c0 / 2) = codes;
     } else if (c0 < cols) {
-        const int64_t n = (cols - c0 + 1) / 2;  // codes past the row's end are zero
+        const int n = (cols - c0 + 1) / 2;  // codes past the row's end are zero
         for (int i = 0; i < 8; ++i)
             if (i < n) row[c0 / 2 + i] = (uint8_t)((i < 4 ? codes.x >> (8 * i) : codes.y >> (8 * i - 32)) & 0xFFu);
     }
 }
 
+// Byte of row srow's first scale; block b's lies mx_block_at(b) further.
+__device__ __forceinline__ int64_t mx_scale_row_at(int64_t srow, int atoms) {
+    const uint32_t in = (uint32_t)srow % MX_ATOM_ROWS;
+    return (int64_t)((uint32_t)srow / MX_ATOM_ROWS) * atoms * MX_ATOM_BYTES + in % 32 * 16 + in / 32 * 4;
+}
+__device__ __forceinline__ int64_t mx_block_at(int b) { return (int64_t)(b / 4) * MX_ATOM_BYTES + b % 4; }
+
 // Store the scales of the warp's blocks, four blocks (one row's share of an
-// atom) per store.  chunk: this lane's 16-value chunk; lanes hold consecutive
-// chunks of one row, the warp's first a multiple of 8; chunks at or past
-// chunk_end are not stored.  srow: the scale row.
+// atom) per store.  S: the row's first scale.  chunk: this lane's 16-value chunk;
+// lanes hold consecutive chunks of one row, the warp's first a multiple of 8;
+// chunks at or past chunk_end are not stored, blocks past the row's end are
+// padding: zero, whatever an empty block's scale would be.
 template <bool NVF4>
-__device__ __forceinline__ void mx_store_scales(uint8_t* S, int64_t srow, int64_t chunk, int64_t chunk_end,
-                                                int64_t atoms, uint32_t byte, int lane) {
+__device__ __forceinline__ void mx_store_scales(uint8_t* S, int chunk, int chunk_end, int cols, uint32_t byte, int lane) {
     constexpr int PER = NVF4 ? 1 : 2;  // lanes per block
+    if (chunk / PER * (16 * PER) >= cols) byte = 0;
     uint32_t w = byte;
     w |= __shfl_down_sync(0xFFFFFFFFu, byte, PER) << 8;
     const uint32_t hi = __shfl_down_sync(0xFFFFFFFFu, w, 2 * PER);
     w = (w & 0xFFFFu) | (hi << 16);
-    if (lane % (4 * PER) == 0 && chunk < chunk_end)
-        *reinterpret_cast<uint32_t*>(S + mx_scale_at(srow, chunk / PER, atoms)) = w;
+    if (lane % (4 * PER) == 0 && chunk < chunk_end) *reinterpret_cast<uint32_t*>(S + mx_block_at(chunk / PER)) = w;
 }
 
 // Warp-wide: the scale row of token row r when rows are sorted by expert (each
