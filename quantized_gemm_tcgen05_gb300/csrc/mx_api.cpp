@@ -362,7 +362,6 @@ int run_product(gemm_handle_t h, const gemm_op_t* op, MxProduct& p, cudaStream_t
     k.tiles_m = (int32_t)tm;
     k.tiles_n = (int32_t)tn;
     k.k_steps = (int32_t)ceil_div(p.K, MX_KSTEP);
-    k.k_atoms = (int32_t)ceil_div(p.K, 64);
     k.splits = c.splits;
     k.a_rows = c.pair ? 128 : rows_staged(p);
     k.stages = c.pair ? 0 : mx_gemm_stages(c.bn, p.format, k.a_rows, c.splits);
@@ -528,6 +527,7 @@ int gemm_mx_norm_quantize(gemm_handle_t h, const gemm_mx_norm_t* op, const void*
         p.wvec = std::min(row_alignment(op->post_weight, 0, ws), row_alignment(op->pre_weight, 0, ws));
         p.gvec = row_alignment(op->gate, op->gate_ld, gs);
         p.atoms = (int32_t)mx_atoms(op->format, cols);
+        p.sm_count = handle_sm_count(h);
         p.eps = op->eps;
         p.residual_scale = op->residual_scale;
         p.c = mx_scale_const(op->tensor_scale);

@@ -19,6 +19,14 @@ __device__ __forceinline__ void st32(void* p, const uint32_t (&w)[8]) {
                  : "memory");
 }
 
+// Bring `count` columns of C's row m, from n on, into L2 before they are needed.
+__device__ __forceinline__ void mx_prefetch_c(const EpiParams& e, int64_t m, int64_t n, int64_t count) {
+    const int64_t es = e.d_type == DT_F32 ? 4 : 2;
+    const char* p = static_cast<const char*>(e.C) + (m * e.ldc + n) * es;
+    for (int64_t b = 0; b < count * es; b += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + b));
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + count * es - es));
+}
+
 // 64 accumulator columns (TMEM address ta, this warp's 32 rows, a row per lane)
 // as finished 16-bit values: w[j] holds columns 2 j and 2 j + 1.
 template <int ACT, int DT>
@@ -142,16 +150,12 @@ __device__ __forceinline__ void mx_store_block_t(const EpiParams& ep, bool vec32
     const int64_t n = n0 + lane;
     if (n < e.N) {
         const float b = ACT >= 0 ? bias_at(ar, n) : 0.0f;
-        for (int r0 = 0; r0 < rows; r0 += 8) {  // eight rows' C in flight together
-            float c[8];
+        float c[32];  // every row's C in flight together
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                c[j] = use_c && r0 + j < rows ? ld_elem(e.C, DT, (m0 + r0 + j) * e.ldc + n) : 0.0f;
+        for (int r = 0; r < 32; ++r) c[r] = use_c && r < rows ? ld_elem(e.C, DT, (m0 + r) * e.ldc + n) : 0.0f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (r0 + j < rows)
-                    st_elem(e.D, DT, (m0 + r0 + j) * e.ldd + n, epi_value<ACT>(ar, stage[(r0 + j) * 33 + lane], c[j], b));
-        }
+        for (int r = 0; r < 32; ++r)
+            if (r < rows) st_elem(e.D, DT, (m0 + r) * e.ldd + n, epi_value<ACT>(ar, stage[r * 33 + lane], c[r], b));
     }
     __syncwarp();
 }

@@ -228,7 +228,12 @@ __global__ void __launch_bounds__(MX_THREADS, 2)
                 ta = tmem + BN;
             }
         }
-    } else if (live && warp >= 4) {
+    } else if (live && warp < 4) {
+        // two warps without a part in the main loop fetch the tile's C
+        if (P.epi.beta != 0.0f && n0 < P.epi.N)
+            for (int r = threadIdx.x - 64; r < rows; r += 64)
+                mx_prefetch_c(P.epi, row0 + r, n0, P.epi.N - n0 < BN ? P.epi.N - n0 : BN);
+    } else if (live) {
         const uint32_t quarter = (uint32_t)(warp % 4 * 32) << 16;
         int s = 0;
         uint32_t ph = 0;

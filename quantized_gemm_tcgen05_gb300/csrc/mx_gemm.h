@@ -11,7 +11,6 @@ struct MxGemmParams {
     int32_t num_experts;
     int32_t tiles_m, tiles_n;    // output tiles (grouped: tiles_m is an upper bound)
     int32_t k_steps;             // 256-wide K-steps
-    int32_t k_atoms;             // 64-wide instruction steps of the whole K
     int32_t splits;              // CTAs of a cluster, each a share of the K-steps (single-CTA kernel)
     int32_t programs;            // persistent programs (pair kernel)
     int32_t a_rows;              // rows of A a stage holds (a multiple of 8, at most 128)

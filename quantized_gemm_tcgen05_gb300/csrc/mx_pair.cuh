@@ -4,9 +4,13 @@
 // Per 256-wide K-step an SM takes in its 128 rows of A, its half of the 256 rows
 // of B, the scale atom of its A rows and both atoms of B (a pair's MMA wants all
 // of B's scales in both CTAs' TMEM): 38 KB for 128 x 256 x 256 products, the
-// least per product that the accumulator's size allows.  That ingest, about 57
-// bytes a clock and SM, is what bounds large products; the tensor core alone
-// would need 512 clocks a step.
+// least per product that the accumulator's size allows.  That ingest is what
+// bounds large products: a few SMs take a step in 0.29 us (131 bytes a
+// nanosecond), all of them together in 0.40, and the MMAs hide behind it but for
+// the last tile's.  Sharing A between two neighbouring pairs of a cluster by
+// multicast asks L2 for a fifth less and changed nothing (32.1 against 31.8 us at
+// 4096^3, 81.5 against 84.2 at 4096x14336x4096), so the limit is what an SM
+// receives, not what L2 gives out.
 //
 // TMEM: 256 accumulator columns and as many scale buffers as the ring has
 // stages.  Scales go from shared memory to TMEM through the registers of four
@@ -135,15 +139,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_PAIR_THREADS, 1)
     const Guard g{P.status, P.timeout_ns, abort_flag};
     const int64_t pid = blockIdx.x >> 1;
     const int64_t blocks = P.offsets ? mx_expert_blocks(P.offsets, P.num_experts, 256, lane) : P.tiles_m;
+    const int64_t tiles = blocks * P.tiles_n;
 
     if (warp == 0) {
         // ---------------- TMA producer (both CTAs) ----------------
         int s = 0;
         uint32_t ph = 0, armed = 0, armed_par = 0;
         bool ok = true;
-        MxTile t;
+        MxTile t, next;
         const uint32_t l_full = mapa_shared(smem_u32(full), 0);
-        for (int64_t i = pid; ok && mx_pair_tile(P, blocks, i, lane, t); i += P.programs) {
+        // the next tile is looked up while the ring is full, not between tiles
+        const int look = (P.k_steps < S ? P.k_steps : S) - 1;
+        bool have = mx_pair_tile(P, blocks, pid, lane, t);
+        for (int64_t i = pid; ok && have; i += P.programs, t = next) {
             const int32_t a0 = (int32_t)(t.row0 + 128 * rank), b0 = (int32_t)(t.n0 + 128 * rank);
             const int32_t sa0 = (int32_t)(t.atom_row + rank), sb0 = (int32_t)(t.n0 / 128);
             int32_t kx = 0, sx = 0;
@@ -171,6 +179,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_PAIR_THREADS, 1)
                     tma_load_2d_pair(a, &tmA, bar, kx, a0);
                 }
                 __syncwarp();
+                if (k == look) have = mx_pair_tile(P, blocks, i + P.programs, lane, next);
                 kx += 128;
                 sx += (int32_t)(Cfg::SA_BYTES / 8);
                 if (++s == S) {
@@ -202,8 +211,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_PAIR_THREADS, 1)
         int s = 0;
         uint32_t ph = 0, it = 0;
         bool ok = true, issued = false;
-        MxTile t;
-        for (int64_t i = pid; ok && mx_pair_tile(P, blocks, i, lane, t); i += P.programs, ++it) {
+        for (int64_t i = pid; ok && i < tiles; i += P.programs, ++it) {
             // the accumulator's previous tile is in the epilogue's registers
             ok = __all_sync(0xFFFFFFFFu, wait_bar_cluster(tempty, (it & 1) ^ 1, g, SITE_MMA_TMEM_EMPTY));
             tc_fence_after_sync();
@@ -252,8 +260,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_PAIR_THREADS, 1)
         int s = 0;
         uint32_t ph = 0;
         bool ok = true;
-        MxTile t;
-        for (int64_t i = pid; ok && mx_pair_tile(P, blocks, i, lane, t); i += P.programs) {
+        for (int64_t i = pid; ok && i < tiles; i += P.programs) {
             for (int k = 0; k < P.k_steps; ++k) {
                 // the scales are there; the buffer's previous readers are done (the
                 // producer has waited for the same phase of empty[s])
@@ -308,6 +315,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_PAIR_THREADS, 1)
             int rows = t.rows - 128 * (int)rank - 32 * ew;
             rows = rows < 0 ? 0 : (rows > 32 ? 32 : rows);
             const int64_t m0 = t.row0 + 128 * rank + 32 * ew, n0 = t.n0 + 128 * half;
+            if (P.epi.beta != 0.0f && lane < rows && n0 < P.epi.N)
+                mx_prefetch_c(P.epi, m0 + lane, n0, P.epi.N - n0 < 128 ? P.epi.N - n0 : 128);
             if (!__all_sync(0xFFFFFFFFu, wait_bar(tfull, it & 1, g, SITE_EPI_TMEM_FULL))) break;
             tc_fence_after_sync();
             const uint32_t ta = tmem + 128 * half + ((uint32_t)(ew * 32) << 16);

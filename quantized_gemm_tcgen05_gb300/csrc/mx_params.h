@@ -56,6 +56,7 @@ struct MxNormParams {
     int32_t type, format;
     int32_t vec;    // F, R, O: as in MxQuantParams
     int32_t atoms;  // scale atoms of a row
+    int32_t sm_count;
     float eps, residual_scale;
     MxScaleConst c;
     const void *post, *pre, *gate;

@@ -13,36 +13,26 @@ namespace qg {
 
 namespace {
 
-constexpr int QWARPS = 8;  // warps of a block
-constexpr int QROWS = 2;   // rows a warp takes, so that its address arithmetic and
-                           // its launch are paid for twice as many bytes
+constexpr int QWARPS = 8;  // warps of a block, a row each
 
+// 32 registers, so that 64 warps an SM keep the loads going: 28.4 us for 4096 x
+// 14336 bf16 (150 MB: 5.3 TB/s); with two rows a warp and 50 registers 30.6.
 template <typename T, bool NVF4>
-__global__ void __launch_bounds__(32 * QWARPS) mx_quantize_kernel(const __grid_constant__ MxQuantParams p) {
+__global__ void __launch_bounds__(32 * QWARPS, 8) mx_quantize_kernel(const __grid_constant__ MxQuantParams p) {
     griddep_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int r0 = (int)blockIdx.x * (QWARPS * QROWS) + warp;  // then QWARPS further
+    const int r = (int)blockIdx.x * QWARPS + warp;
     const int chunk = (int)blockIdx.y * 32 + lane, cols = (int)p.cols;
     const int chunk_end = p.atoms * (NVF4 ? 4 : 8);
-    if (r0 >= p.rows) return;
+    if (r >= p.rows) return;
     griddep_wait();
-    Raw16<T> raw[QROWS];
-#pragma unroll
-    for (int j = 0; j < QROWS; ++j)
-        if (r0 + j * QWARPS < p.rows)
-            raw[j] = mx_load16(static_cast<const T*>(p.X) + blockIdx.z * p.x_bstride + (r0 + j * QWARPS) * p.ldx, chunk * 16,
-                               cols, p.vec);
-#pragma unroll
-    for (int j = 0; j < QROWS; ++j) {
-        const int r = r0 + j * QWARPS;
-        if (r >= p.rows) break;
-        const int64_t srow = p.offsets ? mx_expert_row(p.offsets, p.num_experts, r, lane) : r;
-        if (srow < 0) continue;
-        uint2 codes;
-        const uint32_t byte = mx_quantize16<NVF4>(mx_values<T>(raw[j]), p.c, codes);
-        mx_store_codes(static_cast<uint8_t*>(p.Y) + blockIdx.z * p.q_bstride + r * p.ldq, chunk * 16, cols, codes);
-        mx_store_scales<NVF4>(p.S + blockIdx.z * p.s_bstride + mx_scale_row_at(srow, p.atoms), chunk, chunk_end, cols, byte, lane);
-    }
+    const Raw16<T> raw = mx_load16(static_cast<const T*>(p.X) + blockIdx.z * p.x_bstride + r * p.ldx, chunk * 16, cols, p.vec);
+    const int64_t srow = p.offsets ? mx_expert_row(p.offsets, p.num_experts, r, lane) : r;
+    if (srow < 0) return;
+    uint2 codes;
+    const uint32_t byte = mx_quantize16<NVF4>(mx_values<T>(raw), p.c, codes);
+    mx_store_codes(static_cast<uint8_t*>(p.Y) + blockIdx.z * p.q_bstride + r * p.ldq, chunk * 16, cols, codes);
+    mx_store_scales<NVF4>(p.S + blockIdx.z * p.s_bstride + mx_scale_row_at(srow, p.atoms), chunk, chunk_end, cols, byte, lane);
 }
 
 // E2M1 codes as E4M3 bytes: the magnitude by a byte permute over the eight of
@@ -61,18 +51,20 @@ __device__ __forceinline__ float2 mx_code_pair(uint32_t byte) {
 
 struct E4M3Out {};  // the codes' own values
 
+constexpr int DROWS = 2;  // rows a warp of the inverse takes: it has so little to do for one
+
 // 16 bytes of codes a thread: 32 values.
 template <typename T, bool NVF4>
 __global__ void __launch_bounds__(32 * QWARPS) mx_dequantize_kernel(const __grid_constant__ MxQuantParams p) {
     griddep_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int r0 = (int)blockIdx.x * (QWARPS * QROWS) + warp;
+    const int r0 = (int)blockIdx.x * (QWARPS * DROWS) + warp;
     const int c0 = ((int)blockIdx.y * 32 + lane) * 32, cols = (int)p.cols;
     if (r0 >= p.rows) return;
     griddep_wait();
-    uint32_t w[QROWS][4];
+    uint32_t w[DROWS][4];
 #pragma unroll
-    for (int j = 0; j < QROWS; ++j) {
+    for (int j = 0; j < DROWS; ++j) {
         const uint8_t* q = static_cast<const uint8_t*>(p.X) + blockIdx.z * p.q_bstride + (r0 + j * QWARPS) * p.ldq + c0 / 2;
         w[j][0] = w[j][1] = w[j][2] = w[j][3] = 0;
         if (r0 + j * QWARPS >= p.rows) continue;
@@ -90,7 +82,7 @@ __global__ void __launch_bounds__(32 * QWARPS) mx_dequantize_kernel(const __grid
         }
     }
 #pragma unroll
-    for (int j = 0; j < QROWS; ++j) {
+    for (int j = 0; j < DROWS; ++j) {
         const int r = r0 + j * QWARPS;
         if (r >= p.rows) break;
         const int64_t srow = p.offsets ? mx_expert_row(p.offsets, p.num_experts, r, lane) : r;
@@ -134,8 +126,8 @@ __global__ void __launch_bounds__(32 * QWARPS) mx_dequantize_kernel(const __grid
 }
 
 template <typename F>
-cudaError_t mx_launch(F kernel, const MxQuantParams& p, int64_t chunks, cudaStream_t st) {
-    const int64_t gx = ceil_div(p.rows, QWARPS * QROWS), gy = ceil_div(chunks, 32);
+cudaError_t mx_launch(F kernel, const MxQuantParams& p, int rows, int64_t chunks, cudaStream_t st) {
+    const int64_t gx = ceil_div(p.rows, rows), gy = ceil_div(chunks, 32);
     if (gx > INT32_MAX || gy > 65535 || p.num > 65535) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg;
     memset(&cfg, 0, sizeof cfg);
@@ -156,9 +148,9 @@ cudaError_t launch_mx_quantize(const MxQuantParams& p, cudaStream_t st) {
     const bool nv = p.format == MXF_NVFP4;
     const int64_t chunks = (int64_t)p.atoms * (nv ? 4 : 8);
     switch (p.type) {
-        case DT_F32: return nv ? mx_launch(mx_quantize_kernel<float, true>, p, chunks, st) : mx_launch(mx_quantize_kernel<float, false>, p, chunks, st);
-        case DT_F16: return nv ? mx_launch(mx_quantize_kernel<__half, true>, p, chunks, st) : mx_launch(mx_quantize_kernel<__half, false>, p, chunks, st);
-        case DT_BF16: return nv ? mx_launch(mx_quantize_kernel<__nv_bfloat16, true>, p, chunks, st) : mx_launch(mx_quantize_kernel<__nv_bfloat16, false>, p, chunks, st);
+        case DT_F32: return nv ? mx_launch(mx_quantize_kernel<float, true>, p, QWARPS, chunks, st) : mx_launch(mx_quantize_kernel<float, false>, p, QWARPS, chunks, st);
+        case DT_F16: return nv ? mx_launch(mx_quantize_kernel<__half, true>, p, QWARPS, chunks, st) : mx_launch(mx_quantize_kernel<__half, false>, p, QWARPS, chunks, st);
+        case DT_BF16: return nv ? mx_launch(mx_quantize_kernel<__nv_bfloat16, true>, p, QWARPS, chunks, st) : mx_launch(mx_quantize_kernel<__nv_bfloat16, false>, p, QWARPS, chunks, st);
         default: return cudaErrorInvalidValue;
     }
 }
@@ -167,10 +159,10 @@ cudaError_t launch_mx_dequantize(const MxQuantParams& p, cudaStream_t st) {
     const bool nv = p.format == MXF_NVFP4;
     const int64_t chunks = ceil_div(p.cols, 32);
     switch (p.type) {
-        case DT_F32: return nv ? mx_launch(mx_dequantize_kernel<float, true>, p, chunks, st) : mx_launch(mx_dequantize_kernel<float, false>, p, chunks, st);
-        case DT_F16: return nv ? mx_launch(mx_dequantize_kernel<__half, true>, p, chunks, st) : mx_launch(mx_dequantize_kernel<__half, false>, p, chunks, st);
-        case DT_BF16: return nv ? mx_launch(mx_dequantize_kernel<__nv_bfloat16, true>, p, chunks, st) : mx_launch(mx_dequantize_kernel<__nv_bfloat16, false>, p, chunks, st);
-        case DT_E4M3: return mx_launch(mx_dequantize_kernel<E4M3Out, true>, p, chunks, st);  // no scales read
+        case DT_F32: return nv ? mx_launch(mx_dequantize_kernel<float, true>, p, QWARPS * DROWS, chunks, st) : mx_launch(mx_dequantize_kernel<float, false>, p, QWARPS * DROWS, chunks, st);
+        case DT_F16: return nv ? mx_launch(mx_dequantize_kernel<__half, true>, p, QWARPS * DROWS, chunks, st) : mx_launch(mx_dequantize_kernel<__half, false>, p, QWARPS * DROWS, chunks, st);
+        case DT_BF16: return nv ? mx_launch(mx_dequantize_kernel<__nv_bfloat16, true>, p, QWARPS * DROWS, chunks, st) : mx_launch(mx_dequantize_kernel<__nv_bfloat16, false>, p, QWARPS * DROWS, chunks, st);
+        case DT_E4M3: return mx_launch(mx_dequantize_kernel<E4M3Out, true>, p, QWARPS * DROWS, chunks, st);  // no scales read
         default: return cudaErrorInvalidValue;
     }
 }
@@ -179,25 +171,27 @@ cudaError_t launch_mx_dequantize(const MxQuantParams& p, cudaStream_t st) {
 
 namespace {
 
-// Sum over the block in a fixed order; every thread gets it.  red: one float
-// per warp.
-__device__ __forceinline__ float mx_block_sum(float x, float* red) {
+// Sum over the block in a fixed order; every thread gets it.  red: 16 floats of
+// this sum's own.
+__device__ __forceinline__ float mx_block_sum(float x, float4* red) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xFFFFFFFFu, x, d);
     const int warps = blockDim.x / 32;
     if (warps == 1) return x;
-    __syncthreads();  // the previous sum has been read
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = x;
+    if (threadIdx.x % 32 == 0) reinterpret_cast<float*>(red)[threadIdx.x / 32] = x;
     __syncthreads();
     float s = 0.0f;
-    for (int i = 0; i < warps; ++i) s += red[i];
+    for (int i = 0; i < warps; i += 4) {
+        const float4 f = red[i / 4];  // floats past the last warp's are zero
+        s += (f.x + f.y) + (f.z + f.w);
+    }
     return s;
 }
 
 __device__ __forceinline__ Row16 mx_load16_any(const void* p, int32_t type, int64_t at, int c0, int cols, int vec) {
-    if (type == DT_F32) return mx_values<float>(mx_load16(static_cast<const float*>(p) + at, c0, cols, vec));
+    if (type == DT_BF16) return mx_values<__nv_bfloat16>(mx_load16(static_cast<const __nv_bfloat16*>(p) + at, c0, cols, vec));
     if (type == DT_F16) return mx_values<__half>(mx_load16(static_cast<const __half*>(p) + at, c0, cols, vec));
-    return mx_values<__nv_bfloat16>(mx_load16(static_cast<const __nv_bfloat16*>(p) + at, c0, cols, vec));
+    return mx_values<float>(mx_load16(static_cast<const float*>(p) + at, c0, cols, vec));
 }
 
 __device__ __forceinline__ float mx_sum_squares(const Row16& v, float ss) {
@@ -209,107 +203,120 @@ __device__ __forceinline__ float mx_sum_squares(const Row16& v, float ss) {
     return x + y;
 }
 
-// A block per row; the row stays in registers between the two norms, NC
-// chunks of 16 values a thread, so F, R are read once and r', codes and scales
-// written once.  Sums of squares in fp32 over 16 * NC values a thread, then
-// over the block.  Bounded by HBM when there are many rows, by the two block
-// sums' latency when there are few.
+// A block takes rows blockIdx.x, + gridDim.x, ...; a row stays in registers
+// between the two norms, NC chunks of 16 values a thread, so F, R are read once
+// and r', codes and scales written once.  Sums of squares in fp32 over 16 * NC
+// values a thread, then over the block.
+//
+// A row is a chain of load, sum, sum, store of about 4 us, so with a block a row
+// the chain's latency bounds it (29.4 us for 4096 x 4096 bf16, 3.7 TB/s, whatever
+// is taken out of the arithmetic).  With one chunk a thread the next row's F and R
+// are requested before the present row's sums, which hides the loads (16-bit
+// types; two rows of fp32 do not fit the registers).
 template <typename T, bool NVF4, int NC>
-__global__ void __launch_bounds__(NC == 1 ? 256 : 512, NC == 1 ? 4 : 1) mx_norm_kernel(const __grid_constant__ MxNormParams p) {
-    __shared__ float red[32];
+__global__ void __launch_bounds__(NC == 1 ? 256 : 512, NC == 1 ? 3 : 1) mx_norm_kernel(const __grid_constant__ MxNormParams p) {
+    // partial sums of the first and the second norm; two sets, so that a row's are
+    // not overwritten while a slower warp still reads the previous row's
+    __shared__ float4 red_all[2][8];
     griddep_launch_dependents();
-    const int64_t r = blockIdx.x;
+    if (threadIdx.x < 64) reinterpret_cast<float*>(red_all)[threadIdx.x] = 0.0f;
+    __syncthreads();
     const int lane = threadIdx.x % 32, cols = (int)p.cols;
     const float inv = 1.0f / (float)cols;
-    griddep_wait();
-    // both inputs are requested before the first sum is waited for, where
-    // registers hold them (64 values of a thread in fp32 are too many)
-    constexpr bool EARLY = NC * MxIn<T>::LOADS <= 8;
-    const T* frow = static_cast<const T*>(p.F) + r * p.ldf;
-    const T* rrow = static_cast<const T*>(p.R) + r * p.ldr;
-    Row16 v[NC];
-    Raw16<T> raw[EARLY ? NC : 1];
-    {
-        Raw16<T> f[NC];
+    const uint64_t sc2 = pack2(p.residual_scale, p.residual_scale);
+    const int chunk_end = p.atoms * (NVF4 ? 4 : 8);
+    constexpr bool AHEAD = NC == 1 && sizeof(T) == 2;
+    // where registers do not hold both inputs, R is loaded after the first sum
+    constexpr bool EARLY = NC * MxIn<T>::LOADS <= 4;
+    Raw16<T> f[NC], x[EARLY ? NC : 1];
+    auto load = [&](int64_t r) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c0 = (i * (int)blockDim.x + (int)threadIdx.x) * 16;
-            if (p.F) f[i] = mx_load16(frow, c0, cols, p.vec);
-            if constexpr (EARLY) raw[i] = mx_load16(rrow, c0, cols, p.vec);
+            if (p.F) f[i] = mx_load16(static_cast<const T*>(p.F) + r * p.ldf, c0, cols, p.vec);
+            if constexpr (EARLY) x[i] = mx_load16(static_cast<const T*>(p.R) + r * p.ldr, c0, cols, p.vec);
         }
+    };
+    griddep_wait();
+    if (AHEAD) load(blockIdx.x);
+    int it = 0;
+    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x, ++it) {
+        float4* red = red_all[it & 1];
+        if (!AHEAD) load(r);
+        Row16 v[NC];
         if (p.F) {
 #pragma unroll
             for (int i = 0; i < NC; ++i) v[i] = mx_values<T>(f[i]);
         }
-    }
-    if (p.F) {
-        float rs = 1.0f;
-        if (p.post) {
-            float ss = 0.0f;
+        const Raw16<T> now = x[0];
+        if (AHEAD && r + gridDim.x < p.rows) load(r + gridDim.x);
+        if (p.F) {
+            if (p.post) {
+                float ss = 0.0f;
 #pragma unroll
-            for (int i = 0; i < NC; ++i) ss = mx_sum_squares(v[i], ss);
-            rs = rsqrtf(fmaf(mx_block_sum(ss, red), inv, p.eps));
+                for (int i = 0; i < NC; ++i) ss = mx_sum_squares(v[i], ss);
+                const float rs = rsqrtf(fmaf(mx_block_sum(ss, red), inv, p.eps));
+                const uint64_t rs2 = pack2(rs, rs);
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    const Row16 w = mx_load16_any(p.post, p.weight_type, 0, (i * (int)blockDim.x + (int)threadIdx.x) * 16, cols, p.wvec);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i].p[j] = mul2(mul2(v[i].p[j], rs2), w.p[j]);
+                }
+            }
+            if (p.gate) {
+#pragma unroll
+                for (int i = 0; i < NC; ++i) {
+                    const Row16 w = mx_load16_any(p.gate, p.gate_type, r * p.gate_ld, (i * (int)blockDim.x + (int)threadIdx.x) * 16, cols, p.gvec);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[i].p[j] = mul2(v[i].p[j], w.p[j]);
+                }
+            }
         }
-        const uint64_t rs2 = pack2(rs, rs);
+        float ss = 0.0f;
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int c0 = (i * (int)blockDim.x + (int)threadIdx.x) * 16;
-            if (p.post) {
-                const Row16 w = mx_load16_any(p.post, p.weight_type, 0, c0, cols, p.wvec);
+            Raw16<T> raw = AHEAD ? now : x[EARLY ? i : 0];
+            if constexpr (!EARLY) raw = mx_load16(static_cast<const T*>(p.R) + r * p.ldr, c0, cols, p.vec);
+            Row16 s = mx_values<T>(raw);
+            if (p.F) {
+                // the sum is rounded to the residual's type before it is normed, so
+                // y is the norm of what O holds
 #pragma unroll
-                for (int j = 0; j < 8; ++j) v[i].p[j] = mul2(mul2(v[i].p[j], rs2), w.p[j]);
+                for (int j = 0; j < 8; ++j) s.p[j] = fma2(sc2, v[i].p[j], s.p[j]);
+                raw = mx_round<T>(s);
+                s = mx_values<T>(raw);
             }
-            if (p.gate) {
-                const Row16 w = mx_load16_any(p.gate, p.gate_type, r * p.gate_ld, c0, cols, p.gvec);
+            v[i] = s;
+            ss = mx_sum_squares(s, ss);
+            if (p.O) mx_store16(static_cast<T*>(p.O) + r * p.ldo, c0, cols, p.vec, raw);
+        }
+        const float rs = rsqrtf(fmaf(mx_block_sum(ss, red + 4), inv, p.eps));
+        const uint64_t rs2 = pack2(rs, rs);
+        uint8_t* srow = p.S + mx_scale_row_at(r, p.atoms);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const int chunk = i * (int)blockDim.x + (int)threadIdx.x;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i].p[j] = mul2(v[i].p[j], rs2);
+            if (p.pre) {
+                const Row16 w = mx_load16_any(p.pre, p.weight_type, 0, chunk * 16, cols, p.wvec);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[i].p[j] = mul2(v[i].p[j], w.p[j]);
             }
+            uint2 codes;
+            const uint32_t byte = mx_quantize16<NVF4>(v[i], p.c, codes);
+            mx_store_codes(p.Q + r * p.ldq, chunk * 16, cols, codes);
+            mx_store_scales<NVF4>(srow, chunk, chunk_end, cols, byte, lane);
         }
-    }
-    const uint64_t sc2 = pack2(p.residual_scale, p.residual_scale);
-    float ss = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int c0 = (i * (int)blockDim.x + (int)threadIdx.x) * 16;
-        Raw16<T>& x = raw[EARLY ? i : 0];
-        if constexpr (!EARLY) x = mx_load16(rrow, c0, cols, p.vec);
-        Row16 s = mx_values<T>(x);
-        if (p.F) {
-            // the sum is rounded to the residual's type before it is normed, so
-            // y is the norm of what O holds
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s.p[j] = fma2(sc2, v[i].p[j], s.p[j]);
-            x = mx_round<T>(s);
-            s = mx_values<T>(x);
-        }
-        v[i] = s;
-        ss = mx_sum_squares(s, ss);
-        if (p.O) mx_store16(static_cast<T*>(p.O) + r * p.ldo, c0, cols, p.vec, x);
-    }
-    const float rs = rsqrtf(fmaf(mx_block_sum(ss, red), inv, p.eps));
-    const uint64_t rs2 = pack2(rs, rs);
-    const int chunk_end = p.atoms * (NVF4 ? 4 : 8);
-    uint8_t* srow = p.S + mx_scale_row_at(r, p.atoms);
-#pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        const int chunk = i * (int)blockDim.x + (int)threadIdx.x;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i].p[j] = mul2(v[i].p[j], rs2);
-        if (p.pre) {
-            const Row16 w = mx_load16_any(p.pre, p.weight_type, 0, chunk * 16, cols, p.wvec);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i].p[j] = mul2(v[i].p[j], w.p[j]);
-        }
-        uint2 codes;
-        const uint32_t byte = mx_quantize16<NVF4>(v[i], p.c, codes);
-        mx_store_codes(p.Q + r * p.ldq, chunk * 16, cols, codes);
-        mx_store_scales<NVF4>(srow, chunk, chunk_end, cols, byte, lane);
     }
 }
 
 template <typename T, bool NVF4, int NC>
 cudaError_t mx_norm_launch(const MxNormParams& p, int threads, cudaStream_t st) {
-    return launch_pdl(mx_norm_kernel<T, NVF4, NC>, (int)p.rows, threads, 0, st, p);
+    const int64_t resident = (int64_t)p.sm_count * (NC == 1 ? 768 / threads : 1);
+    return launch_pdl(mx_norm_kernel<T, NVF4, NC>, (int)(p.rows < resident ? p.rows : resident), threads, 0, st, p);
 }
 
 template <typename T, bool NVF4>

@@ -304,8 +304,11 @@ def test_grouped_no_rows_at_all(h, kernel):
     grouped(h, [0, 0], 64, 64, qg.GEMM_NVFP4, synth.BF16, seed=7, extra=4)
 
 
+@pytest.mark.parametrize("pin", ["", "mx2_bn256"])
 @pytest.mark.parametrize("counts", [[1756, 764, 470, 333, 254, 204, 170, 145], [600, 0, 1, 255, 257, 512]])
-def test_grouped_prompt(h, counts):
+def test_grouped_prompt(h, monkeypatch, counts, pin):
+    if pin:
+        monkeypatch.setenv("GEMM_FORCE_KERNEL", pin)
     grouped(h, counts, 1280, 1024, qg.GEMM_NVFP4, synth.BF16, seed=8, alpha=0.125)
 
 
