@@ -116,6 +116,7 @@ int gemm_run_mx_grouped(gemm_handle_t h, const gemm_op_t* op, int32_t format, fl
  *   Q, S = y quantised as gemm_mx_quantize does (its tensor_scale included).
  * F NULL: r' = R, and O may be NULL.  F, R, O: row-major, one of f32 / f16 /
  * bf16, any ld; O may be R or F.  pre_weight NULL: 1.  cols at most 32768.
+ * Rows that no expert of expert_offsets holds get their r', but no Q and S.
  */
 typedef struct {
     int32_t format;         /* gemm_mx_format_t                                 */
@@ -128,6 +129,9 @@ typedef struct {
     int32_t gate_type;       /* GEMM_F32 / GEMM_F16 / GEMM_BF16                  */
     const void* gate;        /* or NULL                                          */
     int64_t gate_ld;         /* elements between rows of the gate; 0: one row for all */
+    const int32_t* expert_offsets; /* device int32[num_experts + 1]: rows sorted by expert, whose
+                                scales then start every expert on an atom row; or NULL */
+    int32_t num_experts;     /* 0 without expert_offsets                         */
 } gemm_mx_norm_t;
 
 int gemm_mx_norm_quantize(gemm_handle_t h, const gemm_mx_norm_t* op, const void* F, const gemm_layout_t* Fdesc,

@@ -87,7 +87,7 @@ class gemm_mx_norm_t(ctypes.Structure):
     _fields_ = [("format", ctypes.c_int32), ("tensor_scale", ctypes.c_float), ("eps", ctypes.c_float),
                 ("residual_scale", ctypes.c_float), ("post_weight", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
                 ("weight_type", ctypes.c_int32), ("gate_type", ctypes.c_int32), ("gate", ctypes.c_void_p),
-                ("gate_ld", ctypes.c_int64)]
+                ("gate_ld", ctypes.c_int64), ("expert_offsets", ctypes.c_void_p), ("num_experts", ctypes.c_int32)]
 
 
 _lib = None

@@ -500,6 +500,7 @@ int gemm_mx_norm_quantize(gemm_handle_t h, const gemm_mx_norm_t* op, const void*
         if ((weights && !ws) || (op->gate && !gs)) return (int)GEMM_ERR_UNSUPPORTED;
         if (!F && (op->post_weight || op->gate)) return (int)GEMM_ERR_INVALID_ARG;
         if (op->gate && op->gate_ld != 0 && op->gate_ld < cols) return (int)GEMM_ERR_INVALID_ARG;
+        if ((rc = check_experts(h, op->expert_offsets, op->num_experts))) return rc;
         if (rows == 0 || cols == 0) return (int)GEMM_OK;
         auto bad = [&](const void* ptr, int64_t n) { return !aligned(ptr, (uintptr_t)n) || !handle_device_pointer(h, ptr); };
         if (!R || !Q || !S || bad(R, es) || bad(Q, 16) || bad(S, 16)) return (int)GEMM_ERR_INVALID_ARG;
@@ -507,7 +508,7 @@ int gemm_mx_norm_quantize(gemm_handle_t h, const gemm_mx_norm_t* op, const void*
         if ((op->post_weight && bad(op->post_weight, ws)) || (op->pre_weight && bad(op->pre_weight, ws)) ||
             (op->gate && bad(op->gate, gs)))
             return (int)GEMM_ERR_INVALID_ARG;
-        if (S_size < (uint64_t)scale_bytes(op->format, rows, cols, 0)) return (int)GEMM_ERR_INVALID_ARG;
+        if (S_size < (uint64_t)scale_bytes(op->format, rows, cols, op->num_experts)) return (int)GEMM_ERR_INVALID_ARG;
         MxNormParams p;
         memset(&p, 0, sizeof p);
         p.F = F;
@@ -528,6 +529,8 @@ int gemm_mx_norm_quantize(gemm_handle_t h, const gemm_mx_norm_t* op, const void*
         p.gvec = row_alignment(op->gate, op->gate_ld, gs);
         p.atoms = (int32_t)mx_atoms(op->format, cols);
         p.sm_count = handle_sm_count(h);
+        p.offsets = op->expert_offsets;
+        p.num_experts = op->num_experts;
         p.eps = op->eps;
         p.residual_scale = op->residual_scale;
         p.c = mx_scale_const(op->tensor_scale);

@@ -63,6 +63,8 @@ struct MxNormParams {
     int32_t weight_type, gate_type;
     int64_t gate_ld;
     int32_t wvec, gvec;  // weights, gate: likewise
+    const int32_t* offsets;  // rows sorted by expert, or null
+    int32_t num_experts;
 };
 
 cudaError_t launch_mx_quantize(const MxQuantParams& p, cudaStream_t st);

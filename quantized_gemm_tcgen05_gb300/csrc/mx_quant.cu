@@ -27,8 +27,12 @@ __global__ void __launch_bounds__(32 * QWARPS, 8) mx_quantize_kernel(const __gri
     if (r >= p.rows) return;
     griddep_wait();
     const Raw16<T> raw = mx_load16(static_cast<const T*>(p.X) + blockIdx.z * p.x_bstride + r * p.ldx, chunk * 16, cols, p.vec);
-    const int64_t srow = p.offsets ? mx_expert_row(p.offsets, p.num_experts, r, lane) : r;
-    if (srow < 0) return;
+    int64_t srow = r;
+    if (p.offsets) {
+        const MxExpertSpan e = mx_expert_of(p.offsets, p.num_experts, r, lane);
+        if (!e.holds(r)) return;
+        srow = e.row0 + (r - e.lo);
+    }
     uint2 codes;
     const uint32_t byte = mx_quantize16<NVF4>(mx_values<T>(raw), p.c, codes);
     mx_store_codes(static_cast<uint8_t*>(p.Y) + blockIdx.z * p.q_bstride + r * p.ldq, chunk * 16, cols, codes);
@@ -53,73 +57,68 @@ struct E4M3Out {};  // the codes' own values
 
 constexpr int DROWS = 2;  // rows a warp of the inverse takes: it has so little to do for one
 
-// 16 bytes of codes a thread: 32 values.
+// A lane takes 16 codes from either half of 1024: its neighbours' follow directly,
+// so whatever the rows' alignment, a warp's accesses are contiguous.
 template <typename T, bool NVF4>
 __global__ void __launch_bounds__(32 * QWARPS) mx_dequantize_kernel(const __grid_constant__ MxQuantParams p) {
     griddep_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int r0 = (int)blockIdx.x * (QWARPS * DROWS) + warp;
-    const int c0 = ((int)blockIdx.y * 32 + lane) * 32, cols = (int)p.cols;
+    const int first = ((int)blockIdx.y * 64 + lane) * 16, cols = (int)p.cols;
     if (r0 >= p.rows) return;
     griddep_wait();
-    uint32_t w[DROWS][4];
+    uint2 w[DROWS][2];
 #pragma unroll
-    for (int j = 0; j < DROWS; ++j) {
-        const uint8_t* q = static_cast<const uint8_t*>(p.X) + blockIdx.z * p.q_bstride + (r0 + j * QWARPS) * p.ldq + c0 / 2;
-        w[j][0] = w[j][1] = w[j][2] = w[j][3] = 0;
-        if (r0 + j * QWARPS >= p.rows) continue;
-        if (c0 + 32 <= cols) {
-            const uint4 u = *reinterpret_cast<const uint4*>(q);
-            w[j][0] = u.x;
-            w[j][1] = u.y;
-            w[j][2] = u.z;
-            w[j][3] = u.w;
-        } else {
-            const int n = (cols - c0 + 1) / 2;
+    for (int j = 0; j < DROWS; ++j)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (i < n) w[j][i / 4] |= (uint32_t)q[i] << (8 * (i % 4));
+        for (int h = 0; h < 2; ++h) {
+            const int c0 = first + 512 * h;
+            const uint8_t* q = static_cast<const uint8_t*>(p.X) + blockIdx.z * p.q_bstride + (r0 + j * QWARPS) * p.ldq + c0 / 2;
+            w[j][h] = make_uint2(0, 0);
+            if (r0 + j * QWARPS >= p.rows) continue;
+            if (c0 + 16 <= cols) {
+                w[j][h] = *reinterpret_cast<const uint2*>(q);
+            } else if (c0 < cols) {
+                const int n = (cols - c0 + 1) / 2;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < n) (i < 4 ? w[j][h].x : w[j][h].y) |= (uint32_t)q[i] << (8 * (i % 4));
+            }
         }
-    }
+    MxExpertSpan e{0, p.rows, 0};
+    if (p.offsets) e = mx_expert_of(p.offsets, p.num_experts, r0, lane);
 #pragma unroll
     for (int j = 0; j < DROWS; ++j) {
         const int r = r0 + j * QWARPS;
         if (r >= p.rows) break;
-        const int64_t srow = p.offsets ? mx_expert_row(p.offsets, p.num_experts, r, lane) : r;
-        if (srow < 0 || c0 >= cols) continue;
-        if constexpr (std::is_same<T, E4M3Out>::value) {
-            uint8_t* out = static_cast<uint8_t*>(p.Y) + blockIdx.z * p.x_bstride + r * p.ldx + c0;
-            uint32_t v[8];
+        if (!e.holds(r)) e = mx_expert_of(p.offsets, p.num_experts, r, lane);
+        if (!e.holds(r)) continue;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = mx_codes_e4m3(w[j][i / 2] >> (16 * (i % 2)));
-            if (p.vec == 2 && c0 + 32 <= cols) {
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "r"(v[0]), "r"(v[1]),
-                             "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                             : "memory");
-            } else if (p.vec && c0 + 32 <= cols) {
-                *reinterpret_cast<uint4*>(out) = make_uint4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<uint4*>(out + 16) = make_uint4(v[4], v[5], v[6], v[7]);
+        for (int h = 0; h < 2; ++h) {
+            const int c0 = first + 512 * h;
+            if (c0 >= cols) break;
+            const uint2 u = w[j][h];
+            if constexpr (std::is_same<T, E4M3Out>::value) {
+                uint8_t* out = static_cast<uint8_t*>(p.Y) + blockIdx.z * p.x_bstride + r * p.ldx + c0;
+                const uint32_t v[4] = {mx_codes_e4m3(u.x), mx_codes_e4m3(u.x >> 16), mx_codes_e4m3(u.y), mx_codes_e4m3(u.y >> 16)};
+                if (p.vec && c0 + 16 <= cols) {
+                    *reinterpret_cast<uint4*>(out) = make_uint4(v[0], v[1], v[2], v[3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c0 + i < cols) out[i] = (uint8_t)(v[i / 4] >> (8 * (i % 4)));
+                }
             } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (c0 + i < cols) out[i] = (uint8_t)(v[i / 4] >> (8 * (i % 4)));
-            }
-        } else {
-            const uint8_t* sp = p.S + blockIdx.z * p.s_bstride + mx_scale_row_at(srow, p.atoms);
-            T* out = static_cast<T*>(p.Y) + blockIdx.z * p.x_bstride + r * p.ldx;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int ch = c0 + 16 * h;
-                if (ch >= cols) break;
-                const float s = mx_scale_value<NVF4>(sp[mx_block_at(ch / (NVF4 ? 16 : 32))]);
+                const uint8_t* sp = p.S + blockIdx.z * p.s_bstride + mx_scale_row_at(e.row0 + (r - e.lo), p.atoms);
+                const float s = mx_scale_value<NVF4>(sp[mx_block_at(c0 / (NVF4 ? 16 : 32))]);
                 Row16 v;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float2 f = mx_code_pair((w[j][2 * h + i / 4] >> (8 * (i % 4))) & 0xFFu);
+                    const float2 f = mx_code_pair(((i < 4 ? u.x : u.y) >> (8 * (i % 4))) & 0xFFu);
                     // code * scale is exact (2 + 4 significant bits); the product with g is rounded, then D
                     v.p[i] = pack2(f.x * s * p.c.g, f.y * s * p.c.g);
                 }
-                mx_store16(out, ch, cols, p.vec, mx_round<T>(v));
+                mx_store16(static_cast<T*>(p.Y) + blockIdx.z * p.x_bstride + r * p.ldx, c0, cols, p.vec, mx_round<T>(v));
             }
         }
     }
@@ -294,7 +293,13 @@ __global__ void __launch_bounds__(NC == 1 ? 256 : 512, NC == 1 ? 3 : 1) mx_norm_
         }
         const float rs = rsqrtf(fmaf(mx_block_sum(ss, red + 4), inv, p.eps));
         const uint64_t rs2 = pack2(rs, rs);
-        uint8_t* srow = p.S + mx_scale_row_at(r, p.atoms);
+        int64_t scale_row = r;
+        if (p.offsets) {
+            const MxExpertSpan e = mx_expert_of(p.offsets, p.num_experts, r, lane);
+            if (!e.holds(r)) continue;  // (O is written, Q and S are not)
+            scale_row = e.row0 + (r - e.lo);
+        }
+        uint8_t* srow = p.S + mx_scale_row_at(scale_row, p.atoms);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const int chunk = i * (int)blockDim.x + (int)threadIdx.x;

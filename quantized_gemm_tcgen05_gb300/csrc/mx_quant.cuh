@@ -324,9 +324,16 @@ __device__ __forceinline__ void mx_store_scales(uint8_t* S, int chunk, int chunk
     if (lane % (4 * PER) == 0 && chunk < chunk_end) *reinterpret_cast<uint32_t*>(S + mx_block_at(chunk / PER)) = w;
 }
 
-// Warp-wide: the scale row of token row r when rows are sorted by expert (each
-// expert starts on an atom row), or -1 when no expert holds it.
-__device__ __forceinline__ int64_t mx_expert_row(const int32_t* off, int32_t E, int64_t r, int lane) {
+// Rows lo .. hi - 1 of one expert, and the scale row of the first (an expert
+// starts on an atom row).
+struct MxExpertSpan {
+    int64_t lo, hi, row0;
+    __device__ __forceinline__ bool holds(int64_t r) const { return r >= lo && r < hi; }
+};
+
+// Warp-wide: the expert that holds row r of rows sorted by expert; an empty span
+// when none does.
+__device__ __forceinline__ MxExpertSpan mx_expert_of(const int32_t* off, int32_t E, int64_t r, int lane) {
     int64_t tiles = 0;
     for (int32_t e0 = 0; e0 < E; e0 += 32) {
         const int32_t e = e0 + lane;
@@ -338,9 +345,11 @@ __device__ __forceinline__ int64_t mx_expert_row(const int32_t* off, int32_t E, 
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
         tiles += n;
-        if (hit) return tiles * MX_ATOM_ROWS + (r - __shfl_sync(0xFFFFFFFFu, lo, first));
+        if (hit)
+            return MxExpertSpan{__shfl_sync(0xFFFFFFFFu, lo, first), __shfl_sync(0xFFFFFFFFu, hi, first),
+                                tiles * MX_ATOM_ROWS};
     }
-    return -1;
+    return MxExpertSpan{0, 0, 0};
 }
 
 }  // namespace qg

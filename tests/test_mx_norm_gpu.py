@@ -180,3 +180,32 @@ def test_zero_and_nan_rows(h):
     assert nan == [False, True, False]
     check_codes_rows = torch.isnan(out).any(-1).cpu().tolist()
     assert check_codes_rows == [False, True, False]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("counts,extra", [([3, 0, 130, 1], 0), ([0, 5], 2), ([1] * 40, 0)])
+def test_rows_by_expert(h, fmt, counts, extra):
+    # the same row by row, scales on the experts' own atom rows
+    rows, cols = sum(counts) + extra, 272
+    f, r = data(rows, cols, torch.bfloat16, 1), data(rows, cols, torch.bfloat16, 2)
+    pre = data(1, cols, torch.bfloat16, 3)[0]
+    want, o = run(h, fmt, f, r, pre=pre)
+    off = np.concatenate([[0], np.cumsum(counts)])
+    offd = torch.from_numpy(off.astype(np.int32)).cuda()
+    e = qg.MxOperand(fmt, rows, cols, num_experts=len(counts))
+    e.codes.fill_(0xAA)
+    n = qg.gemm_mx_norm_t(format=fmt, tensor_scale=1.0, eps=1e-5, residual_scale=0.7, pre_weight=qg.ptr(pre),
+                          weight_type=qg.GEMM_BF16, expert_offsets=qg.ptr(offd), num_experts=len(counts))
+    out = torch.empty_like(want)
+    lay = qg.row_major(r)
+    rc = qg.gemm_mx_norm_quantize(h, n, qg.ptr(f), qg.row_major(f), qg.ptr(r), lay, qg.ptr(out), qg.row_major(out), *e.args(),
+                                  qg.current_stream())
+    assert rc == 0
+    held = sum(counts)
+    assert torch.equal(out, want) and torch.equal(e.codes[:held], o.codes[:held])
+    assert bool((e.codes[held:] == 0xAA).all())
+    nb = R.ceil(cols, R.BLOCK[fmt])
+    atoms, j = R.ceil(nb, 4), np.arange(nb)[None]
+    a = e.scales.cpu().numpy()[R.scale_at(R.expert_rows(off)[:, None], j, atoms)]
+    b = o.scales.cpu().numpy()[R.scale_at(np.arange(held)[:, None], j, atoms)]
+    assert np.array_equal(a, b)

@@ -157,7 +157,7 @@ def test_norm_refusals(h):
     for change, want in [
         (dict(op=n(format=0)), UNS), (dict(op=n(tensor_scale=0.0)), INV), (dict(op=n(eps=-1.0)), INV),
         (dict(op=n(eps=float("nan"))), INV), (dict(op=n(residual_scale=float("inf"))), INV),
-        (dict(op=n(weight_type=qg.GEMM_S8)), UNS), (dict(op=n(gate_type=qg.GEMM_S8)), UNS), (dict(op=n(gate_ld=64)), INV),
+        (dict(op=n(weight_type=qg.GEMM_S8)), UNS), (dict(op=n(gate_type=qg.GEMM_S8)), UNS), (dict(op=n(gate_ld=64)), INV), (dict(op=n(num_experts=1)), INV), (dict(op=n(expert_offsets=qg.ptr(w))), INV),
         (dict(op=n(pre_weight=qg.ptr(w) + 1)), INV), (dict(F=None), INV), (dict(O=None), INV), (dict(R=None), INV),
         (dict(Fdesc=None), INV), (dict(Rdesc=None), INV), (dict(Odesc=ld(rl, type=qg.GEMM_F32, ld=128)), UNS),
         (dict(Fdesc=ld(rl, type=qg.GEMM_BF16)), UNS), (dict(Fdesc=ld(rl, rows=7)), INV), (dict(Qdesc=ld(ql, ld=144)), INV),
