@@ -2,6 +2,7 @@
 // one row, held by one thread, to D.
 #pragma once
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "mx_gemm.h"
 
 namespace qg {
@@ -27,18 +28,44 @@ __device__ __forceinline__ void mx_prefetch_c(const EpiParams& e, int64_t m, int
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p + count * es - es));
 }
 
-// 64 accumulator columns (TMEM address ta, this warp's 32 rows, a row per lane)
-// as finished 16-bit values: w[j] holds columns 2 j and 2 j + 1.
+// x * Phi(x) of two values for a 16-bit D.  erf(z) = z P(y), y = z^2, with P the
+// Chebyshev interpolant of degree 15 of erf(sqrt y) / sqrt y on [0, 3.9^2] in
+// u = 2 y / 3.9^2 - 1 (beyond, erf is 1 to 4e-8), all in fp32: |error| <= 1.5e-7 |x|,
+// where erff's 1 + erf leaves 6e-8 |x|.  Twenty packed operations for two values
+// against some thirty apiece: with erff the epilogue held the next tile's main
+// loop up for two thirds of its own length.
+__device__ __forceinline__ uint64_t mx_gelu2(uint64_t x) {
+    constexpr float c[16] = {-8.173368988e-04f, 1.944994321e-03f, -1.153882593e-03f, 1.828000415e-03f,
+                             -7.548484486e-03f, 1.368475612e-02f, -1.924535446e-02f, 2.906646766e-02f,
+                             -4.289200157e-02f, 5.792884529e-02f, -7.378227264e-02f, 9.066636860e-02f,
+                             -1.095340773e-01f, 1.346912831e-01f, -1.810110509e-01f, 3.625839651e-01f};
+    constexpr float top = 3.9f;
+    float a, b;
+    unpack2(mul2(x, pack2(0.70710678118654752f, 0.70710678118654752f)), a, b);
+    const uint64_t z = pack2(fminf(fmaxf(a, -top), top), fminf(fmaxf(b, -top), top));
+    const uint64_t u = fma2(mul2(z, z), pack2(2.0f / (top * top), 2.0f / (top * top)), pack2(-1.0f, -1.0f));
+    uint64_t r = pack2(c[0], c[0]);
+#pragma unroll
+    for (int i = 1; i < 16; ++i) r = fma2(r, u, pack2(c[i], c[i]));
+    const uint64_t h = mul2(x, pack2(0.5f, 0.5f));
+    return fma2(h, mul2(r, z), h);  // NaN stays NaN through h
+}
+
+// 64 accumulator columns (TMEM address ta, this warp's 32 rows, a row per lane).
+__device__ __forceinline__ void mx_load64(uint32_t ta, float (&v)[2][32]) {
+    tmem_load_chunk<32>(ta, v[0]);
+    tmem_load_chunk<32>(ta + 32, v[1]);
+}
+
+// The same as finished 16-bit values: w[j] holds columns n0 + 2 j and 2 j + 1.
 template <int ACT, int DT>
-__device__ __forceinline__ void mx_pack64(const EpiParams& e, float alpha, uint32_t ta, int64_t n0, uint32_t (&w)[32],
-                                          int lane) {
+__device__ __forceinline__ void mx_pack64(const EpiParams& e, float alpha, const float (&v)[2][32], int64_t n0,
+                                          uint32_t (&w)[32], int lane) {
     EpiArith ar = epi_arith(e);
     ar.alpha = alpha;
     ar.beta = 0.0f;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        float v[32];
-        tmem_load_chunk<32>(ta + 32 * c, v);
         const float bl = ACT >= 0 ? bias_at(ar, n0 + 32 * c + lane) : 0.0f;
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
@@ -47,7 +74,14 @@ __device__ __forceinline__ void mx_pack64(const EpiParams& e, float alpha, uint3
                 b0 = __shfl_sync(0xFFFFFFFFu, bl, 2 * j);
                 b1 = __shfl_sync(0xFFFFFFFFu, bl, 2 * j + 1);
             }
-            const float x0 = epi_value<ACT>(ar, v[2 * j], 0.0f, b0), x1 = epi_value<ACT>(ar, v[2 * j + 1], 0.0f, b1);
+            float x0, x1;
+            if constexpr (ACT == 2) {
+                const uint64_t a2 = pack2(ar.alpha, ar.alpha);
+                unpack2(mx_gelu2(fma2(a2, pack2(v[c][2 * j], v[c][2 * j + 1]), pack2(b0, b1))), x0, x1);
+            } else {
+                x0 = epi_value<ACT>(ar, v[c][2 * j], 0.0f, b0);
+                x1 = epi_value<ACT>(ar, v[c][2 * j + 1], 0.0f, b1);
+            }
             if constexpr (DT == DT_BF16) {
                 const __nv_bfloat162 h = __floats2bfloat162_rn(x0, x1);
                 w[16 * c + j] = *reinterpret_cast<const uint32_t*>(&h);
@@ -57,6 +91,15 @@ __device__ __forceinline__ void mx_pack64(const EpiParams& e, float alpha, uint3
             }
         }
     }
+}
+__device__ __forceinline__ void mx_pack64_any(const EpiParams& e, float alpha, const float (&v)[2][32], int64_t n0,
+                                              uint32_t (&w)[32], int lane) {
+    with_epi_act(e, [&](auto act) {
+        if (e.d_type == DT_BF16)
+            mx_pack64<decltype(act)::value, DT_BF16>(e, alpha, v, n0, w, lane);
+        else
+            mx_pack64<decltype(act)::value, DT_F16>(e, alpha, v, n0, w, lane);
+    });
 }
 
 // The 64 packed columns through `stage` (32 rows of 128 bytes, 16-byte chunks
@@ -125,7 +168,12 @@ __device__ __forceinline__ void mx_store_block_t(const EpiParams& ep, bool vec32
 #pragma unroll
             for (int t = 0; t < PER; ++t) {
                 const float b = ACT >= 0 ? __shfl_sync(0xFFFFFFFFu, bl, PER * q + t) : 0.0f;
-                x[t] = epi_value<ACT>(ar, v[PER * q + t], cv[t], b);
+                // (GELU of a 16-bit D: below, two values at a time)
+                x[t] = epi_value<ACT == 2 && DT != DT_F32 ? 0 : ACT>(ar, v[PER * q + t], cv[t], b);
+            }
+            if constexpr (ACT == 2 && DT != DT_F32) {
+#pragma unroll
+                for (int t = 0; t < PER; t += 2) unpack2(mx_gelu2(pack2(x[t], x[t + 1])), x[t], x[t + 1]);
             }
             uint32_t w[8];
 #pragma unroll

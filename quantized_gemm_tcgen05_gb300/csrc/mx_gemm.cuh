@@ -287,13 +287,10 @@ __global__ void __launch_bounds__(MX_THREADS, 2)
             bool done = false;
             if constexpr (BN == 128) {
                 if (P.vec32 && P.epi.d_type != DT_F32 && P.epi.beta == 0.0f && nh + 64 <= P.epi.N) {
+                    float v[2][32];
                     uint32_t w[32];
-                    with_epi_act(P.epi, [&](auto act) {
-                        if (P.epi.d_type == DT_BF16)
-                            mx_pack64<decltype(act)::value, DT_BF16>(P.epi, alpha, tb, nh, w, lane);
-                        else
-                            mx_pack64<decltype(act)::value, DT_F16>(P.epi, alpha, tb, nh, w, lane);
-                    });
+                    mx_load64(tb, v);
+                    mx_pack64_any(P.epi, alpha, v, nh, w, lane);
                     mx_stage64(buf, w, lane);
                     __syncwarp();
                     mx_store64(buf, static_cast<uint16_t*>(P.epi.D) + m0 * P.epi.ldd + nh, P.epi.ldd, wrows, lane);

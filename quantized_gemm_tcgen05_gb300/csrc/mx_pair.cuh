@@ -322,28 +322,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_PAIR_THREADS, 1)
             const uint32_t ta = tmem + 128 * half + ((uint32_t)(ew * 32) << 16);
             const bool packed = P.vec32 && P.epi.d_type != DT_F32 && P.epi.beta == 0.0f && n0 + 128 <= P.epi.N;
             if (packed && rows > 0) {
-                // a 16-bit D without C: half of the finished values wait in shared
-                // memory, half in registers, so the accumulator is given back
-                // before the first store
+                // a 16-bit D without C: half of the values wait finished in shared
+                // memory, half as they are in registers, so the accumulator is given
+                // back before the second half is worked on and before the first store
+                float v[2][32];
                 uint32_t w[32];
                 uint8_t* buf = reinterpret_cast<uint8_t*>(stage);
-                with_epi_act(P.epi, [&](auto act) {
-                    constexpr int ACT = decltype(act)::value;
-                    if (P.epi.d_type == DT_BF16) {
-                        mx_pack64<ACT, DT_BF16>(P.epi, alpha, ta, n0, w, lane);
-                        mx_stage64(buf, w, lane);
-                        mx_pack64<ACT, DT_BF16>(P.epi, alpha, ta + 64, n0 + 64, w, lane);
-                    } else {
-                        mx_pack64<ACT, DT_F16>(P.epi, alpha, ta, n0, w, lane);
-                        mx_stage64(buf, w, lane);
-                        mx_pack64<ACT, DT_F16>(P.epi, alpha, ta + 64, n0 + 64, w, lane);
-                    }
-                });
+                mx_load64(ta, v);
+                mx_pack64_any(P.epi, alpha, v, n0, w, lane);
+                mx_stage64(buf, w, lane);
+                mx_load64(ta + 64, v);
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote_relaxed(l_tempty);
                 uint16_t* d = static_cast<uint16_t*>(P.epi.D) + m0 * P.epi.ldd + n0;
                 mx_store64(buf, d, P.epi.ldd, rows, lane);
+                mx_pack64_any(P.epi, alpha, v, n0 + 64, w, lane);
                 __syncwarp();
                 mx_stage64(buf, w, lane);
                 __syncwarp();
