@@ -7,6 +7,12 @@
 
 namespace qg {
 
+// Checked build: rows m0 .. + rows - 1, columns n0 .. + cols - 1 inside D (and C).
+__device__ __forceinline__ bool mx_block_in_bounds(const EpiParams& e, int64_t m0, int rows, int64_t n0, int64_t cols) {
+    if (!elem_in_bounds(e, m0 * e.ldd + n0, (rows - 1) * e.ldd + cols, e.d_extent)) return false;
+    return e.beta == 0.0f || elem_in_bounds(e, m0 * e.ldc + n0, (rows - 1) * e.ldc + cols, e.c_extent);
+}
+
 // 32-byte global accesses: a whole sector per lane.
 __device__ __forceinline__ void ld32(const void* p, uint32_t (&w)[8]) {
     asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -134,6 +140,7 @@ template <int ACT, int DT>
 __device__ __forceinline__ void mx_store_block_t(const EpiParams& ep, bool vec32, float alpha, int64_t m0,
                                                  int rows, int64_t n0, float (&v)[32], float* stage, int lane) {
     const EpiParams e = ep;
+    if (!mx_block_in_bounds(e, m0, rows, n0, e.N - n0 < 32 ? e.N - n0 : 32)) return;
     EpiArith ar = epi_arith(e);
     ar.alpha = alpha;
     const int64_t m = m0 + lane;
@@ -228,9 +235,9 @@ __device__ __forceinline__ void mx_store_block(const EpiParams& e, bool vec32, f
 }
 
 // Warp-wide: block b (of `bm` rows, a multiple of 128) of rows sorted by
-// expert -> expert, its first row, its rows, and the scale atom row it starts
-// on.  Returns false past the last block.
-__device__ __forceinline__ bool mx_expert_block(const int32_t* off, int32_t E, int bm, int64_t b, int lane,
+// expert -> expert, its first row, its rows (those below M, the rows there are),
+// and the scale atom row it starts on.  Returns false past the last block.
+__device__ __forceinline__ bool mx_expert_block(const int32_t* off, int32_t E, int64_t M, int bm, int64_t b, int lane,
                                                 int* expert, int64_t* row0, int* rows, int64_t* atom_row) {
     int64_t blocks = 0, tiles = 0;
     for (int32_t e0 = 0; e0 < E; e0 += 32) {
@@ -254,7 +261,8 @@ __device__ __forceinline__ bool mx_expert_block(const int32_t* off, int32_t E, i
             const int64_t left = __shfl_sync(0xFFFFFFFFu, m, l) - q * bm;
             *expert = e0 + l;
             *row0 = __shfl_sync(0xFFFFFFFFu, lo, l) + q * bm;
-            *rows = (int)(left < bm ? left : bm);
+            const int64_t room = M - *row0;
+            *rows = *row0 < 0 || room < 0 ? 0 : (int)(left < bm ? (left < room ? left : room) : (bm < room ? bm : room));
             *atom_row = tiles + __shfl_sync(0xFFFFFFFFu, pt - nt, l) + q * (bm / MX_ATOM_ROWS);
             return true;
         }

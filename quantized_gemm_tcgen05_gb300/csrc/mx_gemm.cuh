@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(MX_THREADS, 2)
     bool live = true;
     float alpha = P.epi.alpha;
     if (P.offsets) {
-        live = mx_expert_block(P.offsets, P.num_experts, 128, tm, lane, &expert, &row0, &rows, &atom_row);
+        live = mx_expert_block(P.offsets, P.num_experts, P.epi.M, 128, tm, lane, &expert, &row0, &rows, &atom_row);
         if (live && P.expert_alpha) alpha *= P.expert_alpha[expert];
     } else {
         row0 = tm * 128;
@@ -286,7 +286,8 @@ __global__ void __launch_bounds__(MX_THREADS, 2)
             const int64_t m0 = row0 + ew * 32, nh = n0 + half * (BN / 2);
             bool done = false;
             if constexpr (BN == 128) {
-                if (P.vec32 && P.epi.d_type != DT_F32 && P.epi.beta == 0.0f && nh + 64 <= P.epi.N) {
+                if (P.vec32 && P.epi.d_type != DT_F32 && P.epi.beta == 0.0f && nh + 64 <= P.epi.N &&
+                    mx_block_in_bounds(P.epi, m0, wrows, nh, 64)) {
                     float v[2][32];
                     uint32_t w[32];
                     mx_load64(tb, v);
@@ -367,6 +368,7 @@ __global__ void __launch_bounds__(MX_THREADS, 2)
                 const float a4[4] = {sum.x, sum.y, sum.z, sum.w};
                 float x[4];
                 const int have = e.N - n < 4 ? (int)(e.N - n) : 4;
+                if (!mx_block_in_bounds(e, m, 1, n, have)) continue;
                 with_epi_act(e, [&](auto act) {
                     constexpr int ACT = decltype(act)::value;
 #pragma unroll

@@ -76,7 +76,7 @@ __device__ __forceinline__ bool mx_pair_tile(const MxGemmParams& P, int64_t bloc
     const int64_t b = t % blocks;
     o.n0 = t / blocks * 256;
     o.expert = 0;
-    if (P.offsets) return mx_expert_block(P.offsets, P.num_experts, 256, b, lane, &o.expert, &o.row0, &o.rows, &o.atom_row);
+    if (P.offsets) return mx_expert_block(P.offsets, P.num_experts, P.epi.M, 256, b, lane, &o.expert, &o.row0, &o.rows, &o.atom_row);
     o.row0 = b * 256;
     o.rows = (int)(P.epi.M - o.row0 < 256 ? P.epi.M - o.row0 : 256);
     o.atom_row = 2 * b;
@@ -321,7 +321,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_PAIR_THREADS, 1)
             tc_fence_after_sync();
             const uint32_t ta = tmem + 128 * half + ((uint32_t)(ew * 32) << 16);
             const bool packed = P.vec32 && P.epi.d_type != DT_F32 && P.epi.beta == 0.0f && n0 + 128 <= P.epi.N;
-            if (packed && rows > 0) {
+            if (packed && rows > 0 && mx_block_in_bounds(P.epi, m0, rows, n0, 128)) {
                 // a 16-bit D without C: half of the values wait finished in shared
                 // memory, half as they are in registers, so the accumulator is given
                 // back before the second half is worked on and before the first store

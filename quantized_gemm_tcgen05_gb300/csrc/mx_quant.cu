@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(32 * QWARPS, 8) mx_quantize_kernel(const __gri
     const Raw16<T> raw = mx_load16(static_cast<const T*>(p.X) + blockIdx.z * p.x_bstride + r * p.ldx, chunk * 16, cols, p.vec);
     int64_t srow = r;
     if (p.offsets) {
-        const MxExpertSpan e = mx_expert_of(p.offsets, p.num_experts, r, lane);
+        const MxExpertSpan e = mx_expert_of(p.offsets, p.num_experts, p.rows, r, lane);
         if (!e.holds(r)) return;
         srow = e.row0 + (r - e.lo);
     }
@@ -86,12 +86,12 @@ __global__ void __launch_bounds__(32 * QWARPS) mx_dequantize_kernel(const __grid
             }
         }
     MxExpertSpan e{0, p.rows, 0};
-    if (p.offsets) e = mx_expert_of(p.offsets, p.num_experts, r0, lane);
+    if (p.offsets) e = mx_expert_of(p.offsets, p.num_experts, p.rows, r0, lane);
 #pragma unroll
     for (int j = 0; j < DROWS; ++j) {
         const int r = r0 + j * QWARPS;
         if (r >= p.rows) break;
-        if (!e.holds(r)) e = mx_expert_of(p.offsets, p.num_experts, r, lane);
+        if (!e.holds(r)) e = mx_expert_of(p.offsets, p.num_experts, p.rows, r, lane);
         if (!e.holds(r)) continue;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(NC == 1 ? 256 : 512, NC == 1 ? 3 : 1) mx_norm_
         const uint64_t rs2 = pack2(rs, rs);
         int64_t scale_row = r;
         if (p.offsets) {
-            const MxExpertSpan e = mx_expert_of(p.offsets, p.num_experts, r, lane);
+            const MxExpertSpan e = mx_expert_of(p.offsets, p.num_experts, p.rows, r, lane);
             if (!e.holds(r)) continue;  // (O is written, Q and S are not)
             scale_row = e.row0 + (r - e.lo);
         }

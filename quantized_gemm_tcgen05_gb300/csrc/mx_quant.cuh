@@ -306,7 +306,8 @@ __device__ __forceinline__ void mx_store_scales(uint8_t* S, int chunk, int chunk
 }
 
 // Rows lo .. hi - 1 of one expert, and the scale row of the first (an expert
-// starts on an atom row).
+// starts on an atom row).  Offsets that are no partition of the rows cannot lead
+// past the scales: a span beyond the `rows` / 128 + E atom rows is empty.
 struct MxExpertSpan {
     int64_t lo, hi, row0;
     __device__ __forceinline__ bool holds(int64_t r) const { return r >= lo && r < hi; }
@@ -314,7 +315,7 @@ struct MxExpertSpan {
 
 // Warp-wide: the expert that holds row r of rows sorted by expert; an empty span
 // when none does.
-__device__ __forceinline__ MxExpertSpan mx_expert_of(const int32_t* off, int32_t E, int64_t r, int lane) {
+__device__ __forceinline__ MxExpertSpan mx_expert_of(const int32_t* off, int32_t E, int64_t rows, int64_t r, int lane) {
     int64_t tiles = 0;
     for (int32_t e0 = 0; e0 < E; e0 += 32) {
         const int32_t e = e0 + lane;
@@ -326,9 +327,10 @@ __device__ __forceinline__ MxExpertSpan mx_expert_of(const int32_t* off, int32_t
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
         tiles += n;
-        if (hit)
-            return MxExpertSpan{__shfl_sync(0xFFFFFFFFu, lo, first), __shfl_sync(0xFFFFFFFFu, hi, first),
-                                tiles * MX_ATOM_ROWS};
+        if (hit) {
+            const MxExpertSpan s{__shfl_sync(0xFFFFFFFFu, lo, first), __shfl_sync(0xFFFFFFFFu, hi, first), tiles * MX_ATOM_ROWS};
+            return s.lo >= 0 && tiles + (r - s.lo) / MX_ATOM_ROWS < rows / MX_ATOM_ROWS + E ? s : MxExpertSpan{0, 0, 0};
+        }
     }
     return MxExpertSpan{0, 0, 0};
 }

@@ -295,6 +295,28 @@ def test_grouped_types_c_and_rows_past_the_experts(h, kernel, d):
     grouped(h, [20, 0, 57], 128, 1500, qg.GEMM_MXFP4, d, seed=5, alpha=2.0 ** -8, with_expert_alpha=False, extra=9)
 
 
+def test_offsets_past_the_rows_write_nothing_beyond_them(h, kernel):
+    # offsets that promise more rows than A and D have: the rows there are come
+    # out right, and nothing after them is touched
+    fmt, n, k, have = qg.GEMM_NVFP4, 128, 256, 150
+    rng = np.random.default_rng(9)
+    off = np.array([0, 40, 400])
+    held = R.expert_rows([0, 40, have])
+    a = Operand(rng, have, k, fmt, row=held, tiles=have // 128 + 2)
+    w = [Operand(rng, n, k, fmt) for _ in range(2)]
+    packed, scales = torch.stack([x.packed for x in w]), torch.cat([x.scales for x in w])
+    offd = dev(off.astype(np.int32))
+    buf = torch.full((450, n), 5.0, device="cuda")
+    rc = qg.gemm_run_mx_grouped(h, qg.gemm_op_t(), fmt, 1.0, None, qg.ptr(a.packed), qg.mx_layout(a.packed, k),
+                                qg.ptr(a.scales), a.scales.numel(), qg.ptr(packed), qg.mx_layout_b(packed, k),
+                                qg.ptr(scales), scales.numel(), 0.0, None, None, qg.ptr(buf),
+                                qg.layout(synth.F32, 0, have, n, n), qg.ptr(offd), 2, qg.current_stream())
+    assert rc == 0
+    for e, s in ((0, slice(0, 40)), (1, slice(40, have))):
+        check(buf[s], a.values[s] @ w[e].values.T, np.abs(a.values[s]) @ np.abs(w[e].values).T, synth.F32)
+    assert bool((buf[have:] == 5).all())
+
+
 @pytest.mark.parametrize("splits", [1, 2, 4])
 def test_grouped_k_slices(h, splits):
     grouped(h, [3, 150, 0, 20], 256, 2048, qg.GEMM_NVFP4, synth.F32, seed=6, op=qg.gemm_op_t(splitk=splits))
