@@ -27,6 +27,9 @@ int row_alignment(const void* p, int64_t ld, int64_t element) {
     if (!p) return 2;
     return aligned(p, 32) && ld * element % 32 == 0 ? 2 : aligned(p, 16) && ld * element % 16 == 0 ? 1 : 0;
 }
+const void* past(const void* p, int64_t n, int64_t element) {
+    return p ? static_cast<const char*>(p) + n * element : nullptr;
+}
 bool known_format(int32_t f) { return f == GEMM_MXFP4 || f == GEMM_NVFP4; }
 int64_t float_size(int32_t t) { return t == GEMM_F32 ? 4 : (t == GEMM_F16 || t == GEMM_BF16) ? 2 : 0; }
 
@@ -427,6 +430,7 @@ int gemm_mx_quantize(gemm_handle_t h, int32_t format, float tensor_scale, const 
                                     num_experts, false, &p);
         if (rc || p.rows == 0 || p.cols == 0) return rc;
         p.X = X;
+        p.x_end = past(X, (p.num - 1) * p.x_bstride + (p.rows - 1) * p.ldx + p.cols, float_size(Xdesc->type));
         p.Y = Q;
         p.S = static_cast<uint8_t*>(S);
         return status_of(launch_mx_quantize(p, reinterpret_cast<cudaStream_t>(stream)));
@@ -540,6 +544,11 @@ int gemm_mx_norm_quantize(gemm_handle_t h, const gemm_mx_norm_t* op, const void*
         p.weight_type = op->weight_type;
         p.gate_type = op->gate_type;
         p.gate_ld = op->gate_ld;
+        p.f_end = past(F, (rows - 1) * p.ldf + cols, es);
+        p.r_end = past(R, (rows - 1) * p.ldr + cols, es);
+        p.post_end = past(p.post, cols, ws);
+        p.pre_end = past(p.pre, cols, ws);
+        p.gate_end = past(p.gate, (rows - 1) * p.gate_ld + cols, gs);
         return status_of(launch_mx_norm(p, reinterpret_cast<cudaStream_t>(stream)));
     });
 }

@@ -32,6 +32,7 @@ inline MxScaleConst mx_scale_const(float g) { return MxScaleConst{g, 6.0f * g, 1
 // Quantisation and its inverse: one matrix of `rows` x `cols`, or `num` of them.
 struct MxQuantParams {
     const void* X;  // values in (quantise); codes in (dequantise)
+    const void* x_end;  // quantise: past the last value
     void* Y;        // codes out; values out
     uint8_t* S;     // scales
     int64_t rows, cols;
@@ -50,6 +51,7 @@ struct MxQuantParams {
 
 struct MxNormParams {
     const void *F, *R;
+    const void *f_end, *r_end, *post_end, *pre_end, *gate_end;  // past the last value of each
     void* O;
     uint8_t *Q, *S;
     int64_t rows, cols, ldf, ldr, ldo, ldq;  // ldq in bytes

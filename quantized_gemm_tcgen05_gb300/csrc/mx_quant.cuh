@@ -9,6 +9,88 @@
 
 namespace qg {
 
+// ---- rows that start anywhere -----------------------------------------------
+//
+// A lane's 16 values are W words (W = 4, 8 or 16) of a row that need not start on
+// a 16-byte boundary; the boundary's distance is the same for every lane of the
+// warp.  Loads take the 16-byte granules that hold the words and shift; stores
+// shift the warp's words onto the granules, every lane completing its last one
+// from its neighbour.  Element by element instead, a warp's accesses touch each
+// sector sixteen times.
+
+// out = the W words that start `bytes` (0 .. 15, the same in every lane) into c.
+template <int W>
+__device__ __forceinline__ void mx_shift_words(uint32_t (&c)[W + 4], int bytes, uint32_t (&out)[W]) {
+    if (bytes & 4) {
+#pragma unroll
+        for (int i = 0; i < W + 3; ++i) c[i] = c[i + 1];
+    }
+    if (bytes & 8) {
+#pragma unroll
+        for (int i = 0; i < W + 2; ++i) c[i] = c[i + 2];
+    }
+#pragma unroll
+    for (int i = 0; i < W; ++i) out[i] = __funnelshift_r(c[i], c[i + 1], (bytes & 3) * 8);
+}
+
+// Whether the granules that hold [p, p + bytes) lie inside [lo, hi).
+__device__ __forceinline__ bool mx_granules_inside(const void* p, int bytes, const void* lo, const void* hi) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), first = a & ~uintptr_t(15), last = (a + bytes + 15) & ~uintptr_t(15);
+    return first >= reinterpret_cast<uintptr_t>(lo) && last <= reinterpret_cast<uintptr_t>(hi);
+}
+
+// W words from p (granules inside the tensor).
+template <int W>
+__device__ __forceinline__ void mx_load_words(const void* p, uint32_t (&out)[W]) {
+    const int o = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+    const uint4* g = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - o);
+    uint32_t c[W + 4];
+#pragma unroll
+    for (int i = 0; i < W / 4 + 1; ++i) {
+        uint4 u = make_uint4(0, 0, 0, 0);
+        if (i < W / 4 || o) u = g[i];
+        c[4 * i] = u.x;
+        c[4 * i + 1] = u.y;
+        c[4 * i + 2] = u.z;
+        c[4 * i + 3] = u.w;
+    }
+    mx_shift_words<W>(c, o, out);
+}
+
+// Warp-wide: every lane with `mine` stores its W words at p, lanes' words one after
+// another; the lanes with `mine` are the first ones of the warp.  T: the element
+// (p is aligned to it), by which the ends of the warp's run are stored.
+template <typename T, int W>
+__device__ __forceinline__ void mx_store_words(void* p, const uint32_t (&w)[W], bool mine, int lane) {
+    const int o = (int)(reinterpret_cast<uintptr_t>(p) & 15), a = (16 - o) & 15;  // bytes up to the first boundary
+    uint32_t c[W + 4], out[W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) c[i] = w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[W + i] = __shfl_down_sync(0xFFFFFFFFu, w[i], 1);
+    const bool next = __shfl_down_sync(0xFFFFFFFFu, mine ? 1 : 0, 1) && lane < 31;
+    if (!mine) return;
+    mx_shift_words<W>(c, a, out);
+    uint4* g = reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(p) + a);
+#pragma unroll
+    for (int i = 0; i < W / 4; ++i)
+        if (i < W / 4 - 1 || next || a == 0) g[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);
+    if (a == 0) return;
+    constexpr int ES = (int)sizeof(T), PER = 4 / ES;  // elements of a word
+    auto element = [&](int i) {
+        uint32_t v = 0;
+#pragma unroll
+        for (int k = 0; k < W; ++k)
+            if (k == i / PER) v = w[k];
+        return (T)(v >> (8 * ES * (i % PER)));
+    };
+    T* e = static_cast<T*>(p);
+    if (lane == 0)  // up to the first boundary of the run
+        for (int i = 0; i < a / ES; ++i) e[i] = element(i);
+    if (!next)  // past its last one
+        for (int i = (4 * W - o) / ES; i < 4 * W / ES; ++i) e[i] = element(i);
+}
+
 // Sixteen values as eight packed pairs.
 struct Row16 {
     uint64_t p[8];
@@ -19,6 +101,7 @@ template <typename T>
 struct MxIn;
 template <>
 struct MxIn<float> {
+    using Bits = uint32_t;
     static constexpr int LOADS = 4;
     static __device__ __forceinline__ float one(const float* p) { return *p; }
     static __device__ __forceinline__ void st(float* p, float x) { *p = x; }
@@ -35,6 +118,7 @@ struct MxIn<float> {
 };
 template <>
 struct MxIn<__half> {
+    using Bits = uint16_t;
     static constexpr int LOADS = 2;
     static __device__ __forceinline__ float one(const __half* p) { return __half2float(*p); }
     static __device__ __forceinline__ void st(__half* p, float x) { *p = __float2half_rn(x); }
@@ -60,6 +144,7 @@ struct MxIn<__half> {
 };
 template <>
 struct MxIn<__nv_bfloat16> {
+    using Bits = uint16_t;
     static constexpr int LOADS = 2;
     static __device__ __forceinline__ float one(const __nv_bfloat16* p) { return __bfloat162float(*p); }
     static __device__ __forceinline__ void st(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
@@ -91,10 +176,13 @@ struct Raw16 {
 // the residual norm may write where it read.  vec: 2 rows 32-byte aligned, one
 // 32-byte load a half of two (every request then covers whole sectors), 1 rows
 // 16-byte aligned, 0 neither.
-template <typename T>
-__device__ __forceinline__ Raw16<T> mx_load16(const T* row, int c0, int cols, int vec) {
+// lo, hi: the tensor's bytes.  ALIGNED: vec is known not to be 0.
+template <bool ALIGNED, typename T>
+__device__ __forceinline__ Raw16<T> mx_load16(const T* row, int c0, int cols, int vec, const void* lo, const void* hi) {
     Raw16<T> r;
-    if (vec && c0 + 16 <= cols) {
+    if (!ALIGNED && !vec && c0 + 16 <= cols && mx_granules_inside(row + c0, 16 * (int)sizeof(T), lo, hi)) {
+        mx_load_words<4 * MxIn<T>::LOADS>(row + c0, reinterpret_cast<uint32_t(&)[4 * MxIn<T>::LOADS]>(r.w));
+    } else if ((ALIGNED || vec) && c0 + 16 <= cols) {
         if (vec == 2) {
 #pragma unroll
             for (int i = 0; i < MxIn<T>::LOADS; i += 2) {
@@ -137,9 +225,16 @@ __device__ __forceinline__ Raw16<T> mx_round(const Row16& v) {
     return r;
 }
 
-template <typename T>
-__device__ __forceinline__ void mx_store16(T* row, int c0, int cols, int vec, const Raw16<T>& r) {
-    if (vec && c0 + 16 <= cols) {
+// Warp-wide (lanes hold consecutive chunks of a row).
+template <bool ALIGNED, typename T>
+__device__ __forceinline__ void mx_store16(T* row, int c0, int cols, int vec, const Raw16<T>& r, int lane) {
+    if (!ALIGNED && !vec) {
+        using E = typename MxIn<T>::Bits;
+        mx_store_words<E, 4 * MxIn<T>::LOADS>(row + c0, reinterpret_cast<const uint32_t(&)[4 * MxIn<T>::LOADS]>(r.w),
+                                              c0 + 16 <= cols, lane);
+    }
+    if (c0 + 16 <= cols) {
+        if (!ALIGNED && !vec) return;
         if (vec == 2) {
 #pragma unroll
             for (int i = 0; i < MxIn<T>::LOADS; i += 2) {

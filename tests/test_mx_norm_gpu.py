@@ -209,3 +209,30 @@ def test_rows_by_expert(h, fmt, counts, extra):
     a = e.scales.cpu().numpy()[R.scale_at(R.expert_rows(off)[:, None], j, atoms)]
     b = o.scales.cpu().numpy()[R.scale_at(np.arange(held)[:, None], j, atoms)]
     assert np.array_equal(a, b)
+
+
+@pytest.mark.parametrize("dt", [synth.F32, synth.F16, synth.BF16])
+@pytest.mark.parametrize("off", [0, 1, 2, 3, 5, 7])
+@pytest.mark.parametrize("cols", [1091, 5003])
+def test_rows_that_start_anywhere(h, dt, off, cols):
+    rows, ld = 9, cols + 10
+
+    def odd(seed):
+        buf = torch.full((rows * ld + 8,), float("nan"), dtype=TD[dt], device="cuda")
+        t = buf[off:off + rows * ld].view(rows, ld)[:, :cols]
+        t.copy_(data(rows, cols, TD[dt], seed))
+        return t
+
+    f, r, gate = odd(1), odd(2), odd(3)
+    post, pre = odd(4)[0], odd(5)[0]
+    back = torch.full((rows * ld + 8,), 7.0, dtype=TD[dt], device="cuda")
+    out, o = run(h, qg.GEMM_NVFP4, f, r, post, pre, gate, gate_ld=ld, out=back[off:off + rows * ld].view(rows, ld)[:, :cols])
+    check_residual(out, f, r, post, gate, 1e-5, 0.7, dt)
+    check_codes(o, out, pre, 1e-5, qg.GEMM_NVFP4)
+    # the same bits as from rows that start on 16-byte boundaries
+    even = lambda t: t.contiguous() if cols % 8 == 0 else torch.cat([t, t[..., :(-cols) % 16]], -1)[..., :cols]  # noqa: E731
+    same, o2 = run(h, qg.GEMM_NVFP4, even(f), even(r), post.clone(), pre.clone(), even(gate), gate_ld=even(gate).stride(0))
+    assert torch.equal(out, same) and torch.equal(o.codes, o2.codes) and torch.equal(o.scales, o2.scales)
+    around = back.float().cpu().clone()
+    around[off:off + rows * ld].view(rows, ld)[:, :cols] = 7.0
+    assert bool((around == 7.0).all())

@@ -206,3 +206,31 @@ def test_dequantize_nan_scale(h, fmt):
     b = R.BLOCK[fmt]
     one = float(R.dequantize(*R.quantize(np.ones((1, b)), fmt), fmt)[0, 0])  # 1 as the format holds it
     assert bool(out[1, :b].isnan().all()) and bool((out[0] == one).all()) and bool((out[1, b:] == one).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("off", range(8))
+def test_rows_that_start_anywhere(h, dtype, off):
+    # odd row strides put every row at another distance from a 16-byte boundary;
+    # what is read past a row must not matter, nothing past it may be written
+    rows, k, ld = 33, 1091, 1101
+    buf = torch.full((rows * ld + 8,), float("nan"), dtype=dtype, device="cuda")
+    x = buf[off:off + rows * ld].view(rows, ld)[:, :k]
+    x.copy_(values(rows, k, dtype, seed=off))
+    o, _ = quantize(h, x, qg.GEMM_NVFP4)
+    packed, scales = expect(x, qg.GEMM_NVFP4)
+    assert np.array_equal(o.scales.cpu().numpy(), scales) and np.array_equal(o.codes.cpu().numpy(), packed)
+    c, cl, s, sb = o.args()
+    code, byte = R.quantize(x.double().cpu().numpy(), qg.GEMM_NVFP4)
+    for out_t, want in ((dtype, R.dequantize(code, byte, qg.GEMM_NVFP4)), (torch.float8_e4m3fn, R.VALUES[code])):
+        back = torch.full((rows * ld + 8,), 7.0, device="cuda").to(out_t)
+        y = back[off:off + rows * ld].view(rows, ld)[:, :k]
+        assert qg.gemm_mx_dequantize(h, qg.GEMM_NVFP4, 1.0, c, cl, s, sb, qg.ptr(y), qg.row_major(y), None, 0,
+                                     qg.current_stream()) == 0
+        # code * scale has at most 6 significant bits: exact in every type, but for
+        # fp16's smallest values
+        want_t = torch.from_numpy(want).to(out_t).double().numpy() if out_t == torch.float16 else want
+        assert np.array_equal(y.double().cpu().numpy() if out_t != torch.float8_e4m3fn else y.float().double().cpu().numpy(), want_t)
+        around = back.float().cpu().clone()
+        around[off:off + rows * ld].view(rows, ld)[:, :k] = 7.0
+        assert bool((around == 7.0).all())
