@@ -13,9 +13,9 @@
 // and neither L2 (28% of its throughput) nor the crossbar (24%) is near its limit.
 // What did not help: sharing A between two neighbouring pairs by multicast (a
 // fifth less asked of L2), fetching operands into L2 ahead, another order of
-// tiles, copies of two K-steps at once in a ring of four (104 us), and giving the accumulator back earlier still (all of it parked in shared
-// memory and a stage less: 98 us; a quarter parked and more registers: 91).  The
-// epilogue shares the schedulers with the warps that issue copies and MMAs, so its
+// tiles, copies of two K-steps at once in a ring of four (104 us), and giving the
+// accumulator back earlier still (all of it parked in shared memory and a stage
+// less: 98 us; a quarter parked and more registers: 91).  The epilogue shares the schedulers with the warps that issue copies and MMAs, so its
 // instructions cost main loop time wherever they stand: GELU takes 86 us to 117.
 //
 // TMEM: 256 accumulator columns and as many scale buffers as the ring has

@@ -15,8 +15,8 @@ namespace {
 
 constexpr int QWARPS = 8;  // warps of a block, a row each
 
-// 32 registers, so that 64 warps an SM keep the loads going: 28.4 us for 4096 x
-// 14336 bf16 (150 MB: 5.3 TB/s); with two rows a warp and 50 registers 30.6.
+// 32 registers, so that 64 warps an SM keep the loads going: 30 us for 4096 x
+// 14336 bf16 (150 MB: 5.0 TB/s); with two rows a warp and 50 registers 30.6.
 template <typename T, bool NVF4>
 __global__ void __launch_bounds__(32 * QWARPS, 8) mx_quantize_kernel(const __grid_constant__ MxQuantParams p) {
     griddep_launch_dependents();
