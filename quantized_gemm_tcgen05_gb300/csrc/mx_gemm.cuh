@@ -365,17 +365,27 @@ __global__ void __launch_bounds__(MX_THREADS, 2)
                     sum.z += p.z;
                     sum.w += p.w;
                 }
-                const float a4[4] = {sum.x, sum.y, sum.z, sum.w};
                 float x[4];
                 const int have = e.N - n < 4 ? (int)(e.N - n) : 4;
                 if (!mx_block_in_bounds(e, m, 1, n, have)) continue;
                 with_epi_act(e, [&](auto act) {
                     constexpr int ACT = decltype(act)::value;
+                    float c[4], b[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float c = (e.beta != 0.0f && j < have) ? ld_elem(e.C, e.d_type, m * e.ldc + n + j) : 0.0f;
-                        x[j] = epi_value<ACT>(ar, a4[j], c, ACT >= 0 ? bias_at(ar, n + j) : 0.0f);
+                        c[j] = (e.beta != 0.0f && j < have) ? ld_elem(e.C, e.d_type, m * e.ldc + n + j) : 0.0f;
+                        b[j] = ACT >= 0 ? bias_at(ar, n + j) : 0.0f;
                     }
+                    auto value = [&](auto dt) {
+                        constexpr int DT = decltype(dt)::value;
+                        mx_value2<ACT, DT>(ar, sum.x, sum.y, c[0], c[1], b[0], b[1], x[0], x[1]);
+                        mx_value2<ACT, DT>(ar, sum.z, sum.w, c[2], c[3], b[2], b[3], x[2], x[3]);
+                    };
+                    // (the 16-bit types' values are the same up to the rounding)
+                    if (ACT == 2 && e.d_type != DT_F32)
+                        value(EpiAct<DT_F16>{});
+                    else
+                        value(EpiAct<DT_F32>{});
                 });
                 if (P.vec32 && have == 4) {
                     st4(e.D, e.d_type, m * e.ldd + n, make_float4(x[0], x[1], x[2], x[3]));

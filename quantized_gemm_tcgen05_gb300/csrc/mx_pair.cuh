@@ -16,7 +16,7 @@
 // tiles, copies of two K-steps at once in a ring of four (104 us), and giving the
 // accumulator back earlier still (all of it parked in shared memory and a stage
 // less: 98 us; a quarter parked and more registers: 91).  The epilogue shares the schedulers with the warps that issue copies and MMAs, so its
-// instructions cost main loop time wherever they stand: GELU takes 86 us to 117.
+// instructions cost main loop time wherever they stand: GELU takes 86 us to 112.
 //
 // TMEM: 256 accumulator columns and as many scale buffers as the ring has
 // stages.  Scales go from shared memory to TMEM through the registers of four
