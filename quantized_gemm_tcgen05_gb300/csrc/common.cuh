@@ -128,6 +128,19 @@ __device__ __forceinline__ bool wait_bar_drain(uint64_t* bar, uint32_t parity, c
     return true;
 }
 
+// The same for phases that other CTAs of the cluster complete.
+__device__ __forceinline__ bool wait_bar_cluster_drain(uint64_t* bar, uint32_t parity, const Guard& g) {
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait_cluster(bar, parity)) {
+        if (globaltimer_ns() - t0 > g.limit_ns) {
+            record_timeout(g, SITE_DRAIN);
+            return false;
+        }
+    }
+    return true;
+}
+
 __device__ __forceinline__ void epi_bar_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // ---- device-side bounds checks (debug build) ------------------------------------

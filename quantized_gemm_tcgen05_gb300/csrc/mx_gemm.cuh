@@ -12,9 +12,10 @@
 // all of them are through, each sends every other its share of the columns of
 // its fp32 partial tile (bulk copies into the idle ring, counted by the
 // receiver's barrier), adds what it received in rank order and finishes its
-// columns.  Nothing goes through global memory but operands and D, and no
-// workspace is needed.  Bulk copies carry their own completion: cluster
-// barriers and remote loads in their place took 4 us of a 9 us launch.
+// columns; how the CTAs announce themselves and leave, also when one of them gave
+// up, stands in mx_exchange.h.  Nothing goes through global memory but operands
+// and D, and no workspace is needed.  Bulk copies carry their own completion:
+// cluster barriers and remote loads in their place took 4 us of a 9 us launch.
 //
 //   warp 0     TMA producer          warps 4-7  scales
 //   warp 1     MMAs                  all        epilogue
@@ -29,6 +30,7 @@
 #include <atomic>
 
 #include "mx_epilogue.cuh"
+#include "mx_exchange.h"
 
 namespace qg {
 
@@ -76,6 +78,37 @@ __device__ __forceinline__ void bulk_s2cluster(uint32_t dst, uint32_t src, uint3
                  : "memory");
 }
 
+// What is in flight within a cluster lands in far less than this.
+__device__ __forceinline__ void mx_settle() {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 200000ull) {
+    }
+}
+
+// The steps of mx_exchange.h: announcements on `idle`, shares (`bytes` each) out of
+// `parts` into the others' `recv`, counted by their `part`.
+struct MxClusterLink {
+    uint64_t *idle, *part;
+    volatile uint32_t* warning;
+    uint32_t parts, recv, bytes;
+    int splits, rank;
+    const Guard& g;
+    __device__ __forceinline__ void expect() { mbar_arrive_expect_tx(part, (uint32_t)splits * bytes); }
+    // (nothing is published: the arrivals are relaxed)
+    __device__ __forceinline__ void announce(int z) { mbar_arrive_remote_relaxed(mapa_shared(smem_u32(idle), z)); }
+    __device__ __forceinline__ bool await_announced() { return wait_bar_cluster_drain(idle, 0, g); }
+    __device__ __forceinline__ void send(int z) {
+        bulk_s2cluster(mapa_shared(recv + (uint32_t)rank * bytes, z), parts + (uint32_t)z * bytes, bytes,
+                       mapa_shared(smem_u32(part), z));
+    }
+    __device__ __forceinline__ bool await_shares() { return wait_bar_cluster_drain(part, 0, g); }
+    __device__ __forceinline__ void warn(int z) { st_cluster_fence(mapa_shared(smem_u32((const void*)warning), z), 1u); }
+    __device__ __forceinline__ void arrive() { cluster_arrive_relaxed(); }
+    __device__ __forceinline__ void wait() { cluster_wait(); }
+    __device__ __forceinline__ bool warned() { return *warning != 0; }
+    __device__ __forceinline__ void settle() { mx_settle(); }
+};
+
 template <int BN, bool NVF4>
 __global__ void __launch_bounds__(MX_THREADS, 2)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -95,6 +128,7 @@ __global__ void __launch_bounds__(MX_THREADS, 2)
     uint64_t* part = idle + 1;                   // the partial tiles' shares have arrived
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(part + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
+    volatile uint32_t* warning = tmem_slot + 2;  // a CTA of the cluster has given up
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int splits = P.splits;
@@ -108,6 +142,7 @@ __global__ void __launch_bounds__(MX_THREADS, 2)
         mbar_init(idle, (uint32_t)splits);
         mbar_init(part, 1);
         *abort_flag = 0;
+        *warning = 0;
         fence_barrier_init();
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
@@ -272,9 +307,7 @@ __global__ void __launch_bounds__(MX_THREADS, 2)
     bool all_ok = __syncthreads_and(ok ? 1 : 0) != 0;
     if (live && !all_ok) {
         // gave up: let copies in flight land and issued MMAs finish before shared memory and TMEM go
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 200000ull) {
-        }
+        mx_settle();
     }
     const int ew = warp % 4, half = warp / 4;
     const uint32_t tb = tmem + half * (BN / 2) + ((uint32_t)(ew * 32) << 16);
@@ -329,25 +362,11 @@ __global__ void __launch_bounds__(MX_THREADS, 2)
         }
         fence_proxy_async_smem();  // ... visible to the bulk copies
         __syncthreads();
-        if (live && threadIdx.x == 0) {
-            // this CTA's ring is idle (its accumulator is complete): tell everyone,
-            // and wait until theirs are.  Nothing is published, so the arrivals are relaxed
-            mbar_arrive_expect_tx(part, (uint32_t)splits * nq * pitch);
-            for (int z = 0; z < splits; ++z) mbar_arrive_remote_relaxed(mapa_shared(smem_u32(idle), z));
-            if (wait_bar_cluster(idle, 0, g, SITE_DRAIN)) {
-                // bytes are sent even after a failure, so that no receiver waits in vain
-                for (int z = 0; z < splits; ++z)
-                    bulk_s2cluster(mapa_shared(smem_u32(recv) + (uint32_t)(rank * nq) * pitch, z),
-                                   smem_u32(smem) + (uint32_t)(z * nq) * pitch, (uint32_t)nq * pitch,
-                                   mapa_shared(smem_u32(part), z));
-            }
-        }
         if (live) {
-            ok = wait_bar_cluster(part, 0, g, SITE_DRAIN);
+            // (whether this CTA's part is right or not: the others wait for it)
+            MxClusterLink link{idle, part, warning, smem_u32(smem), smem_u32(recv), (uint32_t)nq * pitch, splits, rank, g};
+            ok = mx_exchange(link, splits, threadIdx.x == 0);
             all_ok = __syncthreads_and(all_ok && ok ? 1 : 0) != 0;
-            // everyone's copies to this CTA have landed: their senders may leave
-            if (threadIdx.x == 0)
-                for (int z = 0; z < splits; ++z) mbar_arrive_remote_relaxed(mapa_shared(smem_u32(idle), z));
         }
         if (all_ok) {
             const EpiParams& e = P.epi;
@@ -396,14 +415,17 @@ __global__ void __launch_bounds__(MX_THREADS, 2)
                 }
             }
         }
-        // shared memory goes only when every peer has this CTA's share
-        if (live && threadIdx.x == 0) wait_bar_cluster(idle, 1, g, SITE_DRAIN);
     }
     tc_fence_before_sync();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, Cfg::TMEM_COLS);
+    }
+    // shared memory goes only when nobody will read or write it any more
+    if (live && splits > 1) {
+        MxClusterLink link{idle, part, warning, 0, 0, 0, splits, rank, g};
+        mx_exchange_leave(link);
     }
 }
 
