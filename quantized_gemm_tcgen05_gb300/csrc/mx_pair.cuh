@@ -33,11 +33,13 @@
 //   warps 10-13 scales: shared memory -> TMEM, then arrive on the leader's sready[s]
 //
 // Grouped problems: 256-row blocks of one expert's rows; the blocks that exist
-// are counted on the device and shared out, so none is assigned in vain.
+// are counted on the device and shared out, so none is assigned in vain (no more
+// of them than any partition of the rows has, whatever the offsets say).
 #pragma once
 #include <atomic>
 
 #include "mx_epilogue.cuh"
+#include "mx_rows.h"
 
 namespace qg {
 
@@ -64,16 +66,14 @@ struct MxTile {
     int expert, rows;  // rows of the 256 that exist
 };
 
-// Blocks of bm rows that rows sorted by expert make (every lane gets it).
-__device__ __forceinline__ int64_t mx_expert_blocks(const int32_t* off, int32_t E, int bm, int lane) {
-    int n = 0;
-    for (int32_t e = lane; e < E; e += 32) {
-        const int64_t m = (int64_t)off[e + 1] - off[e];
-        n += m > 0 ? (int)((m + bm - 1) / bm) : 0;
-    }
+// Blocks of bm rows that rows sorted by expert make, at most `most` (every lane
+// gets it).  `most` is below 2^24, so 32 lanes' sums fit.
+__device__ __forceinline__ int64_t mx_expert_blocks(const int32_t* off, int32_t E, int bm, int32_t most, int lane) {
+    int32_t n = 0;
+    for (int32_t e = lane; e < E; e += 32) n = mx_add_blocks(n, off[e], off[e + 1], bm, most);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
-    return n;
+    return n < most ? n : most;
 }
 
 // Tile t of the launch (warp-wide): M blocks vary fastest.  False past the end.
@@ -144,7 +144,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(MX_PAIR_THREADS, 1)
     griddep_wait();
     const Guard g{P.status, P.timeout_ns, abort_flag};
     const int64_t pid = blockIdx.x >> 1;
-    const int64_t blocks = P.offsets ? mx_expert_blocks(P.offsets, P.num_experts, 256, lane) : P.tiles_m;
+    const int64_t blocks = P.offsets ? mx_expert_blocks(P.offsets, P.num_experts, 256, P.tiles_m, lane) : P.tiles_m;
     const int64_t tiles = blocks * P.tiles_n;
 
     if (warp == 0) {
