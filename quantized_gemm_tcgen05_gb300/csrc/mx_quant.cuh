@@ -6,6 +6,7 @@
 
 #include "f32x2.cuh"
 #include "mx_params.h"
+#include "mx_rows.h"
 
 namespace qg {
 
@@ -402,14 +403,14 @@ __device__ __forceinline__ void mx_store_scales(uint8_t* S, int chunk, int chunk
 
 // Rows lo .. hi - 1 of one expert, and the scale row of the first (an expert
 // starts on an atom row).  Offsets that are no partition of the rows cannot lead
-// past the scales: a span beyond the `rows` / 128 + E atom rows is empty.
+// past the scales: a span ends with the `rows` / 128 + E atom rows (mx_span_end).
 struct MxExpertSpan {
     int64_t lo, hi, row0;
     __device__ __forceinline__ bool holds(int64_t r) const { return r >= lo && r < hi; }
 };
 
-// Warp-wide: the expert that holds row r of rows sorted by expert; an empty span
-// when none does.
+// Warp-wide: the expert that holds row r of rows sorted by expert; a span without
+// it when none does, or when it has no scales.
 __device__ __forceinline__ MxExpertSpan mx_expert_of(const int32_t* off, int32_t E, int64_t rows, int64_t r, int lane) {
     int64_t tiles = 0;
     for (int32_t e0 = 0; e0 < E; e0 += 32) {
@@ -423,8 +424,8 @@ __device__ __forceinline__ MxExpertSpan mx_expert_of(const int32_t* off, int32_t
         for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
         tiles += n;
         if (hit) {
-            const MxExpertSpan s{__shfl_sync(0xFFFFFFFFu, lo, first), __shfl_sync(0xFFFFFFFFu, hi, first), tiles * MX_ATOM_ROWS};
-            return s.lo >= 0 && tiles + (r - s.lo) / MX_ATOM_ROWS < rows / MX_ATOM_ROWS + E ? s : MxExpertSpan{0, 0, 0};
+            const int64_t at = __shfl_sync(0xFFFFFFFFu, lo, first), end = __shfl_sync(0xFFFFFFFFu, hi, first);
+            return MxExpertSpan{at, mx_span_end(at, end, tiles, rows, E), tiles * MX_ATOM_ROWS};
         }
     }
     return MxExpertSpan{0, 0, 0};

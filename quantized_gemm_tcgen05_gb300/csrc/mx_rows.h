@@ -15,4 +15,14 @@ QG_HD int32_t mx_add_blocks(int32_t n, int32_t lo, int32_t hi, int bm, int32_t m
     return sum < most ? (int32_t)sum : most;
 }
 
+// Where the rows lo .. hi - 1 of an expert end that have scales: its first row lies
+// on atom row `tiles` (the atom rows of the experts before it), and there are
+// rows / 128 + experts atom rows.  A partition of the rows never reaches that limit.
+// An expert that starts before row 0 has none.
+QG_HD int64_t mx_span_end(int64_t lo, int64_t hi, int64_t tiles, int64_t rows, int32_t experts) {
+    const int64_t room = rows / 128 + experts - tiles;
+    if (lo < 0 || room <= 0) return lo;
+    return hi - lo < room * 128 ? hi : lo + room * 128;
+}
+
 }  // namespace qg

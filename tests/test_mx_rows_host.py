@@ -19,7 +19,9 @@ int main() {
     char what[16];
     long long a, b, c, d, e;
     while (scanf("%15s %lld %lld %lld %lld %lld", what, &a, &b, &c, &d, &e) == 6)
-        if (!strcmp(what, "blocks")) printf("%d\n", qg::mx_add_blocks((int)a, (int)b, (int)c, (int)d, (int)e));
+        if (!strcmp(what, "end"))
+            printf("%lld\n", (long long)qg::mx_span_end(a, b, c, d, (int)e));
+        else if (!strcmp(what, "blocks")) printf("%d\n", qg::mx_add_blocks((int)a, (int)b, (int)c, (int)d, (int)e));
 }
 '''
 
@@ -72,3 +74,30 @@ def test_a_partition_never_reaches_the_limit_early(rules):
             n = rules("blocks", [(n, lo, lo + c, bm, most)])[0]
             lo += c
         assert n == sum(-(-c // bm) for c in counts)
+
+
+def test_no_row_of_a_span_has_its_scales_past_the_end(rules):
+    rng, ask = random.Random(3), [(8, 256, 4, 256, 3)]
+    for _ in range(4000):
+        rows, experts = rng.choice([1, 127, 128, 256, 5000, TOP]), rng.choice([1, 3, 40, 4096])
+        lo, hi = values(rng, 2)
+        if rng.random() < 0.5:
+            lo, hi = rng.randint(0, 600), rng.randint(0, 1200)
+        ask.append((lo, max(lo, hi), rng.choice([0, rows // 128, rows // 128 + experts - 1, rng.randint(0, 2 ** 37)]), rows, experts))
+    assert rules("end", ask[:1]) == [136]  # one atom row is left
+    for (lo, hi, tiles, rows, experts), end in zip(ask, rules("end", ask)):
+        held = [r for r in (lo, lo + 127, lo + 128, end - 1, end, hi - 1) if lo <= r < hi]
+        for r in held:
+            inside = lo >= 0 and tiles + (r - lo) // 128 < rows // 128 + experts
+            assert (r < end) == inside, (lo, hi, tiles, rows, experts, end, r)
+
+
+def test_a_span_of_a_partition_is_whole(rules):
+    rng = random.Random(4)
+    for _ in range(60):
+        counts = [rng.choice([0, 1, 127, 128, 129, rng.randint(0, 2000)]) for _ in range(rng.randint(1, 40))]
+        rows, ask, lo, tiles = sum(counts), [], 0, 0
+        for c in counts:
+            ask.append((lo, lo + c, tiles, rows, len(counts)))
+            lo, tiles = lo + c, tiles + -(-c // 128)
+        assert rules("end", [a for a in ask if a[0] < a[1]]) == [a[1] for a in ask if a[0] < a[1]]
