@@ -101,7 +101,8 @@ int gemm_run_mx(gemm_handle_t h, const gemm_op_t* op, int32_t format, float alph
  * The grouped form: rows of A (and of C, D) sorted by expert as in
  * gemm_run_grouped, B with num = num_experts matrices.  expert_alpha (device,
  * num_experts floats, or NULL) multiplies alpha expert by expert: the tensor
- * scales of the experts' weights.
+ * scales of the experts' weights.  Rows that no expert holds keep what D had, also
+ * with K = 0 (D = act(beta C + bias)).
  */
 int gemm_run_mx_grouped(gemm_handle_t h, const gemm_op_t* op, int32_t format, float alpha,
                         const float* expert_alpha, const void* A, const gemm_layout_t* Adesc, const void* SA,

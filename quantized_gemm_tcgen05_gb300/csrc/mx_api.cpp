@@ -348,9 +348,9 @@ int run_product(gemm_handle_t h, const gemm_op_t* op, MxProduct& p, cudaStream_t
         handle_set_choice(h, "empty", p.M, p.N, p.K);
         return GEMM_OK;
     }
-    if (p.K == 0) {  // no products: act(beta * C + bias)
+    if (p.K == 0) {  // no products: act(beta * C + bias), of the rows that K > 0 writes
         handle_set_choice(h, "scale_c", p.M, p.N, p.K);
-        return status_of(launch_scale_c(p.epi, 1, st));
+        return status_of(launch_mx_no_k(p.epi, p.offsets, p.experts, st));
     }
     const int clusters = pair_clusters(h, p.format);
     const MxChoice c = choose(p, handle_sm_count(h), clusters, op->splitk);

@@ -90,6 +90,17 @@ __device__ __forceinline__ void mx_value2(const EpiArith& e, float a0, float a1,
     }
 }
 
+// The same where D's type is known at run time only (the 16-bit types' values differ
+// in the rounding to come).
+template <int ACT>
+__device__ __forceinline__ void mx_value2_any(const EpiArith& e, int32_t d_type, float a0, float a1, float c0, float c1,
+                                              float b0, float b1, float& x0, float& x1) {
+    if (ACT == 2 && d_type != DT_F32)
+        mx_value2<ACT, DT_F16>(e, a0, a1, c0, c1, b0, b1, x0, x1);
+    else
+        mx_value2<ACT, DT_F32>(e, a0, a1, c0, c1, b0, b1, x0, x1);
+}
+
 // 64 accumulator columns (TMEM address ta, this warp's 32 rows, a row per lane).
 __device__ __forceinline__ void mx_load64(uint32_t ta, float (&v)[2][32]) {
     tmem_load_chunk<32>(ta, v[0]);

@@ -395,16 +395,8 @@ __global__ void __launch_bounds__(MX_THREADS, 2)
                         c[j] = (e.beta != 0.0f && j < have) ? ld_elem(e.C, e.d_type, m * e.ldc + n + j) : 0.0f;
                         b[j] = ACT >= 0 ? bias_at(ar, n + j) : 0.0f;
                     }
-                    auto value = [&](auto dt) {
-                        constexpr int DT = decltype(dt)::value;
-                        mx_value2<ACT, DT>(ar, sum.x, sum.y, c[0], c[1], b[0], b[1], x[0], x[1]);
-                        mx_value2<ACT, DT>(ar, sum.z, sum.w, c[2], c[3], b[2], b[3], x[2], x[3]);
-                    };
-                    // (the 16-bit types' values are the same up to the rounding)
-                    if (ACT == 2 && e.d_type != DT_F32)
-                        value(EpiAct<DT_F16>{});
-                    else
-                        value(EpiAct<DT_F32>{});
+                    mx_value2_any<ACT>(ar, e.d_type, sum.x, sum.y, c[0], c[1], b[0], b[1], x[0], x[1]);
+                    mx_value2_any<ACT>(ar, e.d_type, sum.z, sum.w, c[2], c[3], b[2], b[3], x[2], x[3]);
                 });
                 if (P.vec32 && have == 4) {
                     st4(e.D, e.d_type, m * e.ldd + n, make_float4(x[0], x[1], x[2], x[3]));

@@ -36,6 +36,9 @@ QG_HD uint32_t make_idesc_mx(int nvf4, int m, int n) {
 }
 
 cudaError_t launch_mx_gemm(int bn, int format, const MxMaps& m, const MxGemmParams& p, int grid, cudaStream_t st);
+// K = 0: D = act(beta C + bias), of the rows that an expert holds when there are
+// offsets.
+cudaError_t launch_mx_no_k(const EpiParams& e, const int32_t* offsets, int32_t num_experts, cudaStream_t st);
 // Stages of the ring for a tile of a_rows x bn; 0: its partial tiles do not fit.
 int mx_gemm_stages(int bn, int format, int a_rows, int splits);
 
