@@ -503,7 +503,8 @@ int gemm_mx_norm_quantize(gemm_handle_t h, const gemm_mx_norm_t* op, const void*
         const bool weights = op->post_weight || op->pre_weight;
         if ((weights && !ws) || (op->gate && !gs)) return (int)GEMM_ERR_UNSUPPORTED;
         if (!F && (op->post_weight || op->gate)) return (int)GEMM_ERR_INVALID_ARG;
-        if (op->gate && op->gate_ld != 0 && op->gate_ld < cols) return (int)GEMM_ERR_INVALID_ARG;
+        if (op->gate && op->gate_ld != 0 && (op->gate_ld < cols || op->gate_ld > ((int64_t)1 << 40)))
+            return (int)GEMM_ERR_INVALID_ARG;
         if ((rc = check_experts(h, op->expert_offsets, op->num_experts))) return rc;
         if (rows == 0 || cols == 0) return (int)GEMM_OK;
         auto bad = [&](const void* ptr, int64_t n) { return !aligned(ptr, (uintptr_t)n) || !handle_device_pointer(h, ptr); };
