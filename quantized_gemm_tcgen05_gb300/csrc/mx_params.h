@@ -18,10 +18,6 @@ constexpr int MX_KSTEP = 256;       // codes of one 128-byte swizzle row
 QG_HD int32_t mx_block(int32_t format) { return format == MXF_NVFP4 ? 16 : 32; }
 // Atoms along K of one atom row.
 QG_HD int64_t mx_atoms(int32_t format, int64_t cols) { return ceil_div(cols, 4 * (int64_t)mx_block(format)); }
-// Byte of the scale of row r, block b, within a matrix of `atoms` atoms per row.
-QG_HD int64_t mx_scale_at(int64_t r, int64_t b, int64_t atoms) {
-    return ((r / MX_ATOM_ROWS) * atoms + b / 4) * MX_ATOM_BYTES + (r % 32) * 16 + (r % MX_ATOM_ROWS) / 32 * 4 + b % 4;
-}
 
 // Constants of a launch: g, RN(6 g) and its reciprocal, rounded.
 struct MxScaleConst {
