@@ -86,7 +86,8 @@ int gemm_mx_dequantize(gemm_handle_t h, int32_t format, float tensor_scale, cons
  * bias_type apply; GELU is x Phi(x), for an f32 D in gemm.h's form
  * 0.5 x (1 + erf(x / sqrt 2)), for a 16-bit D within 2e-5 of it, relative, before
  * the rounding (negative x included, where gemm.h's form cancels); splitk forces
- * that many K slices (1, 2, 4 or 8; 0 chooses), dispatch is accepted and the
+ * that many K slices (1, 2, 4 or 8, as far as there are 256-wide K-steps and the
+ * partial tiles fit shared memory; 0 chooses), dispatch is accepted and the
  * built-in choice used (nothing is measured or cached); U / V groups, streamk = 1
  * and zero points have no meaning here and are GEMM_ERR_UNSUPPORTED, as are
  * batches and an int8 D.

@@ -330,7 +330,9 @@ MxChoice choose(const MxProduct& p, int sm_count, int clusters, int forced_split
             if (splits > steps || !mx_gemm_stages(bn, p.format, a_rows, splits)) continue;
             const MxChoice c{bn, splits, 0};
             const double us = estimate(p, sm_count, clusters, c);
-            if (best_us < 0 || us < best_us) {
+            // a forced count goes before time: one width may allow it where another does not
+            const bool better = forced_split && splits != best.splits ? splits > best.splits : us < best_us;
+            if (best_us < 0 || better) {
                 best_us = us;
                 best = c;
             }
