@@ -281,14 +281,14 @@ bool forced_kernel(MxChoice* c) {
 // Estimated time of a choice, microseconds.  Measured on GB300 (152 SMs),
 // back-to-back launches:
 //   one-tile kernel  2.5 us for launch, first data and exit (1x64x64), 0.30 us (64
-//     columns) or 0.33 (128) a K-step of 256 while the issuing warp is the bound, else the bytes of the
-//     stages of the CTAs that share an SM at 132 bytes a nanosecond; 1.2 us for
+//     columns) or 0.33 (128) a K-step of 256 while the issuing warp is the bound,
+//     else the bytes of the stages of the CTAs that share an SM at 132 bytes a nanosecond; 1.2 us for
 //     every further wave of CTAs, 0.25 us for every CTA on an SM; K slices: 1.4 us
-//     and 0.025 us a row of a 64-column tile (1x4096x4096: 7.5 us whole, 6.3 in
-//     two, 5.9 in four; 128x4096x4096: 8.0 whole, 9.6 in two)
+//     and 0.025 us a row of a 64-column tile (1x4096x4096: 7.7 us whole, 6.2 in
+//     two, 5.6 in four; 128x4096x4096: 9.0 whole, 10.3 in two)
 //   CTA pair         3.9 us, 0.37 us a K-step, 0.42 when every cluster is busy
 //     (512x4096x4096: 10.5 us against 9.4 in 64-column tiles; 1024x4096x4096:
-//     11.3 against 18; 4096^3: 32 against 65)
+//     11.0 against 18; 4096^3: 31 against 65)
 // No choice takes less than its operands at 6.5 TB/s; among choices that memory
 // bounds, the one with less else to do is ahead.
 double estimate(const MxProduct& p, int sm_count, int clusters, const MxChoice& c) {

@@ -60,9 +60,11 @@ constexpr bool MX_NORM_AHEAD = NC == 1 && !WIDE && sizeof(T) == 2;
 //
 // WIDE: more than 256 threads a row (rows beyond 4096 columns) with 64 registers
 // each.  One or two rows an SM then, whose chain of sums nothing hides: 4096 rows
-// of 8192 columns take 66 us (3.3 TB/s), of 14336 137 us (2.8 TB/s).  Two chunks a
+// of 8192 columns take 66 us (3.3 TB/s), of 14336 136 us (2.8 TB/s).  Two chunks a
 // thread in half the threads were slower (3001 x 9001, not aligned, with a gate
-// per element: 232 us, here 170).
+// per element: 232 us, here 172).  The 64 registers spill: 32 to 144 bytes a thread
+// with 16-bit types, 236 to 316 with f32, more where a thread has two chunks (beyond
+// 16384 columns).  Of the other forms only f32 (4096 x 4096: 52 us) and unaligned rows do.
 template <typename T, bool NVF4, int NC, bool WIDE, bool ALIGNED>
 __global__ void __launch_bounds__(WIDE ? 1024 : 256, WIDE ? 1 : 3) mx_norm_kernel(const __grid_constant__ MxNormParams p) {
     // partial sums of the first and the second norm; two sets, so that a row's are

@@ -6,7 +6,7 @@
 // of B's scales in both CTAs' TMEM): 38 KB for 128 x 256 x 256 products, the
 // least per product that the accumulator's size allows.
 //
-// Measured (back-to-back launches): 4096^3 30 us, 4.6 PFLOP/s; 4096 x 14336 x 4096
+// Measured (back-to-back launches): 4096^3 31 us, 4.4 PFLOP/s; 4096 x 14336 x 4096
 // 80 us in MXFP4, 86 in NVFP4, 6.0 and 5.6 PFLOP/s.  A K-step takes 0.41 us where
 // its copies alone take 0.34 with every SM at it (0.29 with a few) and its MMAs
 // alone 0.25, so the copies come first; the tensor pipe is active 41% of the time,
@@ -15,8 +15,9 @@
 // fifth less asked of L2), fetching operands into L2 ahead, another order of
 // tiles, copies of two K-steps at once in a ring of four (104 us), and giving the
 // accumulator back earlier still (all of it parked in shared memory and a stage
-// less: 98 us; a quarter parked and more registers: 91).  The epilogue shares the schedulers with the warps that issue copies and MMAs, so its
-// instructions cost main loop time wherever they stand: GELU takes 86 us to 112.
+// less: 98 us; a quarter parked and more registers: 91).  The epilogue shares the
+// schedulers with the warps that issue copies and MMAs, so its instructions cost
+// main loop time wherever they stand: GELU takes 86 us to 112.
 //
 // TMEM: 256 accumulator columns and as many scale buffers as the ring has
 // stages.  Scales go from shared memory to TMEM through the registers of four

@@ -17,6 +17,7 @@ constexpr int QWARPS = 8;  // warps of a block, a row each
 
 // 32 registers, so that 64 warps an SM keep the loads going: 30 us for 4096 x
 // 14336 bf16 (150 MB: 5.0 TB/s); with two rows a warp and 50 registers 30.6.
+// NVFP4 spills 16 bytes a thread for them (f32: 40).
 template <typename T, bool NVF4>
 __global__ void __launch_bounds__(32 * QWARPS, 8) mx_quantize_kernel(const __grid_constant__ MxQuantParams p) {
     griddep_launch_dependents();
