@@ -9,7 +9,7 @@
 //   - no wait stops because another one gave up: a CTA that did would be missing
 //     to the others, or gone.  All have a limit of their own, so all end, and with
 //     them the cluster's barrier, which has none;
-//   - in a round without failures every share has arrived before its receiver
+//   - without a failure every share has arrived before its receiver
 //     arrives at the barrier, and every announcement before that, so nothing is in
 //     flight when the cluster leaves.  A receiver that gave up says so to everybody
 //     before it arrives, and all then wait for what may still be in flight.
