@@ -1,7 +1,7 @@
 """Python binding of the GB300 GEMM library (libqgemm.so).
 
 Argument marshalling only: every function here forwards to the C ABI of
-``include/gemm.h`` and ``include/gemm_mx.h`` under the same name; every step of the GEMM runs in the
+``include/gemm.h``, ``include/gemm_mx.h``, ``include/gemm_s8.h`` and ``include/gemm_moe.h`` under the same name; every step of the GEMM runs in the
 library's CUDA kernels.  PyTorch is used for device memory and streams in the
 convenience helpers at the bottom (``layout_of``, ``Workspace``, ``run``).
 
@@ -32,6 +32,7 @@ GEMM_ERR_DEVICE_CHECK = 8
 
 GEMM_F32, GEMM_F16, GEMM_BF16, GEMM_S4, GEMM_S8, GEMM_E4M3, GEMM_E5M2, GEMM_E2M1 = 0, 1, 2, 3, 4, 5, 6, 7
 GEMM_MXFP4, GEMM_NVFP4 = 1, 2  # 4-bit microscaled formats (gemm_mx.h)
+GEMM_ROUTE_SOFTMAX, GEMM_ROUTE_SIGMOID = 0, 1  # scores of gemm_moe_route (gemm_moe.h)
 GEMM_ROW_MAJOR, GEMM_COL_MAJOR = 0, 1
 GEMM_DISPATCH_DEFAULT, GEMM_DISPATCH_MEASURE, GEMM_DISPATCH_REUSE = 0, 1, 2
 GEMM_EPILOGUE_DEFAULT, GEMM_EPILOGUE_BIAS, GEMM_EPILOGUE_RELU, GEMM_EPILOGUE_GELU = 0, 1, 2, 4
@@ -52,6 +53,9 @@ MX_SYMBOLS = (
     "gemm_mx_scale_size", "gemm_mx_quantize", "gemm_mx_dequantize", "gemm_run_mx", "gemm_run_mx_grouped",
     "gemm_mx_norm_quantize",
 )
+# ... of gemm_s8.h and of gemm_moe.h.
+S8_SYMBOLS = ("gemm_s8_quantize", "gemm_run_s8", "gemm_run_s8_grouped")
+MOE_SYMBOLS = ("gemm_moe_route", "gemm_moe_dispatch", "gemm_moe_combine")
 
 
 class LibraryNotBuilt(ImportError):
@@ -88,6 +92,12 @@ class gemm_mx_norm_t(ctypes.Structure):
                 ("residual_scale", ctypes.c_float), ("post_weight", ctypes.c_void_p), ("pre_weight", ctypes.c_void_p),
                 ("weight_type", ctypes.c_int32), ("gate_type", ctypes.c_int32), ("gate", ctypes.c_void_p),
                 ("gate_ld", ctypes.c_int64), ("expert_offsets", ctypes.c_void_p), ("num_experts", ctypes.c_int32)]
+
+
+class gemm_route_t(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("topk", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("group_topk", ctypes.c_int32), ("group_best", ctypes.c_int32), ("renormalize", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
 
 
 _lib = None
@@ -137,6 +147,14 @@ def lib():
                                                P, LP, P, LP, P, I32, P]),
         "gemm_mx_norm_quantize": (ctypes.c_int, [P, ctypes.POINTER(gemm_mx_norm_t), P, LP, P, LP, P, LP, P, LP, P, SZ,
                                                  P]),
+        "gemm_s8_quantize": (ctypes.c_int, [P, P, LP, P, LP, P, P]),
+        "gemm_run_s8": (ctypes.c_int, [P, ctypes.POINTER(gemm_op_t), F, P, LP, P, P, LP, P, F, P, LP, P, LP, P]),
+        "gemm_run_s8_grouped": (ctypes.c_int, [P, ctypes.POINTER(gemm_op_t), F, P, LP, P, P, LP, P, F, P, LP, P, LP, P,
+                                               I32, P]),
+        "gemm_moe_route": (ctypes.c_int, [P, ctypes.POINTER(gemm_route_t), P, LP, P, P, P, P,
+                                          ctypes.POINTER(gemm_workspace_t), P]),
+        "gemm_moe_dispatch": (ctypes.c_int, [P, P, LP, P, I32, P, LP, P, P]),
+        "gemm_moe_combine": (ctypes.c_int, [P, P, LP, P, P, I32, F, P, LP, P, LP, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(L, name)
@@ -308,6 +326,42 @@ def gemm_run_mx_grouped(h, op, format, alpha, expert_alpha, A, Adesc, SA, SA_siz
 
 def gemm_mx_norm_quantize(h, op, F, Fdesc, R, Rdesc, O, Odesc, Q, Qdesc, S, S_size, stream):
     return (_lib or lib()).gemm_mx_norm_quantize(h, op, F, Fdesc, R, Rdesc, O, Odesc, Q, Qdesc, S, S_size, stream)
+
+
+# ---- 8-bit integer operands (gemm_s8.h) ------------------------------------------------
+
+def gemm_s8_quantize(h, X, Xdesc, Q, Qdesc, S, stream):
+    return (_lib or lib()).gemm_s8_quantize(h, X, Xdesc, Q, Qdesc, S, stream)
+
+
+def gemm_run_s8(h, op, alpha, A, Adesc, SA, B, Bdesc, SB, beta, C, Cdesc, D, Ddesc, stream):
+    """Returns the status code (0 = OK).  Pointers are ints (device addresses)."""
+    return (_lib or lib()).gemm_run_s8(h, op, alpha, A, Adesc, SA, B, Bdesc, SB, beta, C, Cdesc, D, Ddesc, stream)
+
+
+def gemm_run_s8_grouped(h, op, alpha, A, Adesc, SA, B, Bdesc, SB, beta, C, Cdesc, D, Ddesc, expert_offsets_dev,
+                        num_experts, stream):
+    return (_lib or lib()).gemm_run_s8_grouped(h, op, alpha, A, Adesc, SA, B, Bdesc, SB, beta, C, Cdesc, D, Ddesc,
+                                               expert_offsets_dev, num_experts, stream)
+
+
+# ---- around the grouped products (gemm_moe.h) ------------------------------------------
+
+def gemm_route_scratch(experts) -> int:
+    """Bytes of workspace partials that gemm_moe_route may need (GEMM_ROUTE_SCRATCH)."""
+    return 304 * 4 * int(experts)
+
+
+def gemm_moe_route(h, op, L, Ldesc, ids, weights, rows, expert_offsets, workspace, stream):
+    return (_lib or lib()).gemm_moe_route(h, op, L, Ldesc, ids, weights, rows, expert_offsets, workspace, stream)
+
+
+def gemm_moe_dispatch(h, X, Xdesc, rows, topk, Y, Ydesc, S, stream):
+    return (_lib or lib()).gemm_moe_dispatch(h, X, Xdesc, rows, topk, Y, Ydesc, S, stream)
+
+
+def gemm_moe_combine(h, Y, Ydesc, rows, weights, topk, beta, C, Cdesc, D, Ddesc, stream):
+    return (_lib or lib()).gemm_moe_combine(h, Y, Ydesc, rows, weights, topk, beta, C, Cdesc, D, Ddesc, stream)
 
 
 # ---- torch convenience (memory and streams only) ------------------------------------

@@ -11,7 +11,7 @@
 #include <algorithm>
 #include <atomic>
 
-#include "handle_internal.h"
+#include "api_checks.h"
 #include "mx_gemm.h"
 
 using namespace qg;
@@ -21,27 +21,7 @@ static_assert((int)GEMM_MXFP4 == (int)MXF_MXFP4 && (int)GEMM_NVFP4 == (int)MXF_N
 
 namespace {
 
-bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-// How rows may be moved: 2 in 32-byte pieces, 1 in 16-byte ones, 0 by element.
-int row_alignment(const void* p, int64_t ld, int64_t element) {
-    if (!p) return 2;
-    return aligned(p, 32) && ld * element % 32 == 0 ? 2 : aligned(p, 16) && ld * element % 16 == 0 ? 1 : 0;
-}
-const void* past(const void* p, int64_t n, int64_t element) {
-    return p ? static_cast<const char*>(p) + n * element : nullptr;
-}
 bool known_format(int32_t f) { return f == GEMM_MXFP4 || f == GEMM_NVFP4; }
-int64_t float_size(int32_t t) { return t == GEMM_F32 ? 4 : (t == GEMM_F16 || t == GEMM_BF16) ? 2 : 0; }
-
-int check_matrix(const gemm_layout_t* d, int32_t order, int64_t rows, int64_t cols) {
-    if (d->order != order) return GEMM_ERR_UNSUPPORTED;
-    if (d->rows != rows || d->cols != cols || d->num < 1) return GEMM_ERR_INVALID_ARG;
-    if (rows < 0 || cols < 0 || rows > INT32_MAX || cols > INT32_MAX) return GEMM_ERR_INVALID_ARG;
-    const int64_t inner = order == GEMM_ROW_MAJOR ? cols : rows;
-    if (d->ld < (inner > 0 ? inner : 1) || d->ld > ((int64_t)1 << 40)) return GEMM_ERR_INVALID_ARG;
-    if (d->num > 1 && (d->batch_stride < 0 || d->batch_stride > ((int64_t)1 << 50))) return GEMM_ERR_INVALID_ARG;
-    return GEMM_OK;
-}
 
 // Packed codes: 16-byte rows, matrices one after another when there are several.
 int check_codes(const gemm_layout_t* d, int64_t lines) {
@@ -59,19 +39,6 @@ int64_t scale_bytes(int32_t format, int64_t rows, int64_t cols, int32_t experts)
 bool tensor_scale_ok(int32_t format, float g) {
     if (format == GEMM_MXFP4) return g == 1.0f;
     return g >= 0x1p-64f && g <= 0x1p64f;  // false for NaN
-}
-
-int check_experts(gemm_handle_t h, const int32_t* offsets, int32_t experts) {
-    if (!offsets && experts == 0) return GEMM_OK;
-    if (!offsets || experts < 1 || experts > 4096) return GEMM_ERR_INVALID_ARG;
-    if (!aligned(offsets, 4) || !handle_device_pointer(h, offsets)) return GEMM_ERR_INVALID_ARG;
-    return GEMM_OK;
-}
-
-int status_of(cudaError_t e) {
-    if (e == cudaSuccess) return GEMM_OK;
-    cudaGetLastError();
-    return GEMM_ERR_CUDA;
 }
 
 // The widest row a quantising grid covers: 512 columns a block, 65535 blocks.
@@ -397,18 +364,6 @@ int run_product(gemm_handle_t h, const gemm_op_t* op, MxProduct& p, cudaStream_t
         return status_of(launch_mx_pair(p.format, m, k, k.programs, st));
     }
     return status_of(launch_mx_gemm(c.bn, p.format, m, k, (int)(tm * tn * c.splits), st));
-}
-
-// Nothing throws across the C ABI.
-template <typename F>
-int guarded(gemm_handle_t h, F&& f) {
-    if (!h) return GEMM_ERR_INVALID_ARG;
-    try {
-        const int rc = handle_bind(h);
-        return rc ? rc : f();
-    } catch (...) {
-        return GEMM_ERR_CUDA;
-    }
 }
 
 }  // namespace

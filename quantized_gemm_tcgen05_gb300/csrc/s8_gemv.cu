@@ -1,0 +1,167 @@
+// Streaming int8 product on the CUDA cores, for a few rows per expert: B's codes
+// are read once and are the work, four products an instruction (dp4a) into exact
+// 32-bit sums.
+//
+// A warp owns R = 4 rows of B and one of `kslices` contiguous slices of K; its lanes
+// take 16-byte chunks.  A block of 8 warps covers 8 / kslices row groups for one tile
+// of MT tokens.  Lanes' and slices' sums are integers: any order gives the same.
+#include <atomic>
+
+#include "s8_epilogue.cuh"
+
+namespace qg {
+
+namespace {
+
+constexpr int R = 4, WARPS = 8;
+
+// Chunk c of a row of K codes; past K zeros, and nothing is read there.
+__device__ __forceinline__ uint4 chunk_of(const int8_t* row, int64_t c, int64_t K) {
+    if ((c + 1) * 16 <= K) return __ldg(reinterpret_cast<const uint4*>(row) + c);
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (c * 16 + i < K) w[i / 4] |= (uint32_t)(uint8_t)row[c * 16 + i] << (8 * (i % 4));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int s) {
+    s = __dp4a((int)a.x, (int)b.x, s);
+    s = __dp4a((int)a.y, (int)b.y, s);
+    s = __dp4a((int)a.z, (int)b.z, s);
+    return __dp4a((int)a.w, (int)b.w, s);
+}
+
+template <int MT, int U>
+__global__ void __launch_bounds__(WARPS * 32, MT == 1 ? 4 : 2) s8_gemv_kernel(const __grid_constant__ S8GemmParams p) {
+    __shared__ int32_t red[WARPS][MT][R];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = p.kslices, per_block = WARPS / S;
+    const int gi = warp / S, s = warp % S;
+    const int64_t N = p.epi.N, K = p.K;
+    const int64_t nchunk = (K + 15) / 16, cps = (nchunk + S - 1) / S;
+    const int64_t cbeg = s * cps, cend = cbeg + cps < nchunk ? cbeg + cps : nchunk;
+    const int64_t ngroups = (N + R - 1) / R;
+    griddep_launch_dependents();
+    griddep_wait();
+    int expert = 0, rows = 0;
+    int64_t m0 = 0, atom_row = 0;
+    if (p.offsets) {
+        if (!mx_expert_block(p.offsets, p.num_experts, p.epi.M, MT, blockIdx.y, lane, &expert, &m0, &rows, &atom_row)) return;
+    } else {
+        m0 = (int64_t)blockIdx.y * MT;
+        rows = (int)(p.epi.M - m0 < MT ? p.epi.M - m0 : MT);
+    }
+    if (rows <= 0) return;
+    const int8_t* B = p.B + expert * p.b_bs;
+    const EpiArith ar0 = epi_arith(p.epi);
+    for (int64_t gbase = (int64_t)blockIdx.x * per_block; gbase < ngroups; gbase += (int64_t)gridDim.x * per_block) {
+        const int64_t grp = gbase + gi;
+        int32_t acc[MT][R];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < R; ++r) acc[m][r] = 0;
+        if (grp < ngroups) {
+            const int8_t* brow[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r)  // (rows past N read the last one; their sums are not stored)
+                brow[r] = B + (grp * R + r < N ? grp * R + r : N - 1) * p.ldb;
+            for (int64_t c = cbeg + lane; c < cend; c += 32 * U) {
+                uint4 b[U][R];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int r = 0; r < R; ++r)
+                        if (c + 32 * u < cend) b[u][r] = chunk_of(brow[r], c + 32 * u, K);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (c + 32 * u >= cend) break;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        if (m >= rows) break;
+                        const uint4 a = chunk_of(p.A + (m0 + m) * p.lda, c + 32 * u, K);
+#pragma unroll
+                        for (int r = 0; r < R; ++r) acc[m][r] = dot16(a, b[u][r], acc[m][r]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int32_t v = __reduce_add_sync(0xFFFFFFFFu, acc[m][r]);
+                if (lane == 0) red[warp][m][r] = v;
+            }
+        __syncthreads();
+        // a thread takes a pair of neighbouring columns
+        for (int t = threadIdx.x; t < per_block * MT * (R / 2); t += WARPS * 32) {
+            const int g2 = t / (MT * (R / 2)), m = t / (R / 2) % MT, r = t % (R / 2) * 2;
+            const int64_t n = (gbase + g2) * R + r, row = m0 + m;
+            if (m >= rows || n >= N) continue;
+            const int have = N - n < 2 ? 1 : 2;
+            if (!mx_block_in_bounds(p.epi, row, 1, n, have)) continue;
+            int32_t s0 = 0, s1 = 0;
+            for (int k = 0; k < S; ++k) {
+                s0 += red[g2 * S + k][m][r];
+                s1 += red[g2 * S + k][m][r + 1];
+            }
+            EpiArith ar = ar0;
+            ar.alpha = 1.0f;
+            const float token = s8_token_factor(p, row);
+            const float v0 = s8_scaled(s0, token, s8_channel_factor(p, expert, n));
+            const float v1 = have > 1 ? s8_scaled(s1, token, s8_channel_factor(p, expert, n + 1)) : 0.0f;
+            const bool use_c = ar.beta != 0.0f;
+            const float c0 = use_c ? ld_elem(p.epi.C, p.epi.d_type, row * p.epi.ldc + n) : 0.0f;
+            const float c1 = use_c && have > 1 ? ld_elem(p.epi.C, p.epi.d_type, row * p.epi.ldc + n + 1) : 0.0f;
+            float x0, x1;
+            with_epi_act(p.epi, [&](auto act) {
+                constexpr int ACT = decltype(act)::value;
+                const float b0 = ACT >= 0 ? bias_at(ar, n) : 0.0f, b1 = ACT >= 0 && have > 1 ? bias_at(ar, n + 1) : 0.0f;
+                mx_value2_any<ACT>(ar, p.epi.d_type, v0, v1, c0, c1, b0, b1, x0, x1);
+            });
+            st_elem(p.epi.D, p.epi.d_type, row * p.epi.ldd + n, x0);
+            if (have > 1) st_elem(p.epi.D, p.epi.d_type, row * p.epi.ldd + n + 1, x1);
+        }
+        __syncthreads();  // red[] is written again
+    }
+}
+
+template <int MT, int U>
+cudaError_t launch_t(const S8GemmParams& p, int sm_count, cudaStream_t st) {
+    const int64_t groups = ceil_div(p.epi.N, R), blocks = ceil_div(groups, WARPS / p.kslices);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(blocks < 1 << 30 ? blocks : 1 << 30), (unsigned)p.tiles_m);
+    cfg.blockDim = dim3(WARPS * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, s8_gemv_kernel<MT, U>, p);
+}
+
+}  // namespace
+
+int s8_gemv_slices(int64_t n, int64_t k, int64_t tiles, int sm_count) {
+    const int64_t groups = ceil_div(n, R), nchunk = ceil_div(k, 16), want = (int64_t)sm_count * 32;
+    int s = 1;
+    // more slices while the GPU is short of warps and every lane keeps a chunk
+    while (s < WARPS && groups * tiles * s < want && nchunk / (2 * s) >= 32) s *= 2;
+    return s;
+}
+
+cudaError_t launch_s8_gemv(const S8GemmParams& p, int sm_count, cudaStream_t st) {
+    if (p.tiles_m < 1 || p.tiles_m > 65535) return cudaErrorInvalidValue;
+    switch (p.tile_rows) {
+        case 1: return launch_t<1, 2>(p, sm_count, st);
+        case 2: return launch_t<2, 2>(p, sm_count, st);
+        case 4: return launch_t<4, 1>(p, sm_count, st);
+        case 8: return launch_t<8, 1>(p, sm_count, st);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace qg
