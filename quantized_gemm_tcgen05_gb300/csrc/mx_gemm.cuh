@@ -70,21 +70,6 @@ struct MxCfg {
     }
 };
 
-// Bulk copy from this CTA's shared memory to another CTA's (cluster addresses),
-// completing its bytes on a barrier there.
-__device__ __forceinline__ void bulk_s2cluster(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
-    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "r"(src), "r"(bytes), "r"(bar)
-                 : "memory");
-}
-
-// What is in flight within a cluster lands in far less than this.
-__device__ __forceinline__ void mx_settle() {
-    const uint64_t t0 = globaltimer_ns();
-    while (globaltimer_ns() - t0 < 200000ull) {
-    }
-}
-
 // The steps of mx_exchange.h: announcements on `idle`, shares (`bytes` each) out of
 // `parts` into the others' `recv`, counted by their `part`.
 struct MxClusterLink {

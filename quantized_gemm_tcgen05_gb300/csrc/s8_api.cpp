@@ -109,8 +109,53 @@ int64_t token_tiles(const S8GemmParams& p, int64_t rows) {
     return std::min(p.epi.M / rows + p.num_experts, p.epi.M);
 }
 
+enum S8Kernel { S8_GEMV, S8_TILE };
+struct S8Choice {
+    S8Kernel kernel;
+    int width;   // S8_TILE: 32 or 128 tokens a tile at most
+    int rows;    // tokens of a tile
+    int splits;
+};
+
+// Rows an expert has on average, or all.
+int64_t rows_each(const S8GemmParams& p) { return p.num_experts ? ceil_div(p.epi.M, p.num_experts) : p.epi.M; }
+
+// GEMM_FORCE_KERNEL=s8_gemv / s8_t32 / s8_t128 (the names gemm_last_choice prints,
+// up to the slash) pins the kernel, for tests and sweeps.
+bool forced_kernel(S8Choice* c) {
+    const char* f = getenv("GEMM_FORCE_KERNEL");
+    if (!f || strncmp(f, "s8_", 3)) return false;
+    if (!strncmp(f, "s8_gemv", 7)) c->kernel = S8_GEMV;
+    else c->kernel = S8_TILE, c->width = strncmp(f, "s8_t32", 6) == 0 ? 32 : 128;
+    return true;
+}
+
+S8Choice choose(const S8GemmParams& p, int sm_count, int forced_split) {
+    const int64_t each = rows_each(p);
+    S8Choice c{each <= 4 ? S8_GEMV : S8_TILE, each <= 32 ? 32 : 128, 0, 1};
+    forced_kernel(&c);
+    if (c.kernel == S8_GEMV) {
+        c.rows = each <= 1 ? 1 : each <= 2 ? 2 : each <= 4 ? 4 : 8;
+        return c;
+    }
+    c.rows = (int)(ceil_div(ceil_div(each, ceil_div(each, c.width)), 16) * 16);
+    const int64_t tiles = token_tiles(p, c.rows) * ceil_div(p.epi.N, 128), steps = ceil_div(p.K, S8_KSTEP);
+    const int64_t slots = (int64_t)sm_count * (c.width == 32 ? 2 : 1);
+    while (c.splits < 8 && 2 * c.splits <= steps && (forced_split ? c.splits < forced_split : tiles * c.splits * 2 <= slots)) c.splits *= 2;
+    return c;
+}
+
+// Tensor map over int8 codes: [matrices][lines][codes of a line], boxes of one
+// K-step (128 codes, swizzled) x box_lines.
+int map_s8(gemm_handle_t h, CUtensorMap* m, const void* ptr, int64_t k, int64_t lines, int64_t ld, int32_t num, int64_t bstride,
+           int32_t box_lines) {
+    const uint64_t dims[3] = {(uint64_t)k, (uint64_t)lines, (uint64_t)num};
+    const uint64_t strides[2] = {(uint64_t)ld, (uint64_t)bstride};
+    const uint32_t box[3] = {S8_KSTEP, (uint32_t)box_lines, 1};
+    return handle_encode(h, m, CU_TENSOR_MAP_DATA_TYPE_UINT8, num > 1 ? 3 : 2, ptr, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 int run_product(gemm_handle_t h, const gemm_op_t* op, S8GemmParams& p, cudaStream_t st) {
-    (void)op;
     const int64_t M = p.epi.M, N = p.epi.N;
     if (M == 0 || N == 0) {
         handle_set_choice(h, "empty", M, N, p.K);
@@ -120,16 +165,40 @@ int run_product(gemm_handle_t h, const gemm_op_t* op, S8GemmParams& p, cudaStrea
         handle_set_choice(h, "scale_c", M, N, p.K);
         return status_of(launch_mx_no_k(p.epi, p.offsets, p.num_experts, st));
     }
-    const int64_t per = p.num_experts ? ceil_div(M, p.num_experts) : M;
-    p.tile_rows = per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 8;
-    const int64_t tiles = token_tiles(p, p.tile_rows);
-    if (tiles > 65535) return GEMM_ERR_UNSUPPORTED;
-    p.tiles_m = (int32_t)tiles;
-    p.kslices = s8_gemv_slices(N, p.K, tiles, handle_sm_count(h));
+    const S8Choice c = choose(p, handle_sm_count(h), op->splitk);
+    const char* grouped = p.num_experts ? "_grouped" : "";
     char name[64];
-    snprintf(name, sizeof name, "s8%s_gemv%d/k%d", p.num_experts ? "_grouped" : "", p.tile_rows, p.kslices);
+    p.tile_rows = c.rows;
+    const int64_t tm = token_tiles(p, c.rows);
+    if (c.kernel == S8_GEMV) {
+        if (tm > 65535) return GEMM_ERR_UNSUPPORTED;
+        p.tiles_m = (int32_t)tm;
+        p.kslices = s8_gemv_slices(N, p.K, tm, handle_sm_count(h));
+        snprintf(name, sizeof name, "s8%s_gemv%d/k%d", grouped, c.rows, p.kslices);
+        handle_set_choice(h, name, M, N, p.K);
+        return status_of(launch_s8_gemv(p, handle_sm_count(h), st));
+    }
+    const int64_t tn = ceil_div(N, 128);
+    if (tm * tn * c.splits > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+    p.tiles_m = (int32_t)tm;
+    p.tiles_n = (int32_t)tn;
+    p.k_steps = (int32_t)ceil_div(p.K, S8_KSTEP);
+    p.splits = c.splits;
+    p.b3d = p.num_experts > 1;
+    p.idesc = make_idesc_f16(0, 128, c.rows);
+    const int64_t es = float_size(p.epi.d_type);
+    auto four = [&](const void* q, int64_t ld) { return !q || (aligned(q, (uintptr_t)(4 * es)) && ld % 4 == 0); };
+    p.vec4 = four(p.epi.D, p.epi.ldd) && four(p.epi.C, p.epi.ldc);
+    p.status = handle_status(h);
+    p.timeout_ns = handle_timeout_ns(h);
+    S8Maps m;
+    memset(&m, 0, sizeof m);
+    int rc = map_s8(h, &m.a, p.A, p.K, M, p.lda, 1, 0, c.rows);
+    if (rc == GEMM_OK) rc = map_s8(h, &m.b, p.B, p.K, N, p.ldb, p.num_experts > 1 ? p.num_experts : 1, p.b_bs, 128);
+    if (rc != GEMM_OK) return rc;
+    snprintf(name, sizeof name, "s8%s_t%d/%s%d", grouped, c.width, c.splits > 1 ? "splitk" : "rows", c.splits > 1 ? c.splits : c.rows);
     handle_set_choice(h, name, M, N, p.K);
-    return status_of(launch_s8_gemv(p, handle_sm_count(h), st));
+    return status_of(launch_s8_gemm(c.width, m, p, (int)(tm * tn * c.splits), st));
 }
 
 }  // namespace

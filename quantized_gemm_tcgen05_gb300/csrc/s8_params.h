@@ -18,11 +18,32 @@ struct S8GemmParams {
     int32_t tiles_m;           // token tiles (grouped: an upper bound)
     int32_t tile_rows;         // tokens of a tile
     int32_t kslices;           // streaming kernel: warps that share a row's K
+    // the tensor-core kernels
+    int32_t tiles_n;           // tiles of channels
+    int32_t k_steps;           // 128-wide K-steps
+    int32_t splits;            // CTAs of a cluster, each a share of the K-steps
+    int32_t programs;          // persistent programs (pair kernel)
+    int32_t b3d;               // B's map takes an expert coordinate
+    uint32_t idesc;
+    int32_t vec4;              // D (and C): four columns of a row at once
+    uint32_t* status;
+    uint64_t timeout_ns;
 };
+
+struct S8Maps {
+    CUtensorMap a, b;
+};
+
+constexpr int S8_KSTEP = 128;   // codes of one 128-byte swizzle row
+constexpr int S8_CHUNK = 8;     // K-steps whose sums fp32 holds exactly: 1024 products of at most 2^14
 
 // The streaming kernel on the CUDA cores: any M, meant for a few rows per expert.
 constexpr int S8_GEMV_ROWS = 8;  // tokens of a tile, at most
 cudaError_t launch_s8_gemv(const S8GemmParams& p, int sm_count, cudaStream_t st);
 int s8_gemv_slices(int64_t n, int64_t k, int64_t tiles, int sm_count);
+
+// The tensor-core kernel, one tile of 128 channels x up to `width` tokens per
+// cluster (width 32 or 128).
+cudaError_t launch_s8_gemm(int width, const S8Maps& m, const S8GemmParams& p, int grid, cudaStream_t st);
 
 }  // namespace qg

@@ -12,7 +12,7 @@ import quantized_gemm_tcgen05_gb300 as qg
 
 pytestmark = pytest.mark.gpu
 OK = qg.GEMM_OK
-KERNELS = ["", "s8_gemv"]
+KERNELS = ["", "s8_gemv", "s8_t32", "s8_t128"]
 
 
 @pytest.fixture(scope="module")
@@ -228,6 +228,21 @@ def test_graph_and_stream(h, m, n, k):
             g.replay()
         side.synchronize()
     assert torch.equal(p.out[:m, :n].cpu(), p.expected())
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("m,n,k", [(1, 4096, 14336), (31, 8192, 4096), (130, 2048, 8192)])
+def test_cold_operands_back_to_back(h, pin, kernel, m, n, k):
+    """Operands that come from far (copies land late and out of order), launches that overlap."""
+    pin(kernel)
+    ps = [Problem(m, n, k, "f32", seed=i) for i in range(3)]
+    flush = torch.empty(160 << 20, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        flush.zero_()
+        for p in ps:
+            p.run(h)
+    for p in ps:
+        assert torch.equal(p.out[:m, :n].cpu(), p.expected())
 
 
 def test_offsets_beyond_32_bits(h):
