@@ -135,17 +135,18 @@ int gemm_moe_route(gemm_handle_t h, const gemm_route_t* op, const void* L, const
         p.weights = weights;
         p.rows = rows;
         p.offsets = expert_offsets;
-        if (expert_offsets && tokens <= ROUTE_ONE_BLOCK) {
+        const bool scratch = workspace && workspace->partials && workspace->partials_size >= GEMM_ROUTE_SCRATCH(experts);
+        if (expert_offsets && (tokens <= ROUTE_WARPS || (tokens <= ROUTE_ONE_BLOCK && !scratch))) {
             p.blocks = 1;
             p.tokens_per_block = ROUTE_ONE_BLOCK;
         } else {
-            const int64_t per = std::max<int64_t>(8, ceil_div(tokens, ROUTE_MAX_BLOCKS));
+            // a token a warp, blocks for every SM, then more tokens a warp
+            const int64_t per = std::max<int64_t>(ROUTE_WARPS, ceil_div(tokens, std::min(handle_sm_count(h), ROUTE_MAX_BLOCKS)));
             p.tokens_per_block = (int32_t)per;
             p.blocks = (int32_t)ceil_div(tokens, per);
         }
         if (expert_offsets && p.blocks > 1) {
-            if (!workspace || !workspace->partials) return (int)GEMM_ERR_WORKSPACE;
-            if (workspace->partials_size < GEMM_ROUTE_SCRATCH(experts)) return (int)GEMM_ERR_WORKSPACE;
+            if (!scratch) return (int)GEMM_ERR_WORKSPACE;
             if (!usable(h, workspace->partials, 16)) return (int)GEMM_ERR_INVALID_ARG;
             p.counts = static_cast<int32_t*>(workspace->partials);
         }

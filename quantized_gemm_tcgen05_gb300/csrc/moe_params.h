@@ -11,6 +11,7 @@ constexpr int MOE_MAX_TOPK = 32;
 // counts), and tokens that one block handles alone.
 constexpr int ROUTE_MAX_BLOCKS = 304;
 constexpr int ROUTE_ONE_BLOCK = 64;
+constexpr int ROUTE_WARPS = 16;  // of a block: tokens it works on at a time
 
 enum RouteScore : int32_t { ROUTE_SOFTMAX = 0, ROUTE_SIGMOID = 1 };
 

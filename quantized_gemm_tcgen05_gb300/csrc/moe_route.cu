@@ -3,15 +3,18 @@
 //
 // A warp takes a token; lane i holds experts i, i + 32, ...  Scores are numbers
 // turned into unsigned keys of the same order (0: never chosen), so that a round
-// of the choice is one warp-wide integer maximum and one minimum over the indices
-// that have it.
+// of the choice is a warp-wide integer maximum.
 //
 // The choice is defined in 64 bits.  Without a bias it is the logits' own order,
-// which fp32 holds exactly.  With one (and for groups' scores) the scores are
-// first taken in fp32: where two neighbours in the order, or the last group kept
-// and the first left out, are nearer than fp32's error, the token is done again in
-// 64 bits.  That is rare (a few tokens in a thousand), where 64-bit exponentials
-// for all would be most of the time.
+// which fp32 holds exactly.  With one (and for groups' scores) it is that of sums
+// whose error fp32 leaves open.  Three tries, each only where the one before
+// cannot tell:
+//   1. keys of 22 bits with the expert's number below them: a round is one maximum,
+//      and needs no second one for the index;
+//   2. keys of 32 bits (a few tokens in a hundred);
+//   3. scores in 64 bits (one in a thousand).  All tokens that way would take ten
+//      times the time: there are two 64-bit units an SM.
+// What bounds it is the number of instructions: 4001 x 256 logits are 4 MB.
 #include "common.cuh"
 #include "moe_params.h"
 
@@ -59,12 +62,14 @@ struct KeyType<double> {
     using type = uint64_t;
 };
 
-// A bound of the fp32 error of c = s + bias, or of a sum of two of them.  s: the
-// exponential's argument is off by up to 2^-24 |l - max| (x e^-x is at most 0.37),
-// the exponential by 2 units, a sum of E <= 1024 of them by 10 roundings, the
-// quotient by one: below 1.5e-6 s.  The bias and the sum add roundings relative to
-// themselves.
-__device__ __forceinline__ float error_bound(float c) { return 4e-6f * (1.0f + fabsf(c)); }
+// A bound of the fp32 error of a token's scores s, without the part that grows with
+// c.  Sigmoid: the exponential is off by 2 units, s (1 - s) 2^-22 <= 2^-24, a sum and a
+// quotient by half a unit each: below 2e-7.  Softmax: the exponential's argument is off
+// by up to 2^-24 |l - max| (x e^-x is at most 0.37), the exponential by 2 units, a sum of
+// E <= 1024 of them by 37 roundings at most, the quotient by one: below 3e-6 s.
+__device__ __forceinline__ float score_error(int32_t score, float largest) { return score == ROUTE_SOFTMAX ? 4e-6f * largest : 4e-7f; }
+// ... of c = s + bias.
+__device__ __forceinline__ float choice_error(float err, float c) { return err + 1.2e-7f * fabsf(c); }
 
 // Choose for one token.  l: this lane's logits (-inf past the last expert).
 // Slot j's expert lands in lane j's `id` (-1: none).  Returns false where fp32
@@ -76,6 +81,7 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[V]
     const bool by_logit = !p.bias;
     K key[V];
     bool sure = true;
+    float err = 0.0f;
     if (!by_logit || p.groups > 1) {
         T s[V];
         if (p.score == ROUTE_SOFTMAX) {
@@ -88,7 +94,9 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[V]
             sum = warp_sum(sum);
 #pragma unroll
             for (int v = 0; v < V; ++v) s[v] = s[v] / sum;
+            err = score_error(p.score, (float)((T)1 / sum));
         } else {
+            err = score_error(p.score, 1.0f);
 #pragma unroll
             for (int v = 0; v < V; ++v) s[v] = (T)1 / ((T)1 + exp_t(-(T)l[v]));
         }
@@ -103,12 +111,15 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[V]
     if (p.groups > 1) {
         // group g's score in lane g, as a key
         const int size = p.experts / p.groups;
+        int group[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) group[v] = (v * 32 + lane) / size;
         K mine = 0;
         for (int g = 0; g < p.groups; ++g) {
             K first = 0;
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if ((v * 32 + lane) / size == g && key[v] > first) first = key[v];
+                if (group[v] == g && key[v] > first) first = key[v];
             const K a = warp_max(first);
             K score = a;
             if (p.group_best > 1 && a) {
@@ -119,7 +130,7 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[V]
                 bool skipped = !holder;
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    if ((v * 32 + lane) / size != g) continue;
+                    if (group[v] != g) continue;
                     if (!skipped && key[v] == a)
                         skipped = true;
                     else if (key[v] > second)
@@ -143,12 +154,12 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[V]
             const uint32_t best = __reduce_max_sync(FULL, !kept && lane < p.groups ? (uint32_t)mine : 0u);
             if (best) {
                 const float w = number_of(worst), b = number_of(best);
-                if (w - b < 2.0f * error_bound(w)) sure = false;
+                if (w - b < 4.0f * choice_error(err, w)) sure = false;
             }
         }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int g = (v * 32 + lane) / size;
+            const int g = group[v];
             if (!(g < 32 && kept_mask >> g & 1)) key[v] = 0;
             else if (by_logit) key[v] = key[v] ? key_of((T)l[v]) : (K)0;
         }
@@ -175,7 +186,7 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[V]
         if constexpr (!EXACT) {
             if (check && before) {
                 const float x = number_of(before), y = number_of(m);
-                if (x - y < 2.0f * error_bound(x)) {
+                if (x - y < 2.0f * choice_error(err, fmaxf(fabsf(x), fabsf(y)))) {
                     // equal logits with equal biases have equal scores in any arithmetic
                     float la = 0.0f, lb = 0.0f;
 #pragma unroll
@@ -199,15 +210,165 @@ __device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[V]
     return sure;
 }
 
-// (The logits are read again: an array handed to a function would live in memory.)
+// The same with keys of 22 bits above 1023 - expert: the keys differ, the largest
+// one names its expert, and of equal ones the lowest index comes first.  16-bit
+// logits lose nothing that way; else 2^-13 of a number are missing.
 template <int V>
-__device__ __noinline__ int choose_exactly(const RouteParams& p, int t, float top, int lane) {
-    float l[V];
+__device__ __forceinline__ bool choose_fast(const RouteParams& p, const float (&l)[V], float top, const float* bias, bool exact_keys,
+                                            int lane, int& id) {
+    constexpr float CUT = 1.3e-4f;
+    const bool by_logit = !p.bias;
+    uint32_t key[V];
+    bool sure = true;
+    float err = 0.0f;
+    auto packed = [&](float c, int v) { return (key_of(c) & ~1023u) | (uint32_t)(1023 - (v * 32 + lane)); };
+    auto number = [](uint32_t k) { return number_of(k & ~1023u); };
+    if (!by_logit || p.groups > 1) {
+        float s[V];
+        if (p.score == ROUTE_SOFTMAX) {
+            float sum = 0.0f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) l[v] = v * 32 + lane < p.experts ? ld_elem(p.L, p.type, t * p.ld + v * 32 + lane) : -INFINITY;
+            for (int v = 0; v < V; ++v) {
+                s[v] = l[v] > -INFINITY ? expf(l[v] - top) : 0.0f;
+                sum += s[v];
+            }
+            const float r = 1.0f / warp_sum(sum);
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] *= r;
+            err = score_error(p.score, r);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] = 1.0f / (1.0f + expf(-l[v]));
+            err = score_error(p.score, 1.0f);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float b = by_logit ? 0.0f : bias[v * 32 + lane];
+            key[v] = l[v] > -INFINITY && b > -INFINITY ? packed(s[v] + b, v) : 0u;
+        }
+    }
+    if (p.groups > 1) {
+        // group g's two largest keys in lane g
+        const int size = p.experts / p.groups;
+        const bool two = p.group_best > 1;
+        uint32_t m1 = 0, m2 = 0;
+        unsigned kept_mask;
+        auto merge = [&](uint32_t a, uint32_t b) {
+            m2 = m1 > a ? (m2 > a ? m2 : a) : (m1 > b ? m1 : b);
+            m1 = m1 > a ? m1 : a;
+        };
+        if (size % 32 == 0) {  // a group is all lanes of some registers
+            int g = 0, left = size;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const uint32_t a = warp_max(key[v]), b = two ? warp_max(key[v] == a ? 0u : key[v]) : 0u;
+                if (lane == g) merge(a, b);
+                if ((left -= 32) == 0) {
+                    left = size;
+                    ++g;
+                }
+            }
+        } else {
+            int group[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) group[v] = (v * 32 + lane) / size;
+            for (int g = 0; g < p.groups; ++g) {
+                uint32_t first = 0, second = 0;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (group[v] == g) first = first > key[v] ? first : key[v];
+                const uint32_t a = warp_max(first);
+                if (two) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        if (group[v] == g && key[v] != a) second = second > key[v] ? second : key[v];
+                    second = warp_max(second);
+                }
+                if (lane == g) merge(a, second);
+            }
+        }
+        const float score = number(m1) + (two && m2 ? number(m2) : 0.0f);
+        const float spread = CUT * (fabsf(number(m1)) + (two && m2 ? fabsf(number(m2)) : 0.0f)) + 2.0f * choice_error(err, score);
+        const uint32_t mine = lane < p.groups && m1 ? key_of(score) : 0u;
+        int better = 0;
+        for (int g = 0; g < p.groups; ++g) {
+            const uint32_t other = __shfl_sync(FULL, mine, g);
+            better += other > mine || (other == mine && g < lane);
+        }
+        const bool kept = lane < p.groups && better < p.group_topk;
+        kept_mask = __ballot_sync(FULL, kept);
+        const uint32_t low = __reduce_min_sync(FULL, kept ? key_of(score - spread) : 0xFFFFFFFFu);
+        const uint32_t high = warp_max(!kept && mine ? key_of(score + spread) : 0u);
+        // (a NaN, of infinities, counts as a number here: then the next try decides)
+        if (__any_sync(FULL, lane < p.groups && m1 && !(fabsf(score) < INFINITY))) sure = false;
+        if (high && __any_sync(FULL, kept && mine) && !(low > high)) sure = false;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int g = size % 32 == 0 ? v * 32 / size : (v * 32 + lane) / size;
+            if (!(g < 32 && kept_mask >> g & 1)) key[v] = 0;
+            else if (by_logit && key[v]) key[v] = packed(l[v], v);
+        }
+    } else if (by_logit) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = l[v] > -INFINITY ? packed(l[v], v) : 0u;
+    }
+    uint32_t best = 0, before = 0;
+    id = -1;
+    const int rounds = p.topk + (exact_keys ? 0 : 1);
+    for (int j = 0; j < rounds; ++j) {
+        // the largest key below the last one
+        best = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint32_t k = j == 0 || key[v] < before ? key[v] : 0u;
+            best = best > k ? best : k;
+        }
+        const uint32_t m = warp_max(best);
+        if (!m) break;
+        if (!exact_keys && j > 0) {
+            if (by_logit) {
+                sure &= (before >> 10) != (m >> 10);
+            } else {
+                const float x = number(before), y = number(m), most = fmaxf(fabsf(x), fabsf(y));
+                sure &= x - y > CUT * most + 2.0f * choice_error(err, most);
+            }
+        }
+        before = m;
+        if (lane == j && j < p.topk) id = 1023 - (int)(m & 1023u);
+    }
+    return sure;
+}
+
+template <int V>
+__device__ __forceinline__ void load_logits(const RouteParams& p, int t, int lane, float (&l)[V]) {
+    const int64_t at = t * p.ld + lane;
+    auto load = [&](auto of) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) l[v] = v * 32 + lane < p.experts ? of(at + v * 32) : -INFINITY;
+    };
+    if (p.type == DT_F32)
+        load([&](int64_t i) { return static_cast<const float*>(p.L)[i]; });
+    else if (p.type == DT_BF16)
+        load([&](int64_t i) { return __bfloat162float(static_cast<const __nv_bfloat16*>(p.L)[i]); });
+    else
+        load([&](int64_t i) { return __half2float(static_cast<const __half*>(p.L)[i]); });
+}
+
+// The second and the third try.  (The logits are read again: an array handed to a
+// function would live in memory.)
+template <int V, typename T>
+__device__ __noinline__ int choose_again(const RouteParams& p, int t, float top, int lane, bool& sure) {
+    float l[V];
+    load_logits<V>(p, t, lane, l);
     int id;
-    choose<V, double>(p, l, top, lane, id);
+    sure = choose<V, T>(p, l, top, lane, id);
     return id;
+}
+template <int V>
+__device__ __forceinline__ int choose_carefully(const RouteParams& p, int t, float top, int lane) {
+    bool sure;
+    const int id = choose_again<V, float>(p, t, top, lane, sure);
+    return sure ? id : choose_again<V, double>(p, t, top, lane, sure);
 }
 
 // Where the experts' rows start: exclusive sums of `count` (block-wide; threads
@@ -255,40 +416,44 @@ __device__ __forceinline__ void place(const int32_t* ids, int32_t* rows, int64_t
     }
 }
 
-constexpr int ROUTE_THREADS = 256, ROUTE_ONE_THREADS = 512;
-
 // Block b takes tokens b * tokens_per_block ..; with rows wanted it counts its
 // entries by expert.  A single block then finishes the rows itself; several leave
 // their counts to route_place_kernel.
 template <int V>
-__global__ void __launch_bounds__(ROUTE_ONE_THREADS) route_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(32 * ROUTE_WARPS) route_kernel(const __grid_constant__ RouteParams p) {
     __shared__ int32_t count[MOE_MAX_EXPERTS], start[MOE_MAX_EXPERTS + 1], carry[32];
+    __shared__ float bias[32 * V];
     griddep_launch_dependents();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     if (p.offsets)
         for (int e = threadIdx.x; e < p.experts; e += blockDim.x) count[e] = 0;
-    __syncthreads();
     griddep_wait();
+    bool bias_bad = false;
+    if (p.bias)
+        for (int e = threadIdx.x; e < 32 * V; e += blockDim.x) {
+            bias[e] = e < p.experts ? p.bias[e] : 0.0f;
+            bias_bad |= bias[e] != bias[e];
+        }
+    bias_bad = __syncthreads_or(bias_bad ? 1 : 0) != 0;
+    const bool exact_keys = !p.bias && p.type != DT_F32;
     const int t0 = blockIdx.x * p.tokens_per_block;
     const int t1 = p.tokens - t0 < p.tokens_per_block ? p.tokens : t0 + p.tokens_per_block;
     for (int t = t0 + warp; t < t1; t += blockDim.x / 32) {
         float l[V];
         float top = -INFINITY;
-        bool bad = false;
+        bool bad = bias_bad;
+        load_logits<V>(p, t, lane, l);
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = v * 32 + lane;
-            l[v] = e < p.experts ? ld_elem(p.L, p.type, t * p.ld + e) : -INFINITY;
-            bad |= l[v] != l[v] || (p.score == ROUTE_SOFTMAX && l[v] == INFINITY);
-            if (p.bias && e < p.experts) bad |= p.bias[e] != p.bias[e];
+            bad |= l[v] != l[v];
             top = fmaxf(top, l[v]);
         }
-        bad = __any_sync(FULL, bad);
+        bad = __any_sync(FULL, bad || (p.score == ROUTE_SOFTMAX && top == INFINITY));
         top = number_of(warp_max(key_of(top)));
         int id = -1;
         float w = __uint_as_float(0x7FC00000u);
         if (!bad) {
-            if (!choose<V, float>(p, l, top, lane, id)) id = choose_exactly<V>(p, t, top, lane);
+            if (!choose_fast<V>(p, l, top, bias, exact_keys, lane, id)) id = choose_carefully<V>(p, t, top, lane);
             // weights: lane j has slot j
             const bool have = id >= 0;
             float x = -INFINITY;
@@ -347,12 +512,21 @@ __global__ void __launch_bounds__(512) route_place_kernel(const __grid_constant_
     for (int e = threadIdx.x; e < p.experts; e += blockDim.x) count[e] = before[e] = 0;
     __syncthreads();
     griddep_wait();
-    const int n = p.blocks * p.experts, mine = (int)blockIdx.x * p.experts;
-    for (int i = threadIdx.x; i < n; i += blockDim.x) {
-        const int32_t c = p.counts[i];
-        if (c) {
-            atomicAdd(&count[i % p.experts], c);
-            if (i < mine) atomicAdd(&before[i % p.experts], c);
+    // a thread has one expert and every `parts`-th block
+    const int threads = (int)blockDim.x;
+    for (int e0 = 0; e0 < p.experts; e0 += threads) {
+        const int here = p.experts - e0 < threads ? p.experts - e0 : threads, parts = threads / here;
+        const int e = e0 + (int)threadIdx.x % here, part = (int)threadIdx.x / here;
+        int32_t all = 0, below = 0;
+        if (part < parts) {
+#pragma unroll 8
+            for (int b = part; b < p.blocks; b += parts) {
+                const int32_t c = p.counts[(int64_t)b * p.experts + e];
+                all += c;
+                below += b < (int)blockIdx.x ? c : 0;
+            }
+            atomicAdd(&count[e], all);
+            atomicAdd(&before[e], below);
         }
     }
     __syncthreads();
@@ -373,8 +547,7 @@ __global__ void __launch_bounds__(512) route_place_kernel(const __grid_constant_
 
 cudaError_t launch_route(const RouteParams& p, cudaStream_t st) {
     const int per = (p.experts + 31) / 32;
-    const int threads = p.blocks == 1 ? ROUTE_ONE_THREADS : ROUTE_THREADS;
-    auto go = [&](auto kernel) { return launch_pdl(kernel, p.blocks, threads, 0, st, p); };
+    auto go = [&](auto kernel) { return launch_pdl(kernel, p.blocks, 32 * ROUTE_WARPS, 0, st, p); };
     cudaError_t e = per <= 1 ? go(route_kernel<1>) : per <= 2 ? go(route_kernel<2>) : per <= 4 ? go(route_kernel<4>) : per <= 8 ? go(route_kernel<8>) : per <= 16 ? go(route_kernel<16>) : go(route_kernel<32>);
     if (e != cudaSuccess || !p.offsets || p.blocks == 1) return e;
     return launch_pdl(route_place_kernel, p.blocks, 512, 0, st, p);
