@@ -35,7 +35,7 @@ typedef struct {
 
 /*
  * Choose `topk` experts for each of L's rows (tokens x experts, row-major,
- * f32 / f16 / bf16; at most 1024 experts).
+ * f32 / f16 / bf16; at most 1024 experts and 2^23 tokens).
  *   Choice scores  c = s + bias.  An expert whose logit or bias is -inf is never
  *     chosen.  With groups, only experts of the group_topk groups with the best
  *     group scores are.  Slots hold the experts with the largest c (without a

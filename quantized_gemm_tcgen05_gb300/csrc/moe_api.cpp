@@ -106,7 +106,7 @@ int gemm_moe_route(gemm_handle_t h, const gemm_route_t* op, const void* L, const
             if (experts % groups || op->group_topk < 1 || op->group_topk > groups) return (int)GEMM_ERR_INVALID_ARG;
             if (op->group_best < 1 || op->group_best > 2) return (int)GEMM_ERR_INVALID_ARG;
         }
-        if (tokens > INT32_MAX / MOE_MAX_TOPK) return (int)GEMM_ERR_UNSUPPORTED;
+        if (tokens > ROUTE_MAX_TOKENS) return (int)GEMM_ERR_UNSUPPORTED;
         if (tokens > 0 && (rows != nullptr) != (expert_offsets != nullptr)) return (int)GEMM_ERR_INVALID_ARG;
         if (op->bias && !usable(h, op->bias, 4)) return (int)GEMM_ERR_INVALID_ARG;
         if (expert_offsets && !usable(h, expert_offsets, 4)) return (int)GEMM_ERR_INVALID_ARG;
@@ -136,19 +136,21 @@ int gemm_moe_route(gemm_handle_t h, const gemm_route_t* op, const void* L, const
         p.rows = rows;
         p.offsets = expert_offsets;
         const bool scratch = workspace && workspace->partials && workspace->partials_size >= GEMM_ROUTE_SCRATCH(experts);
-        if (expert_offsets && (tokens <= ROUTE_WARPS || (tokens <= ROUTE_ONE_BLOCK && !scratch))) {
+        if (expert_offsets && (tokens <= ROUTE_FEW || (tokens <= ROUTE_ONE_BLOCK && !scratch))) {
             p.blocks = 1;
             p.tokens_per_block = ROUTE_ONE_BLOCK;
         } else {
-            // a token a warp, blocks for every SM, then more tokens a warp
-            const int64_t per = std::max<int64_t>(ROUTE_WARPS, ceil_div(tokens, std::min(handle_sm_count(h), ROUTE_MAX_BLOCKS)));
+            // a token a warp, a block an SM, then more tokens a warp
+            int64_t per = std::max<int64_t>(ROUTE_FEW, ceil_div(tokens, std::min(handle_sm_count(h), ROUTE_MAX_BLOCKS)));
+            if (per > 65535) per = ceil_div(tokens, ROUTE_MAX_BLOCKS);
             p.tokens_per_block = (int32_t)per;
             p.blocks = (int32_t)ceil_div(tokens, per);
         }
         if (expert_offsets && p.blocks > 1) {
             if (!scratch) return (int)GEMM_ERR_WORKSPACE;
             if (!usable(h, workspace->partials, 16)) return (int)GEMM_ERR_INVALID_ARG;
-            p.counts = static_cast<int32_t*>(workspace->partials);
+            p.counts = static_cast<uint16_t*>(workspace->partials);
+            p.pitch = (int32_t)(ceil_div(experts, 8) * 8);
         }
         return status_of(launch_route(p, reinterpret_cast<cudaStream_t>(stream)));
     });

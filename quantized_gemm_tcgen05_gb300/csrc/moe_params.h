@@ -11,7 +11,12 @@ constexpr int MOE_MAX_TOPK = 32;
 // counts), and tokens that one block handles alone.
 constexpr int ROUTE_MAX_BLOCKS = 304;
 constexpr int ROUTE_ONE_BLOCK = 64;
-constexpr int ROUTE_WARPS = 16;  // of a block: tokens it works on at a time
+// Threads of a block (a token a warp): with more experts a lane holds more keys.
+QG_HD int route_threads(int experts) { return experts <= 256 ? 1024 : 512; }
+constexpr int ROUTE_FEW = 16;    // tokens for which a single block is the quickest
+
+// A block's counts are 16-bit numbers, and rows 32-bit ones.
+constexpr int64_t ROUTE_MAX_TOKENS = 1 << 23;
 
 enum RouteScore : int32_t { ROUTE_SOFTMAX = 0, ROUTE_SIGMOID = 1 };
 
@@ -28,7 +33,8 @@ struct RouteParams {
     float* weights;
     int32_t* rows;      // with offsets, or null
     int32_t* offsets;
-    int32_t* counts;    // workspace: [blocks][experts]
+    uint16_t* counts;   // workspace: [blocks][pitch]
+    int32_t pitch;      // experts, rounded up to 8
     int32_t blocks, tokens_per_block;
 };
 

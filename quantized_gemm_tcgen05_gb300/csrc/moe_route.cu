@@ -7,14 +7,16 @@
 //
 // The choice is defined in 64 bits.  Without a bias it is the logits' own order,
 // which fp32 holds exactly.  With one (and for groups' scores) it is that of sums
-// whose error fp32 leaves open.  Three tries, each only where the one before
-// cannot tell:
-//   1. keys of 22 bits with the expert's number below them: a round is one maximum,
-//      and needs no second one for the index;
-//   2. keys of 32 bits (a few tokens in a hundred);
-//   3. scores in 64 bits (one in a thousand).  All tokens that way would take ten
-//      times the time: there are two 64-bit units an SM.
-// What bounds it is the number of instructions: 4001 x 256 logits are 4 MB.
+// whose error fp32 leaves open.  So, each only where the one before cannot tell:
+//   1. keys of 22 bits with the expert's number below them: a round is one maximum
+//      that names its expert;
+//   2. where neighbours in that order are too near, a lane takes each of the
+//      candidates and compares 32-bit keys (a token in ten or twenty);
+//   3. ... and 64-bit scores (one in a thousand).
+// All scores in 64 bits would take ten times the time: a 64-bit instruction of a warp
+// holds its unit for 16 cycles, and there is one unit an SM.
+// What bounds it is the number of instructions (some 800 a token of 256 experts) and
+// one token's chain of them: 4001 x 256 logits are 4 MB, 0.6 us.
 #include "common.cuh"
 #include "moe_params.h"
 
@@ -51,17 +53,6 @@ __device__ __forceinline__ T warp_sum(T x) {
 __device__ __forceinline__ float exp_t(float x) { return expf(x); }
 __device__ __forceinline__ double exp_t(double x) { return exp(x); }
 
-template <typename T>
-struct KeyType;
-template <>
-struct KeyType<float> {
-    using type = uint32_t;
-};
-template <>
-struct KeyType<double> {
-    using type = uint64_t;
-};
-
 // A bound of the fp32 error of a token's scores s, without the part that grows with
 // c.  Sigmoid: the exponential is off by 2 units, s (1 - s) 2^-22 <= 2^-24, a sum and a
 // quotient by half a unit each: below 2e-7.  Softmax: the exponential's argument is off
@@ -70,274 +61,6 @@ struct KeyType<double> {
 __device__ __forceinline__ float score_error(int32_t score, float largest) { return score == ROUTE_SOFTMAX ? 4e-6f * largest : 4e-7f; }
 // ... of c = s + bias.
 __device__ __forceinline__ float choice_error(float err, float c) { return err + 1.2e-7f * fabsf(c); }
-
-// Choose for one token.  l: this lane's logits (-inf past the last expert).
-// Slot j's expert lands in lane j's `id` (-1: none).  Returns false where fp32
-// cannot tell (T = float only).  V: experts a lane.
-template <int V, typename T>
-__device__ __forceinline__ bool choose(const RouteParams& p, const float (&l)[V], float top, int lane, int& id) {
-    using K = typename KeyType<T>::type;
-    constexpr bool EXACT = sizeof(T) == 8;
-    const bool by_logit = !p.bias;
-    K key[V];
-    bool sure = true;
-    float err = 0.0f;
-    if (!by_logit || p.groups > 1) {
-        T s[V];
-        if (p.score == ROUTE_SOFTMAX) {
-            T sum = 0;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                s[v] = l[v] > -INFINITY ? exp_t((T)l[v] - (T)top) : (T)0;
-                sum += s[v];
-            }
-            sum = warp_sum(sum);
-#pragma unroll
-            for (int v = 0; v < V; ++v) s[v] = s[v] / sum;
-            err = score_error(p.score, (float)((T)1 / sum));
-        } else {
-            err = score_error(p.score, 1.0f);
-#pragma unroll
-            for (int v = 0; v < V; ++v) s[v] = (T)1 / ((T)1 + exp_t(-(T)l[v]));
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = v * 32 + lane;
-            const float b = p.bias && e < p.experts ? p.bias[e] : 0.0f;
-            const T c = s[v] + (T)b;
-            key[v] = l[v] > -INFINITY && b > -INFINITY ? key_of(c) : (K)0;
-        }
-    }
-    if (p.groups > 1) {
-        // group g's score in lane g, as a key
-        const int size = p.experts / p.groups;
-        int group[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) group[v] = (v * 32 + lane) / size;
-        K mine = 0;
-        for (int g = 0; g < p.groups; ++g) {
-            K first = 0;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (group[v] == g && key[v] > first) first = key[v];
-            const K a = warp_max(first);
-            K score = a;
-            if (p.group_best > 1 && a) {
-                // without one expert that has it
-                const unsigned have = __ballot_sync(FULL, first == a);
-                const bool holder = (int)__ffs((int)have) - 1 == lane;
-                K second = 0;
-                bool skipped = !holder;
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    if (group[v] != g) continue;
-                    if (!skipped && key[v] == a)
-                        skipped = true;
-                    else if (key[v] > second)
-                        second = key[v];
-                }
-                const K b = warp_max(second);
-                if (b) score = key_of(number_of(a) + number_of(b));
-            }
-            if (lane == g) mine = score;
-        }
-        int better = 0;
-        for (int g = 0; g < p.groups; ++g) {
-            const K other = __shfl_sync(FULL, mine, g);
-            better += other > mine || (other == mine && g < lane);
-        }
-        const bool kept = lane < p.groups && better < p.group_topk;
-        const unsigned kept_mask = __ballot_sync(FULL, kept);
-        if constexpr (!EXACT) {
-            // the worst one kept against the best one left out
-            const uint32_t worst = __reduce_min_sync(FULL, kept ? (uint32_t)mine : 0xFFFFFFFFu);
-            const uint32_t best = __reduce_max_sync(FULL, !kept && lane < p.groups ? (uint32_t)mine : 0u);
-            if (best) {
-                const float w = number_of(worst), b = number_of(best);
-                if (w - b < 4.0f * choice_error(err, w)) sure = false;
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int g = group[v];
-            if (!(g < 32 && kept_mask >> g & 1)) key[v] = 0;
-            else if (by_logit) key[v] = key[v] ? key_of((T)l[v]) : (K)0;
-        }
-    } else if (by_logit) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = l[v] > -INFINITY ? key_of((T)l[v]) : (K)0;
-    }
-    id = -1;
-    K before = 0;
-    int before_id = -1;
-    const bool check = !EXACT && !by_logit;
-    for (int j = 0; j < p.topk + (check ? 1 : 0); ++j) {
-        K best = 0;
-        int at = 0x7FFFFFFF;
-#pragma unroll
-        for (int v = V - 1; v >= 0; --v)
-            if (key[v] >= best && key[v]) {
-                best = key[v];
-                at = v * 32 + lane;
-            }
-        const K m = warp_max(best);
-        if (!m) break;
-        const int e = (int)__reduce_min_sync(FULL, best == m ? (unsigned)at : 0x7FFFFFFFu);
-        if constexpr (!EXACT) {
-            if (check && before) {
-                const float x = number_of(before), y = number_of(m);
-                if (x - y < 2.0f * choice_error(err, fmaxf(fabsf(x), fabsf(y)))) {
-                    // equal logits with equal biases have equal scores in any arithmetic
-                    float la = 0.0f, lb = 0.0f;
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        if (v == before_id / 32) la = l[v];
-                        if (v == e / 32) lb = l[v];
-                    }
-                    la = __shfl_sync(FULL, la, before_id % 32);
-                    lb = __shfl_sync(FULL, lb, e % 32);
-                    if (la != lb || p.bias[before_id] != p.bias[e]) sure = false;
-                }
-            }
-        }
-        before = m;
-        before_id = e;
-        if (j < p.topk && lane == j) id = e;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (v * 32 + lane == e) key[v] = 0;
-    }
-    return sure;
-}
-
-// The same with keys of 22 bits above 1023 - expert: the keys differ, the largest
-// one names its expert, and of equal ones the lowest index comes first.  16-bit
-// logits lose nothing that way; else 2^-13 of a number are missing.
-template <int V>
-__device__ __forceinline__ bool choose_fast(const RouteParams& p, const float (&l)[V], float top, const float* bias, bool exact_keys,
-                                            int lane, int& id) {
-    constexpr float CUT = 1.3e-4f;
-    const bool by_logit = !p.bias;
-    uint32_t key[V];
-    bool sure = true;
-    float err = 0.0f;
-    auto packed = [&](float c, int v) { return (key_of(c) & ~1023u) | (uint32_t)(1023 - (v * 32 + lane)); };
-    auto number = [](uint32_t k) { return number_of(k & ~1023u); };
-    if (!by_logit || p.groups > 1) {
-        float s[V];
-        if (p.score == ROUTE_SOFTMAX) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                s[v] = l[v] > -INFINITY ? expf(l[v] - top) : 0.0f;
-                sum += s[v];
-            }
-            const float r = 1.0f / warp_sum(sum);
-#pragma unroll
-            for (int v = 0; v < V; ++v) s[v] *= r;
-            err = score_error(p.score, r);
-        } else {
-#pragma unroll
-            for (int v = 0; v < V; ++v) s[v] = 1.0f / (1.0f + expf(-l[v]));
-            err = score_error(p.score, 1.0f);
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float b = by_logit ? 0.0f : bias[v * 32 + lane];
-            key[v] = l[v] > -INFINITY && b > -INFINITY ? packed(s[v] + b, v) : 0u;
-        }
-    }
-    if (p.groups > 1) {
-        // group g's two largest keys in lane g
-        const int size = p.experts / p.groups;
-        const bool two = p.group_best > 1;
-        uint32_t m1 = 0, m2 = 0;
-        unsigned kept_mask;
-        auto merge = [&](uint32_t a, uint32_t b) {
-            m2 = m1 > a ? (m2 > a ? m2 : a) : (m1 > b ? m1 : b);
-            m1 = m1 > a ? m1 : a;
-        };
-        if (size % 32 == 0) {  // a group is all lanes of some registers
-            int g = 0, left = size;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const uint32_t a = warp_max(key[v]), b = two ? warp_max(key[v] == a ? 0u : key[v]) : 0u;
-                if (lane == g) merge(a, b);
-                if ((left -= 32) == 0) {
-                    left = size;
-                    ++g;
-                }
-            }
-        } else {
-            int group[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) group[v] = (v * 32 + lane) / size;
-            for (int g = 0; g < p.groups; ++g) {
-                uint32_t first = 0, second = 0;
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (group[v] == g) first = first > key[v] ? first : key[v];
-                const uint32_t a = warp_max(first);
-                if (two) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        if (group[v] == g && key[v] != a) second = second > key[v] ? second : key[v];
-                    second = warp_max(second);
-                }
-                if (lane == g) merge(a, second);
-            }
-        }
-        const float score = number(m1) + (two && m2 ? number(m2) : 0.0f);
-        const float spread = CUT * (fabsf(number(m1)) + (two && m2 ? fabsf(number(m2)) : 0.0f)) + 2.0f * choice_error(err, score);
-        const uint32_t mine = lane < p.groups && m1 ? key_of(score) : 0u;
-        int better = 0;
-        for (int g = 0; g < p.groups; ++g) {
-            const uint32_t other = __shfl_sync(FULL, mine, g);
-            better += other > mine || (other == mine && g < lane);
-        }
-        const bool kept = lane < p.groups && better < p.group_topk;
-        kept_mask = __ballot_sync(FULL, kept);
-        const uint32_t low = __reduce_min_sync(FULL, kept ? key_of(score - spread) : 0xFFFFFFFFu);
-        const uint32_t high = warp_max(!kept && mine ? key_of(score + spread) : 0u);
-        // (a NaN, of infinities, counts as a number here: then the next try decides)
-        if (__any_sync(FULL, lane < p.groups && m1 && !(fabsf(score) < INFINITY))) sure = false;
-        if (high && __any_sync(FULL, kept && mine) && !(low > high)) sure = false;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int g = size % 32 == 0 ? v * 32 / size : (v * 32 + lane) / size;
-            if (!(g < 32 && kept_mask >> g & 1)) key[v] = 0;
-            else if (by_logit && key[v]) key[v] = packed(l[v], v);
-        }
-    } else if (by_logit) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) key[v] = l[v] > -INFINITY ? packed(l[v], v) : 0u;
-    }
-    uint32_t best = 0, before = 0;
-    id = -1;
-    const int rounds = p.topk + (exact_keys ? 0 : 1);
-    for (int j = 0; j < rounds; ++j) {
-        // the largest key below the last one
-        best = 0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const uint32_t k = j == 0 || key[v] < before ? key[v] : 0u;
-            best = best > k ? best : k;
-        }
-        const uint32_t m = warp_max(best);
-        if (!m) break;
-        if (!exact_keys && j > 0) {
-            if (by_logit) {
-                sure &= (before >> 10) != (m >> 10);
-            } else {
-                const float x = number(before), y = number(m), most = fmaxf(fabsf(x), fabsf(y));
-                sure &= x - y > CUT * most + 2.0f * choice_error(err, most);
-            }
-        }
-        before = m;
-        if (lane == j && j < p.topk) id = 1023 - (int)(m & 1023u);
-    }
-    return sure;
-}
 
 template <int V>
 __device__ __forceinline__ void load_logits(const RouteParams& p, int t, int lane, float (&l)[V]) {
@@ -354,21 +77,277 @@ __device__ __forceinline__ void load_logits(const RouteParams& p, int t, int lan
         load([&](int64_t i) { return __half2float(static_cast<const __half*>(p.L)[i]); });
 }
 
-// The second and the third try.  (The logits are read again: an array handed to a
-// function would live in memory.)
-template <int V, typename T>
-__device__ __noinline__ int choose_again(const RouteParams& p, int t, float top, int lane, bool& sure) {
+// A score in fp32 or in 64 bits.  total: softmax's sum.
+template <typename T>
+__device__ __forceinline__ T score_of(int32_t kind, float l, float top, T total) {
+    return kind == ROUTE_SOFTMAX ? exp_t((T)l - (T)top) / total : (T)1 / ((T)1 + exp_t(-(T)l));
+}
+
+// Groups kept, as a mask, by keys of all choice scores.  sure: fp32's error leaves
+// no doubt (err: that of one score; 0 for keys in 64 bits).
+template <int V, typename K>
+__device__ __forceinline__ unsigned keep_groups(const RouteParams& p, const K (&key)[V], float err, int lane, bool& sure) {
+    const int size = p.experts / p.groups;
+    const bool two = p.group_best > 1;
+    K m1 = 0, m2 = 0;  // group g's two largest keys, in lane g
+    auto merge = [&](K a, K b) {
+        m2 = m1 > a ? (m2 > a ? m2 : a) : (m1 > b ? m1 : b);
+        m1 = m1 > a ? m1 : a;
+    };
+    if (size % 32 == 0) {  // a group is all lanes of some registers
+        int g = 0, left = size;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const K a = warp_max(key[v]);
+            K b = 0;
+            if (two) {
+                const unsigned have = __ballot_sync(FULL, key[v] == a);
+                b = __popc(have) > 1 ? a : warp_max(key[v] == a ? (K)0 : key[v]);
+            }
+            if (lane == g) merge(a, b);
+            if ((left -= 32) == 0) {
+                left = size;
+                ++g;
+            }
+        }
+    } else {
+        int group[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) group[v] = (v * 32 + lane) / size;
+        for (int g = 0; g < p.groups; ++g) {
+            K first = 0, second = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (group[v] == g) {
+                    second = key[v] > first ? first : (key[v] > second ? key[v] : second);
+                    first = key[v] > first ? key[v] : first;
+                }
+            const K a = warp_max(first);
+            K b = 0;
+            if (two) {
+                const unsigned have = __ballot_sync(FULL, first == a);
+                b = __popc(have) > 1 ? a : warp_max(first == a ? second : first);
+            }
+            if (lane == g) merge(a, b);
+        }
+    }
+    const auto score = two && m2 ? number_of(m1) + number_of(m2) : number_of(m1);
+    const K mine = lane < p.groups && m1 ? key_of(score) : (K)0;
+    int better = 0;
+    for (int g = 0; g < p.groups; ++g) {
+        const K other = __shfl_sync(FULL, mine, g);
+        better += other > mine || (other == mine && g < lane);
+    }
+    const bool kept = lane < p.groups && better < p.group_topk;
+    const K high = warp_max(!kept ? mine : (K)0);
+    if (err > 0.0f && high) {
+        // (all groups kept are live here) the best one left out against each one kept
+        const float x = (float)score, y = (float)number_of(high);
+        const float far = fmaxf(fabsf(x), fabsf(y));
+        if (__any_sync(FULL, kept && !(x - y > 2.0f * (2.0f * err + 2.4e-7f * far)))) sure = false;
+    }
+    return __ballot_sync(FULL, kept);
+}
+
+// The choice from 64-bit scores of all experts: slot j's expert in lane j.
+template <int V>
+__device__ __noinline__ int choose_exactly(const RouteParams& p, int t, float top, int lane) {
     float l[V];
+    uint64_t key[V];
     load_logits<V>(p, t, lane, l);
-    int id;
-    sure = choose<V, T>(p, l, top, lane, id);
+    double total = 0.0;
+    if (p.score == ROUTE_SOFTMAX) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (l[v] > -INFINITY) total += exp((double)l[v] - (double)top);
+        total = warp_sum(total);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const float b = p.bias && v * 32 + lane < p.experts ? p.bias[v * 32 + lane] : 0.0f;
+        key[v] = l[v] > -INFINITY && b > -INFINITY ? key_of(score_of<double>(p.score, l[v], top, total) + (double)b) : 0ull;
+    }
+    if (p.groups > 1) {
+        bool sure = true;
+        const unsigned kept = keep_groups<V>(p, key, 0.0f, lane, sure);
+        const int size = p.experts / p.groups;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int g = (v * 32 + lane) / size;
+            if (!(g < 32 && kept >> g & 1)) key[v] = 0;
+        }
+    }
+    if (!p.bias) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = key[v] ? (uint64_t)key_of(l[v]) : 0ull;
+    }
+    int id = -1;
+    for (int j = 0; j < p.topk; ++j) {
+        uint64_t best = 0;
+        int at = 0x7FFFFFFF;
+#pragma unroll
+        for (int v = V - 1; v >= 0; --v)
+            if (key[v] >= best && key[v]) {
+                best = key[v];
+                at = v * 32 + lane;
+            }
+        const uint64_t m = warp_max(best);
+        if (!m) break;
+        const int e = (int)__reduce_min_sync(FULL, best == m ? (unsigned)at : 0x7FFFFFFFu);
+        if (lane == j) id = e;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (v * 32 + lane == e) key[v] = 0;
+    }
     return id;
 }
+
+// Lane j < n has candidate `id` and its key: puts them into order, ties to the lowest
+// index.
+template <typename K>
+__device__ __forceinline__ void sort_candidates(int n, int lane, int& id, K& key, float& l, float& b) {
+    int rank = 0;
+    for (int i = 0; i < n; ++i) {
+        const K other = __shfl_sync(FULL, key, i);
+        const int e = __shfl_sync(FULL, id, i);
+        rank += other > key || (other == key && e < id);
+    }
+    int from = lane;
+    for (int i = 0; i < n; ++i)
+        if (__shfl_sync(FULL, rank, i) == lane) from = i;
+    id = __shfl_sync(FULL, id, from);
+    key = __shfl_sync(FULL, key, from);
+    l = __shfl_sync(FULL, l, from);
+    b = __shfl_sync(FULL, b, from);
+}
+
+// The order of n <= 32 candidates, among which the topk are.  Slot j's expert in
+// lane j.
 template <int V>
-__device__ __forceinline__ int choose_carefully(const RouteParams& p, int t, float top, int lane) {
-    bool sure;
-    const int id = choose_again<V, float>(p, t, top, lane, sure);
-    return sure ? id : choose_again<V, double>(p, t, top, lane, sure);
+__device__ __noinline__ int choose_among(const RouteParams& p, int t, float top, float total, float err, int n, int id, int lane) {
+    const bool mine = lane < n;
+    float l = mine ? ld_elem(p.L, p.type, t * p.ld + id) : 0.0f;
+    float b = mine && p.bias ? p.bias[id] : 0.0f;
+    const float c = p.bias ? score_of<float>(p.score, l, top, total) + b : l;
+    uint32_t key = mine ? key_of(c) : 0u;
+    sort_candidates(n, lane, id, key, l, b);
+    bool doubt = false;
+    if (p.bias) {
+        // against the next one: equal logits with equal biases have equal scores in any
+        // arithmetic
+        const float x = number_of(key), y = number_of(__shfl_down_sync(FULL, key, 1));
+        // (all lanes take part in both exchanges)
+        const float next_l = __shfl_down_sync(FULL, l, 1), next_b = __shfl_down_sync(FULL, b, 1);
+        const bool same = l == next_l && b == next_b;
+        doubt = lane < p.topk && lane + 1 < n && !same && !(x - y > 2.0f * choice_error(err, fmaxf(fabsf(x), fabsf(y))));
+    }
+    if (__any_sync(FULL, doubt)) {
+        double sum = 0.0;
+        if (p.score == ROUTE_SOFTMAX) {
+            float all[V];
+            load_logits<V>(p, t, lane, all);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (all[v] > -INFINITY) sum += exp((double)all[v] - (double)top);
+            sum = warp_sum(sum);
+        }
+        uint64_t exact = lane < n ? key_of(score_of<double>(p.score, l, top, sum) + (double)b) : 0ull;
+        sort_candidates(n, lane, id, exact, l, b);
+    }
+    return lane < p.topk && lane < n ? id : -1;
+}
+
+// Choose for one token.  l: this lane's logits (-inf past the last expert).  Slot
+// j's expert in lane j (-1: none).  V: experts a lane.
+//
+// Keys of 22 bits lie above 1023 - expert: all differ, and of equal ones the lowest
+// index comes first.  16-bit logits lose nothing that way; else 2^-13 of a number
+// are missing.
+template <int V>
+__device__ __forceinline__ int choose(const RouteParams& p, int t, const float (&l)[V], float top, const float* bias, bool exact_keys, int lane) {
+    constexpr float CUT = 1.3e-4f;
+    const bool by_logit = !p.bias;
+    uint32_t key[V];
+    float err = 0.0f, total = 1.0f;
+    if (!by_logit || p.groups > 1) {
+        float s[V];
+        if (p.score == ROUTE_SOFTMAX) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                s[v] = l[v] > -INFINITY ? expf(l[v] - top) : 0.0f;
+                sum += s[v];
+            }
+            total = warp_sum(sum);
+            const float r = 1.0f / total;
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] *= r;
+            err = score_error(p.score, r);
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) s[v] = 1.0f / (1.0f + expf(-l[v]));
+            err = score_error(p.score, 1.0f);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float b = by_logit ? 0.0f : bias[v * 32 + lane];
+            key[v] = l[v] > -INFINITY && b > -INFINITY ? key_of(s[v] + b) : 0u;
+        }
+    }
+    if (p.groups > 1) {
+        bool sure = true;
+        const unsigned kept = keep_groups<V>(p, key, err, lane, sure);
+        if (!sure) return choose_exactly<V>(p, t, top, lane);
+        const int size = p.experts / p.groups;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int g = size % 32 == 0 ? v * 32 / size : (v * 32 + lane) / size;
+            if (!(g < 32 && kept >> g & 1)) key[v] = 0;
+            else if (by_logit && key[v]) key[v] = key_of(l[v]);
+        }
+    } else if (by_logit) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) key[v] = l[v] > -INFINITY ? key_of(l[v]) : 0u;
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = key[v] ? (key[v] & ~1023u) | (uint32_t)(1023 - (v * 32 + lane)) : 0u;
+    int id = -1, n = 0;
+    uint32_t before = 0xFFFFFFFFu, last = 0;  // last: the key of slot topk - 1
+    bool doubt = false;
+    for (int round = 0; round <= 32; ++round) {  // (ends before: n goes up)
+        // the largest key below the one before
+        uint32_t best = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const uint32_t k = key[v] < before ? key[v] : 0u;
+            best = best > k ? best : k;
+        }
+        const uint32_t m = warp_max(best);
+        if (!m) break;
+        if (!exact_keys && n > 0) {
+            // whether the order of two neighbours (beyond topk: of slot topk - 1 and this
+            // one) is certain
+            const uint32_t a = n <= p.topk ? before : last;
+            bool certain;
+            if (by_logit) {
+                certain = a >> 10 != m >> 10;
+            } else {
+                const float x = number_of(a & ~1023u), y = number_of(m & ~1023u), most = fmaxf(fabsf(x), fabsf(y));
+                certain = x - y > CUT * most + 2.0f * choice_error(err, most);
+            }
+            if (n >= p.topk && certain) break;
+            doubt |= !certain;
+        }
+        if (n == 32) return choose_exactly<V>(p, t, top, lane);
+        if (lane == n) id = 1023 - (int)(m & 1023u);
+        before = m;
+        if (++n == p.topk) {
+            last = m;
+            if (exact_keys) break;
+        }
+    }
+    if (doubt) return choose_among<V>(p, t, top, total, err, n, id, lane);
+    return lane < p.topk ? id : -1;
 }
 
 // Where the experts' rows start: exclusive sums of `count` (block-wide; threads
@@ -400,19 +379,30 @@ __device__ __forceinline__ void exclusive_sums(const int32_t* count, int32_t* st
     __syncthreads();
 }
 
-// One warp: the rows of entries [first, last), in order; next[e]: expert e's next row.
-__device__ __forceinline__ void place(const int32_t* ids, int32_t* rows, int64_t first, int64_t last, volatile int32_t* next,
-                                      int lane) {
-    for (int64_t i0 = first; i0 < last; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int32_t e = i < last ? ids[i] : -1;
-        const unsigned same = __match_any_sync(FULL, e);
-        const int rank = __popc(same & ((1u << lane) - 1u));
+// One warp: the rows of n entries, in order; next[e]: expert e's next row; mask: a
+// zero per expert.  near: the first `staged` entries, in shared memory.
+__device__ __forceinline__ void place(const int32_t* ids, const int32_t* near, int staged, int32_t* rows, int n, volatile int32_t* next,
+                                      volatile uint32_t* mask, int lane) {
+    auto entry = [&](int i) { return i >= n ? -1 : i < staged ? near[i] : ids[i]; };
+    int32_t e = entry(lane);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        const int32_t after = entry(i + 32);  // on its way during this round
+        // the lanes that have the same expert (an instruction that finds them takes ten
+        // times as long)
+        if (e >= 0) atomicOr(const_cast<uint32_t*>(&mask[e]), 1u << lane);
+        __syncwarp();
+        const uint32_t same = e >= 0 ? mask[e] : 0u;
         const int32_t at = e >= 0 ? next[e] : 0;
+        const int rank = __popc(same & ((1u << lane) - 1u));
         __syncwarp();
-        if (e >= 0 && rank == 0) next[e] = at + __popc(same);
+        if (e >= 0 && rank == 0) {
+            next[e] = at + __popc(same);
+            mask[e] = 0;
+        }
         __syncwarp();
-        if (i < last) rows[i] = e >= 0 ? at + rank : -1;
+        if (i < n) rows[i] = e >= 0 ? at + rank : -1;
+        e = after;
     }
 }
 
@@ -420,7 +410,7 @@ __device__ __forceinline__ void place(const int32_t* ids, int32_t* rows, int64_t
 // entries by expert.  A single block then finishes the rows itself; several leave
 // their counts to route_place_kernel.
 template <int V>
-__global__ void __launch_bounds__(32 * ROUTE_WARPS) route_kernel(const __grid_constant__ RouteParams p) {
+__global__ void __launch_bounds__(V <= 8 ? 1024 : 512) route_kernel(const __grid_constant__ RouteParams p) {
     __shared__ int32_t count[MOE_MAX_EXPERTS], start[MOE_MAX_EXPERTS + 1], carry[32];
     __shared__ float bias[32 * V];
     griddep_launch_dependents();
@@ -453,15 +443,10 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_kernel(const __grid_co
         int id = -1;
         float w = __uint_as_float(0x7FC00000u);
         if (!bad) {
-            if (!choose_fast<V>(p, l, top, bias, exact_keys, lane, id)) id = choose_carefully<V>(p, t, top, lane);
+            id = choose<V>(p, t, l, top, bias, exact_keys, lane);
             // weights: lane j has slot j
             const bool have = id >= 0;
-            float x = -INFINITY;
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float u = __shfl_sync(FULL, l[v], id & 31);
-                if (have && v == id / 32) x = u;
-            }
+            const float x = have ? ld_elem(p.L, p.type, t * p.ld + id) : -INFINITY;
             w = 0.0f;
             if (p.renormalize) {
                 // relative to the largest chosen logit, so that nothing under- or overflows
@@ -495,62 +480,93 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_kernel(const __grid_co
     if (!p.offsets) return;
     __syncthreads();
     if (p.blocks > 1) {
-        for (int e = threadIdx.x; e < p.experts; e += blockDim.x) p.counts[(int64_t)blockIdx.x * p.experts + e] = count[e];
+        for (int e = threadIdx.x; e < p.pitch; e += blockDim.x) p.counts[(int64_t)blockIdx.x * p.pitch + e] = e < p.experts ? (uint16_t)count[e] : (uint16_t)0;
         return;
     }
     exclusive_sums(count, start, p.experts, carry);
     for (int e = threadIdx.x; e <= p.experts; e += blockDim.x) p.offsets[e] = start[e];
+    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) count[e] = 0;
     __syncthreads();
-    if (warp == 0) place(p.ids, p.rows, 0, (int64_t)p.tokens * p.topk, start, lane);
+    if (warp == 0) place(p.ids, nullptr, 0, p.rows, p.tokens * p.topk, start, reinterpret_cast<uint32_t*>(count), lane);
 }
 
 // Block b's rows: expert e's start plus what the blocks before it hold of e, then
 // one by one.  Every block adds up all counts (integers, so in any order).
-__global__ void __launch_bounds__(512) route_place_kernel(const __grid_constant__ RouteParams p) {
-    __shared__ int32_t count[MOE_MAX_EXPERTS], before[MOE_MAX_EXPERTS], start[MOE_MAX_EXPERTS + 1], carry[32];
+constexpr int PLACE_THREADS = 512;
+__global__ void __launch_bounds__(PLACE_THREADS) route_place_kernel(const __grid_constant__ RouteParams p) {
+    // sums of a thread's share of the blocks, eight experts each: of all, and of those
+    // before this one
+    __shared__ __align__(16) int32_t share[2][PLACE_THREADS * 8];
+    __shared__ int32_t count[MOE_MAX_EXPERTS], start[MOE_MAX_EXPERTS + 1], carry[32], near[PLACE_THREADS];
     griddep_launch_dependents();
-    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) count[e] = before[e] = 0;
-    __syncthreads();
+    const int tid = (int)threadIdx.x;
+    const int octets = p.pitch / 8, parts = PLACE_THREADS / octets, part = tid / octets, o = tid % octets;
+    const int64_t t0 = (int64_t)blockIdx.x * p.tokens_per_block;
+    const int64_t t1 = p.tokens - t0 < p.tokens_per_block ? p.tokens : t0 + p.tokens_per_block;
+    const int n = (int)(t1 - t0) * p.topk;
+    const int32_t* ids = p.ids + t0 * p.topk;
     griddep_wait();
-    // a thread has one expert and every `parts`-th block
-    const int threads = (int)blockDim.x;
-    for (int e0 = 0; e0 < p.experts; e0 += threads) {
-        const int here = p.experts - e0 < threads ? p.experts - e0 : threads, parts = threads / here;
-        const int e = e0 + (int)threadIdx.x % here, part = (int)threadIdx.x / here;
-        int32_t all = 0, below = 0;
-        if (part < parts) {
+    const int32_t first = tid < n ? ids[tid] : -1;
+    int32_t all[8] = {}, below[8] = {};
+    if (part < parts) {
 #pragma unroll 8
-            for (int b = part; b < p.blocks; b += parts) {
-                const int32_t c = p.counts[(int64_t)b * p.experts + e];
-                all += c;
-                below += b < (int)blockIdx.x ? c : 0;
+        for (int b = part; b < p.blocks; b += parts) {
+            const uint4 c = reinterpret_cast<const uint4*>(p.counts + (int64_t)b * p.pitch)[o];
+            const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+            const bool earlier = b < (int)blockIdx.x;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int32_t x = (int32_t)(w[i / 2] >> (16 * (i & 1)) & 0xFFFFu);
+                all[i] += x;
+                below[i] += earlier ? x : 0;
             }
-            atomicAdd(&count[e], all);
-            atomicAdd(&before[e], below);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        *reinterpret_cast<int4*>(&share[0][tid * 8 + i]) = make_int4(all[i], all[i + 1], all[i + 2], all[i + 3]);
+        *reinterpret_cast<int4*>(&share[1][tid * 8 + i]) = make_int4(below[i], below[i + 1], below[i + 2], below[i + 3]);
+    }
+    near[tid] = first;
+    __syncthreads();
+    int32_t before[2] = {0, 0};  // of experts tid and tid + 512
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int e = tid + k * PLACE_THREADS;
+        if (e < p.experts) {
+            int32_t sum = 0;
+            for (int q = 0; q < parts; ++q) {
+                sum += share[0][q * p.pitch + e];
+                before[k] += share[1][q * p.pitch + e];
+            }
+            count[e] = sum;
         }
     }
     __syncthreads();
     exclusive_sums(count, start, p.experts, carry);
     if (blockIdx.x == 0)
-        for (int e = threadIdx.x; e <= p.experts; e += blockDim.x) p.offsets[e] = start[e];
+        for (int e = tid; e <= p.experts; e += PLACE_THREADS) p.offsets[e] = start[e];
     __syncthreads();
-    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) start[e] += before[e];
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const int64_t t0 = (int64_t)blockIdx.x * p.tokens_per_block;
-        const int64_t t1 = p.tokens - t0 < p.tokens_per_block ? p.tokens : t0 + p.tokens_per_block;
-        place(p.ids, p.rows, t0 * p.topk, t1 * p.topk, start, (int)threadIdx.x);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int e = tid + k * PLACE_THREADS;
+        if (e < p.experts) {
+            start[e] += before[k];
+            count[e] = 0;
+        }
     }
+    __syncthreads();
+    if (tid < 32) place(ids, near, PLACE_THREADS, p.rows + t0 * p.topk, n, start, reinterpret_cast<uint32_t*>(count), tid);
 }
 
 }  // namespace
 
 cudaError_t launch_route(const RouteParams& p, cudaStream_t st) {
     const int per = (p.experts + 31) / 32;
-    auto go = [&](auto kernel) { return launch_pdl(kernel, p.blocks, 32 * ROUTE_WARPS, 0, st, p); };
+    auto go = [&](auto kernel) { return launch_pdl(kernel, p.blocks, p.blocks == 1 ? 512 : route_threads(p.experts), 0, st, p); };
     cudaError_t e = per <= 1 ? go(route_kernel<1>) : per <= 2 ? go(route_kernel<2>) : per <= 4 ? go(route_kernel<4>) : per <= 8 ? go(route_kernel<8>) : per <= 16 ? go(route_kernel<16>) : go(route_kernel<32>);
     if (e != cudaSuccess || !p.offsets || p.blocks == 1) return e;
-    return launch_pdl(route_place_kernel, p.blocks, 512, 0, st, p);
+    return launch_pdl(route_place_kernel, p.blocks, PLACE_THREADS, 0, st, p);
 }
 
 }  // namespace qg
