@@ -8,6 +8,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "api_checks.h"
 #include "mx_gemm.h"
@@ -109,7 +110,7 @@ int64_t token_tiles(const S8GemmParams& p, int64_t rows) {
     return std::min(p.epi.M / rows + p.num_experts, p.epi.M);
 }
 
-enum S8Kernel { S8_GEMV, S8_TILE };
+enum S8Kernel { S8_GEMV, S8_TILE, S8_PAIR };
 struct S8Choice {
     S8Kernel kernel;
     int width;   // S8_TILE: 32 or 128 tokens a tile at most
@@ -120,20 +121,39 @@ struct S8Choice {
 // Rows an expert has on average, or all.
 int64_t rows_each(const S8GemmParams& p) { return p.num_experts ? ceil_div(p.epi.M, p.num_experts) : p.epi.M; }
 
-// GEMM_FORCE_KERNEL=s8_gemv / s8_t32 / s8_t128 (the names gemm_last_choice prints,
+// Clusters of two that the CTA-pair kernel keeps resident (asked once per device).
+int pair_clusters(gemm_handle_t h) {
+    static std::atomic<int> known[64];
+    std::atomic<int>& k = known[handle_device(h) & 63];
+    int n = k.load();
+    if (n == 0) {
+        n = std::max(0, std::min(s8_pair_max_clusters(), handle_sm_count(h) / 2)) + 1;
+        k.store(n);
+    }
+    return n - 1;
+}
+
+// GEMM_FORCE_KERNEL=s8_gemv / s8_t32 / s8_t128 / s8_pair (the names gemm_last_choice prints,
 // up to the slash) pins the kernel, for tests and sweeps.
 bool forced_kernel(S8Choice* c) {
     const char* f = getenv("GEMM_FORCE_KERNEL");
     if (!f || strncmp(f, "s8_", 3)) return false;
     if (!strncmp(f, "s8_gemv", 7)) c->kernel = S8_GEMV;
+    else if (!strncmp(f, "s8_pair", 7)) c->kernel = S8_PAIR;
     else c->kernel = S8_TILE, c->width = strncmp(f, "s8_t32", 6) == 0 ? 32 : 128;
     return true;
 }
 
-S8Choice choose(const S8GemmParams& p, int sm_count, int forced_split) {
+S8Choice choose(const S8GemmParams& p, int sm_count, int clusters, int forced_split) {
     const int64_t each = rows_each(p);
     S8Choice c{each <= 4 ? S8_GEMV : S8_TILE, each <= 32 ? 32 : 128, 0, 1};
+    if (each > 256 && !forced_split && clusters > 0) c.kernel = S8_PAIR;
     forced_kernel(&c);
+    if (c.kernel == S8_PAIR && clusters < 1) c.kernel = S8_TILE;
+    if (c.kernel == S8_PAIR) {
+        c.rows = (int)std::min<int64_t>(S8_PAIR_TOKENS, ceil_div(each, 32) * 32);
+        return c;
+    }
     if (c.kernel == S8_GEMV) {
         c.rows = each <= 1 ? 1 : each <= 2 ? 2 : each <= 4 ? 4 : 8;
         return c;
@@ -165,7 +185,8 @@ int run_product(gemm_handle_t h, const gemm_op_t* op, S8GemmParams& p, cudaStrea
         handle_set_choice(h, "scale_c", M, N, p.K);
         return status_of(launch_mx_no_k(p.epi, p.offsets, p.num_experts, st));
     }
-    const S8Choice c = choose(p, handle_sm_count(h), op->splitk);
+    const int clusters = pair_clusters(h);
+    const S8Choice c = choose(p, handle_sm_count(h), clusters, op->splitk);
     const char* grouped = p.num_experts ? "_grouped" : "";
     char name[64];
     p.tile_rows = c.rows;
@@ -178,7 +199,8 @@ int run_product(gemm_handle_t h, const gemm_op_t* op, S8GemmParams& p, cudaStrea
         handle_set_choice(h, name, M, N, p.K);
         return status_of(launch_s8_gemv(p, handle_sm_count(h), st));
     }
-    const int64_t tn = ceil_div(N, 128);
+    const bool pair = c.kernel == S8_PAIR;
+    const int64_t tn = ceil_div(N, pair ? 256 : 128);
     if (tm * tn * c.splits > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
     p.tiles_m = (int32_t)tm;
     p.tiles_n = (int32_t)tn;
@@ -193,9 +215,15 @@ int run_product(gemm_handle_t h, const gemm_op_t* op, S8GemmParams& p, cudaStrea
     p.timeout_ns = handle_timeout_ns(h);
     S8Maps m;
     memset(&m, 0, sizeof m);
-    int rc = map_s8(h, &m.a, p.A, p.K, M, p.lda, 1, 0, c.rows);
+    int rc = map_s8(h, &m.a, p.A, p.K, M, p.lda, 1, 0, pair ? S8_PAIR_TOKENS / 2 : c.rows);
     if (rc == GEMM_OK) rc = map_s8(h, &m.b, p.B, p.K, N, p.ldb, p.num_experts > 1 ? p.num_experts : 1, p.b_bs, 128);
     if (rc != GEMM_OK) return rc;
+    if (pair) {
+        p.programs = (int32_t)std::min<int64_t>(clusters, tm * tn);
+        snprintf(name, sizeof name, "s8%s_pair/rows%d", grouped, c.rows);
+        handle_set_choice(h, name, M, N, p.K);
+        return status_of(launch_s8_pair(m, p, p.programs, st));
+    }
     snprintf(name, sizeof name, "s8%s_t%d/%s%d", grouped, c.width, c.splits > 1 ? "splitk" : "rows", c.splits > 1 ? c.splits : c.rows);
     handle_set_choice(h, name, M, N, p.K);
     return status_of(launch_s8_gemm(c.width, m, p, (int)(tm * tn * c.splits), st));

@@ -1,0 +1,412 @@
+// Int8 product on CTA pairs: persistent clusters of two, one tile of 256 channels x
+// up to 192 tokens at a time (tcgen05.mma.cta_group::2).
+//
+// Each CTA takes in its 128 channels and its half of the tile's tokens, and turns
+// both into f16: the channels' codes into its TMEM, the tokens' into its shared
+// memory, in slots of 64 of K.  Two groups of four warps take a stage's two halves.
+// The accumulator has two buffers; every 16 slots (1024 products) eight warps add the
+// full one to 32-bit sums in registers, 96 of them a thread, and after the tile's
+// last finish and store them, while the MMAs go on in the other buffer.
+//
+//   warps 0-3    TMA producer, (leader) MMAs, two without work
+//   warps 4-11   sums and epilogue: a 32-lane quarter and half of the columns each
+//   warps 12-19  f16 operands
+#include <atomic>
+
+#include "mx_rows.h"
+#include "s8_tile.cuh"
+
+namespace qg {
+
+namespace {
+
+constexpr int THREADS = 640;
+constexpr int TN = S8_PAIR_TOKENS, HALF = TN / 2;
+constexpr int S = 4;   // raw stages: 128 of K
+constexpr int NS = 4;  // f16 slots: 64 of K
+constexpr uint32_t W_BYTES = 128 * 128, X_BYTES = HALF * 128, STAGE_BYTES = W_BYTES + X_BYTES;
+constexpr uint32_t SLOT_BYTES = HALF * 128;
+constexpr uint32_t RING_BYTES = S * STAGE_BYTES + NS * SLOT_BYTES;
+constexpr uint32_t AUX_BYTES = (2 * S + 2 * NS + 5) * 8 + 16;
+constexpr uint32_t SMEM_BYTES = 1024 + RING_BYTES + AUX_BYTES;
+constexpr int SLOT_CHUNK = 2 * S8_CHUNK;  // slots whose sums fp32 holds exactly
+static_assert(2 * TN + 32 * NS <= 512 && SMEM_BYTES <= 232448 && STAGE_BYTES % 1024 == 0 && SLOT_BYTES % 1024 == 0, "");
+
+// Registers of a thread: 640 threads are launched with 96.
+constexpr int REGS_LAUNCH = 96, REGS_SUMS = 128, REGS_OPERANDS = 80, REGS_REST = 64;
+static_assert(256 * REGS_SUMS + 256 * REGS_OPERANDS + 128 * REGS_REST <= THREADS * REGS_LAUNCH, "what was launched is shared out");
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+struct Tile {
+    int64_t n0, row0;
+    int expert, rows, tn;  // rows that exist; the MMA's columns: a multiple of 32
+};
+
+// Tile t of the launch (warp-wide): token blocks vary fastest.  False past the end.
+__device__ __forceinline__ bool pair_tile(const S8GemmParams& P, int64_t blocks, int64_t t, int lane, Tile& o) {
+    if (t >= blocks * P.tiles_n) return false;
+    const int64_t b = t % blocks;
+    o.n0 = t / blocks * 256;
+    o.expert = 0;
+    if (P.offsets) {
+        int64_t atom_row;
+        if (!mx_expert_block(P.offsets, P.num_experts, P.epi.M, P.tile_rows, b, lane, &o.expert, &o.row0, &o.rows, &atom_row)) return false;
+    } else {
+        o.row0 = b * P.tile_rows;
+        o.rows = (int)(P.epi.M - o.row0 < P.tile_rows ? P.epi.M - o.row0 : P.tile_rows);
+    }
+    o.tn = o.rows > 32 ? (o.rows + 31) / 32 * 32 : 32;
+    return true;
+}
+
+__device__ __forceinline__ int64_t expert_blocks(const S8GemmParams& P, int lane) {
+    int32_t n = 0;
+    for (int32_t e = lane; e < P.num_experts; e += 32) n = mx_add_blocks(n, P.offsets[e], P.offsets[e + 1], P.tile_rows, P.tiles_m);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
+    return n < P.tiles_m ? n : P.tiles_m;
+}
+
+// Half of a stage (64 codes of 128 channels) to 32 TMEM columns.
+__device__ __forceinline__ void weights_half(const uint8_t* raw, int half, uint32_t taddr, int row) {
+    const uint8_t* base = raw + row * 128;
+    const int x = row & 7;
+    uint32_t r[32];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) s8_to_f16(*reinterpret_cast<const uint4*>(base + (((4 * half + c) ^ x) << 4)), r + 8 * c);
+    tmem_st_32x32b(taddr, r);
+}
+// Half of a stage (64 codes of `rows` tokens, a multiple of 16) to an f16 tile.
+__device__ __forceinline__ void tokens_half(const uint8_t* raw, int half, uint8_t* out, int rows, int thread) {
+    const int r8 = thread & 7;
+    for (int i = thread >> 3; i < rows / 2; i += 16) {  // four chunks of rows / 8 octets
+        const int c = i & 3, row = (i >> 2) * 8 + r8;
+        uint32_t h[8];
+        s8_to_f16(*reinterpret_cast<const uint4*>(raw + row * 128 + (((4 * half + c) ^ r8) << 4)), h);
+        uint8_t* to = out + row * 128;
+        *reinterpret_cast<uint4*>(to + (((2 * c) ^ r8) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(to + (((2 * c + 1) ^ r8) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+    }
+}
+
+// Eight tokens m0 .. of this lane's channel n.
+template <int ACT, int DT>
+__device__ __forceinline__ void store8(const S8GemmParams& P, const EpiArith& ar, const int32_t* sum, int64_t m0, int rows, int64_t n, bool in,
+                                        float channel, float bias, float tokens, int first) {
+    const EpiParams& e = P.epi;
+    float c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = ar.beta != 0.0f && in && i < rows ? ld_elem(e.C, DT, (m0 + i) * e.ldc + n) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float t0 = __shfl_sync(0xFFFFFFFFu, tokens, first + i), t1 = __shfl_sync(0xFFFFFFFFu, tokens, first + i + 1);
+        float x0, x1;
+        mx_value2<ACT, DT>(ar, s8_scaled(sum[i], t0, channel), s8_scaled(sum[i + 1], t1, channel), c[i], c[i + 1], bias, bias, x0, x1);
+        if (in && i < rows) st_elem(e.D, DT, (m0 + i) * e.ldd + n, x0);
+        if (in && i + 1 < rows) st_elem(e.D, DT, (m0 + i + 1) * e.ldd + n, x1);
+    }
+}
+__device__ __forceinline__ void store8_any(const S8GemmParams& P, const EpiArith& ar, const int32_t* sum, int64_t m0, int rows, int64_t n, bool in,
+                                            float channel, float bias, float tokens, int first) {
+    with_epi_act(P.epi, [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        if (P.epi.d_type == DT_BF16)
+            store8<ACT, DT_BF16>(P, ar, sum, m0, rows, n, in, channel, bias, tokens, first);
+        else if (P.epi.d_type == DT_F16)
+            store8<ACT, DT_F16>(P, ar, sum, m0, rows, n, in, channel, bias, tokens, first);
+        else
+            store8<ACT, DT_F32>(P, ar, sum, m0, rows, n, in, channel, bias, tokens, first);
+    });
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
+    s8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ S8GemmParams P) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* slots = smem + S * STAGE_BYTES;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING_BYTES);
+    uint64_t* empty = full + S;        // a stage's codes have been read (8 warps)
+    uint64_t* ready = empty + S;       // leader: both CTAs' operands are in the slot (8 warps)
+    uint64_t* slot_free = ready + NS;
+    uint64_t* tfull = slot_free + NS;
+    uint64_t* tempty = tfull + 2;      // leader: a buffer is in both CTAs' sums (16 warps)
+    uint64_t* done = tempty + 2;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 8);
+        }
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&ready[s], 8);
+            mbar_init(&slot_free[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], 16);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers exist before any cross-CTA arrive
+    tc_fence_after_sync();
+    const uint32_t tmem = *tmem_slot, tmem_w = tmem + 2 * TN;
+    griddep_launch_dependents();
+    griddep_wait();
+    const Guard g{P.status, P.timeout_ns, abort_flag};
+    const int64_t pid = blockIdx.x >> 1;
+    const int64_t blocks = P.offsets ? expert_blocks(P, lane) : P.tiles_m;
+    const int nslots = 2 * P.k_steps;  // of a tile
+
+    if (warp < 4) {
+        regs_down<REGS_REST>();
+        if (warp == 0) {
+            // ---------------- TMA producer (both CTAs) ----------------
+            int s = 0;
+            uint32_t ph = 0, armed = 0, armed_par = 0;
+            bool ok = true;
+            Tile t;
+            for (int64_t i = pid; ok && pair_tile(P, blocks, i, lane, t); i += P.programs) {
+                const int32_t w0 = (int32_t)(t.n0 + 128 * rank), x0 = (int32_t)(t.row0 + rank * (t.tn / 2));
+                for (int k = 0; k < P.k_steps; ++k) {
+                    ok = __all_sync(0xFFFFFFFFu, wait_bar(&empty[s], ph ^ 1, g, SITE_PRODUCER_EMPTY));
+                    if (!ok) break;
+                    uint8_t* w = smem + (uint32_t)s * STAGE_BYTES;
+                    armed |= 1u << s;
+                    armed_par = (armed_par & ~(1u << s)) | (ph << s);
+                    if (elect_one()) {
+                        mbar_arrive_expect_tx(&full[s], STAGE_BYTES);
+                        if (P.b3d)
+                            tma_load_3d(w, &tmB, &full[s], k * S8_KSTEP, w0, t.expert);
+                        else
+                            tma_load_2d(w, &tmB, &full[s], k * S8_KSTEP, w0);
+                        tma_load_2d(w + W_BYTES, &tmA, &full[s], k * S8_KSTEP, x0);
+                    }
+                    __syncwarp();
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (lane == 0) {
+                // never leave with copies in flight into this CTA's shared memory
+                for (int i = 0; i < S; ++i)
+                    if (armed & (1u << i)) wait_bar_drain(&full[i], (armed_par >> i) & 1u, g);
+            }
+            __syncwarp();
+        } else if (warp == 1 && leader) {
+            // ---------------- MMAs (even CTA) ----------------
+            const uint64_t xd0 = make_sw128_kmajor_desc(smem_u32(slots));
+            int slot = 0;
+            uint32_t ph = 0, chunk = 0;
+            bool ok = true, issued = false;
+            Tile t;
+            for (int64_t i = pid; ok && pair_tile(P, blocks, i, lane, t); i += P.programs) {
+                const uint32_t idesc = make_idesc_f16(0, 256, t.tn);
+                for (int j = 0; j < nslots; ++j) {
+                    const uint32_t b = chunk & 1;
+                    if (j % SLOT_CHUNK == 0) {
+                        ok = __all_sync(0xFFFFFFFFu, wait_bar_cluster(&tempty[b], ((chunk >> 1) & 1) ^ 1, g, SITE_MMA_TMEM_EMPTY));
+                        if (!ok) break;
+                    }
+                    ok = __all_sync(0xFFFFFFFFu, wait_bar_cluster(&ready[slot], ph, g, SITE_MMA_OPERAND));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint64_t xd = xd0 + (uint64_t)((uint32_t)slot * (SLOT_BYTES / 16));
+                    const uint32_t wa = tmem_w + 32 * slot, d = tmem + TN * b;
+                    const bool last = j % SLOT_CHUNK == SLOT_CHUNK - 1 || j == nslots - 1;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) umma_f16_ts_pair(d, wa + 8 * q, xd + 2 * q, idesc, q || j % SLOT_CHUNK ? 1u : 0u);
+                        umma_commit_pair_mc(&slot_free[slot], 0x3);
+                        if (last) umma_commit_pair_mc(&tfull[b], 0x3);
+                    }
+                    __syncwarp();
+                    issued = true;
+                    if (last) ++chunk;
+                    if (++slot == NS) {
+                        slot = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+            if (issued) {  // every issued MMA has finished before TMEM is freed
+                if (elect_one()) umma_commit_pair_mc(done, 0x1);
+                __syncwarp();
+                wait_bar_drain(done, 0, g);
+            }
+            __syncwarp();
+        }
+    } else if (warp < 12) {
+        // ---------------- sums and epilogue ----------------
+        regs_up<REGS_SUMS>();
+        const int quarter = warp % 4, half = (warp - 4) / 4;
+        const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+        const uint32_t l_tempty = mapa_shared(smem_u32(tempty), 0);
+        uint32_t chunk = 0;
+        Tile t;
+        EpiArith ar = epi_arith(P.epi);
+        ar.alpha = 1.0f;
+        bool ok = true;
+        for (int64_t i = pid; ok && pair_tile(P, blocks, i, lane, t); i += P.programs) {
+            const int cols = t.tn / 2, c0 = half * cols;  // this warp's columns: a multiple of 16
+            int32_t sum[HALF];
+#pragma unroll
+            for (int q = 0; q < HALF; ++q) sum[q] = 0;
+            for (int j = 0; j < nslots; j += SLOT_CHUNK, ++chunk) {
+                const uint32_t b = chunk & 1;
+                ok = __all_sync(0xFFFFFFFFu, wait_bar(&tfull[b], (chunk >> 1) & 1, g, SITE_EPI_TMEM_FULL));
+                if (!ok) break;
+                tc_fence_after_sync();
+                __syncwarp();
+#pragma unroll
+                for (int q = 0; q < HALF; q += 16)
+                    if (q < cols) {
+                        uint32_t v[16];
+                        tmem_ld_32x32b_x16(tmem + TN * b + c0 + q + lanes, v);
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) sum[q + r] += __float2int_rn(__uint_as_float(v[r]));
+                    }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote_relaxed(l_tempty + 8u * b);
+            }
+            if (!ok) break;
+            const int64_t n = t.n0 + 128 * rank + 32 * quarter + lane, m0 = t.row0 + c0;
+            const int rows = t.rows - c0 < cols ? t.rows - c0 : cols;
+            const bool in = n < P.epi.N;
+            const float channel = in ? s8_channel_factor(P, t.expert, n) : 0.0f, bias = bias_at(ar, n);
+            if (rows > 0 && mx_block_in_bounds(P.epi, m0, rows, t.n0 + 128 * rank + 32 * quarter < P.epi.N ? t.n0 + 128 * rank + 32 * quarter : 0, 1)) {
+                float tokens = 0.0f;
+#pragma unroll
+                for (int q = 0; q < HALF; q += 8)
+                    if (q < rows) {
+                        if (q % 32 == 0) tokens = q + lane < rows ? s8_token_factor(P, m0 + q + lane) : 0.0f;
+                        store8_any(P, ar, sum + q, m0 + q, rows - q, n, in, channel, bias, tokens, q % 32);
+                    }
+            }
+        }
+    } else {
+        // ---------------- f16 operands ----------------
+        regs_down<REGS_OPERANDS>();
+        const int half = (warp - 12) / 4, thread = threadIdx.x & 127, row = warp % 4 * 32 + lane;
+        const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
+        const uint32_t l_ready = mapa_shared(smem_u32(ready), 0);
+        int s = 0, slot = half;
+        uint32_t ph = 0, sph = 1;
+        bool ok = true;
+        Tile t;
+        for (int64_t i = pid; ok && pair_tile(P, blocks, i, lane, t); i += P.programs) {
+            for (int k = 0; k < P.k_steps; ++k) {
+                ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[s], ph, g, SITE_DQ_RAW));
+                if (!ok) break;
+                ok = __all_sync(0xFFFFFFFFu, wait_bar(&slot_free[slot], sph, g, SITE_DQ_EMPTY));
+                if (!ok) break;
+                tc_fence_after_sync();
+                __syncwarp();
+                const uint8_t* w = smem + (uint32_t)s * STAGE_BYTES;
+                tokens_half(w + W_BYTES, half, slots + slot * SLOT_BYTES, t.tn / 2, thread);
+                weights_half(w, half, tmem_w + 32 * slot + lanes, row);
+                tmem_st_wait();
+                fence_proxy_async_smem();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&empty[s]);
+                    if (leader)
+                        mbar_arrive(&ready[slot]);
+                    else
+                        mbar_arrive_remote(l_ready + 8u * slot);  // (a release: the operands are in this CTA's shared memory)
+                }
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1;
+                }
+                slot += 2;
+                if (slot >= NS) {
+                    slot -= NS;
+                    sph ^= 1;
+                }
+            }
+        }
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // the leader's MMAs and all cross-CTA arrivals are done
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+cudaError_t configure() {
+    static std::atomic<uint64_t> configured{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(configured.load() & bit)) {
+        // the split of registers above holds for this many at launch; with fewer, the
+        // warps that ask for more would wait for ever
+        cudaFuncAttributes a;
+        e = cudaFuncGetAttributes(&a, s8_pair_kernel);
+        if (e != cudaSuccess) return e;
+        if (a.numRegs != REGS_LAUNCH) return cudaErrorInvalidConfiguration;
+        e = cudaFuncSetAttribute(s8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM_BYTES);
+        if (e != cudaSuccess) return e;
+        configured.fetch_or(bit);
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_s8_pair(const S8Maps& m, const S8GemmParams& p, int clusters, cudaStream_t st) {
+    if (p.tile_rows < 32 || p.tile_rows > TN || p.tile_rows % 32) return cudaErrorInvalidValue;
+    const cudaError_t e = configure();
+    if (e != cudaSuccess) return e;
+    return launch_pdl(s8_pair_kernel, 2 * clusters, THREADS, SMEM_BYTES, st, m.a, m.b, p);
+}
+
+int s8_pair_max_clusters() {
+    if (configure() != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2, 1, 1);
+    cfg.blockDim = dim3(THREADS, 1, 1);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, s8_pair_kernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
+}  // namespace qg

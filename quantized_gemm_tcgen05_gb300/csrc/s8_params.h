@@ -46,4 +46,11 @@ int s8_gemv_slices(int64_t n, int64_t k, int64_t tiles, int sm_count);
 // cluster (width 32 or 128).
 cudaError_t launch_s8_gemm(int width, const S8Maps& m, const S8GemmParams& p, int grid, cudaStream_t st);
 
+// The CTA-pair kernel: 256 channels x up to S8_PAIR_TOKENS tokens, persistent
+// clusters of two.
+constexpr int S8_PAIR_TOKENS = 192;
+cudaError_t launch_s8_pair(const S8Maps& m, const S8GemmParams& p, int clusters, cudaStream_t st);
+// Clusters that can be resident at once.
+int s8_pair_max_clusters();
+
 }  // namespace qg

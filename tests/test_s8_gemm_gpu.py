@@ -12,7 +12,7 @@ import quantized_gemm_tcgen05_gb300 as qg
 
 pytestmark = pytest.mark.gpu
 OK = qg.GEMM_OK
-KERNELS = ["", "s8_gemv", "s8_t32", "s8_t128"]
+KERNELS = ["", "s8_gemv", "s8_t32", "s8_t128", "s8_pair"]
 
 
 @pytest.fixture(scope="module")
