@@ -399,6 +399,13 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// The same with a release at the scope of this CTA: what this CTA's own tensor core
+// or threads read before the other CTA goes on from the barrier, as its half of a
+// pair's operands.  (The release at cluster scope cost 1000 cycles a K-step there.)
+__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // The same without the release, for arrivals that publish no ordinary memory:
 // TMEM handed over (its accesses completed by tcgen05.wait and fenced by
 // tc_fence_before_sync), or shared memory that the caller has done with.  The

@@ -74,27 +74,43 @@ __device__ __forceinline__ int64_t expert_blocks(const S8GemmParams& P, int lane
     return n < P.tiles_m ? n : P.tiles_m;
 }
 
-// Half of a stage (64 codes of 128 channels) to 32 TMEM columns.
-__device__ __forceinline__ void weights_half(const uint8_t* raw, int half, uint32_t taddr, int row) {
-    const uint8_t* base = raw + row * 128;
-    const int x = row & 7;
-    uint32_t r[32];
+// Half of a stage, 64 codes of 128 channels and of `rows` tokens (a multiple of 16,
+// at most 8 * OCTETS): a thread's codes, and their way into 32 TMEM columns and an f16 tile.
+// The tokens' four chunks of 16 codes and eight rows go to eight threads each, so that
+// neither side has bank conflicts.
+template <int OCTETS>
+struct HalfStage {
+    static constexpr int N = OCTETS * 4 / 16;
+    uint4 w[4], x[N];
+    __device__ __forceinline__ void load(const uint8_t* wraw, const uint8_t* xraw, int half, int row, int rows, int thread) {
+        const int x7 = row & 7, r8 = thread & 7;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) s8_to_f16(*reinterpret_cast<const uint4*>(base + (((4 * half + c) ^ x) << 4)), r + 8 * c);
-    tmem_st_32x32b(taddr, r);
-}
-// Half of a stage (64 codes of `rows` tokens, a multiple of 16) to an f16 tile.
-__device__ __forceinline__ void tokens_half(const uint8_t* raw, int half, uint8_t* out, int rows, int thread) {
-    const int r8 = thread & 7;
-    for (int i = thread >> 3; i < rows / 2; i += 16) {  // four chunks of rows / 8 octets
-        const int c = i & 3, row = (i >> 2) * 8 + r8;
-        uint32_t h[8];
-        s8_to_f16(*reinterpret_cast<const uint4*>(raw + row * 128 + (((4 * half + c) ^ r8) << 4)), h);
-        uint8_t* to = out + row * 128;
-        *reinterpret_cast<uint4*>(to + (((2 * c) ^ r8) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(to + (((2 * c + 1) ^ r8) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+        for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4*>(wraw + row * 128 + (((4 * half + c) ^ x7) << 4));
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int i = (thread >> 3) + 16 * k;
+            if (i < rows / 2) x[k] = *reinterpret_cast<const uint4*>(xraw + ((i >> 2) * 8 + r8) * 128 + (((4 * half + (i & 3)) ^ r8) << 4));
+        }
     }
-}
+    __device__ __forceinline__ void store(uint32_t taddr, uint8_t* out, int rows, int thread) const {
+        uint32_t r[32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s8_to_f16(w[c], r + 8 * c);
+        tmem_st_32x32b(taddr, r);
+        const int r8 = thread & 7;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int i = (thread >> 3) + 16 * k, c = 2 * (i & 3);
+            if (i < rows / 2) {
+                uint32_t h[8];
+                s8_to_f16(x[k], h);
+                uint8_t* to = out + ((i >> 2) * 8 + r8) * 128;
+                *reinterpret_cast<uint4*>(to + ((c ^ r8) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(to + (((c + 1) ^ r8) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+        }
+    }
+};
 
 // Eight tokens m0 .. of this lane's channel n.
 template <int ACT, int DT>
@@ -323,23 +339,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             for (int k = 0; k < P.k_steps; ++k) {
                 ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[s], ph, g, SITE_DQ_RAW));
                 if (!ok) break;
+                const uint8_t* w = smem + (uint32_t)s * STAGE_BYTES;
+                HalfStage<HALF / 8> codes;
+                codes.load(w, w + W_BYTES, half, row, t.tn / 2, thread);
                 ok = __all_sync(0xFFFFFFFFu, wait_bar(&slot_free[slot], sph, g, SITE_DQ_EMPTY));
                 if (!ok) break;
                 tc_fence_after_sync();
                 __syncwarp();
-                const uint8_t* w = smem + (uint32_t)s * STAGE_BYTES;
-                tokens_half(w + W_BYTES, half, slots + slot * SLOT_BYTES, t.tn / 2, thread);
-                weights_half(w, half, tmem_w + 32 * slot + lanes, row);
+                if (lane == 0) mbar_arrive(&empty[s]);
+                codes.store(tmem_w + 32 * slot + lanes, slots + slot * SLOT_BYTES, t.tn / 2, thread);
                 tmem_st_wait();
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(&empty[s]);
                     if (leader)
                         mbar_arrive(&ready[slot]);
                     else
-                        mbar_arrive_remote(l_ready + 8u * slot);  // (a release: the operands are in this CTA's shared memory)
+                        mbar_arrive_remote_cta(l_ready + 8u * slot);
                 }
                 if (++s == S) {
                     s = 0;
