@@ -27,8 +27,10 @@ constexpr int NS = 4;  // f16 slots: 64 of K
 constexpr uint32_t W_BYTES = 128 * 128, X_BYTES = HALF * 128, STAGE_BYTES = W_BYTES + X_BYTES;
 constexpr uint32_t SLOT_BYTES = HALF * 128;
 constexpr uint32_t RING_BYTES = S * STAGE_BYTES + NS * SLOT_BYTES;
+constexpr int STAGE_PITCH = 36;  // words of a token's row in an epilogue warp's buffer
+constexpr uint32_t EPI_BYTES = 8 * 32 * STAGE_PITCH * 4;
 constexpr uint32_t AUX_BYTES = (2 * S + 2 * NS + 5) * 8 + 16;
-constexpr uint32_t SMEM_BYTES = 1024 + RING_BYTES + AUX_BYTES;
+constexpr uint32_t SMEM_BYTES = 1024 + RING_BYTES + EPI_BYTES + AUX_BYTES;
 constexpr int SLOT_CHUNK = 2 * S8_CHUNK;  // slots whose sums fp32 holds exactly
 static_assert(2 * TN + 32 * NS <= 512 && SMEM_BYTES <= 232448 && STAGE_BYTES % 1024 == 0 && SLOT_BYTES % 1024 == 0, "");
 
@@ -112,33 +114,58 @@ struct HalfStage {
     }
 };
 
-// Eight tokens m0 .. of this lane's channel n.
+// A block of 32 tokens (m0 ..) x 32 channels (n0 ..) of finished sums, in `stage` with
+// a token a row: a lane has the same four channels of eight tokens, so that a token's
+// 32 channels are stored together.  tokens: the factor of token `lane`.
 template <int ACT, int DT>
-__device__ __forceinline__ void store8(const S8GemmParams& P, const EpiArith& ar, const int32_t* sum, int64_t m0, int rows, int64_t n, bool in,
-                                        float channel, float bias, float tokens, int first) {
+__device__ __forceinline__ void store_block(const S8GemmParams& P, const int32_t* stage, int64_t m0, int rows, int64_t n0, float tokens,
+                                            const S8Channels& ch, int lane) {
     const EpiParams& e = P.epi;
-    float c[8];
+    EpiArith ar = epi_arith(e);
+    ar.alpha = 1.0f;
+    const int64_t n = n0 + 4 * (lane & 7);
+    const int have = e.N - n < 4 ? (int)(e.N - n) : 4;
+    const bool vec = P.vec4 && have == 4, use_c = ar.beta != 0.0f;
+    const int64_t d_step = 4 * e.ldd, c_step = 4 * e.ldc;
+    int64_t d = (m0 + lane / 8) * e.ldd + n, cat = (m0 + lane / 8) * e.ldc + n;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c[i] = ar.beta != 0.0f && in && i < rows ? ld_elem(e.C, DT, (m0 + i) * e.ldc + n) : 0.0f;
+    for (int q = 0; q < 8; ++q, d += d_step, cat += c_step) {
+        const int r = 4 * q + lane / 8;
+        const float token = __shfl_sync(0xFFFFFFFFu, tokens, r);
+        if (r >= rows || have <= 0) continue;
+        const int4 s = *reinterpret_cast<const int4*>(stage + r * STAGE_PITCH + 4 * (lane & 7));
+        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f}, x[4];
+        if (use_c) {
+            if (vec) {
+                const float4 f = ld4(e.C, DT, cat);
+                c[0] = f.x, c[1] = f.y, c[2] = f.z, c[3] = f.w;
+            } else {
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const float t0 = __shfl_sync(0xFFFFFFFFu, tokens, first + i), t1 = __shfl_sync(0xFFFFFFFFu, tokens, first + i + 1);
-        float x0, x1;
-        mx_value2<ACT, DT>(ar, s8_scaled(sum[i], t0, channel), s8_scaled(sum[i + 1], t1, channel), c[i], c[i + 1], bias, bias, x0, x1);
-        if (in && i < rows) st_elem(e.D, DT, (m0 + i) * e.ldd + n, x0);
-        if (in && i + 1 < rows) st_elem(e.D, DT, (m0 + i + 1) * e.ldd + n, x1);
+                for (int k = 0; k < 4; ++k)
+                    if (k < have) c[k] = ld_elem(e.C, DT, cat + k);
+            }
+        }
+        mx_value2<ACT, DT>(ar, s8_scaled(s.x, token, ch.scale[0]), s8_scaled(s.y, token, ch.scale[1]), c[0], c[1], ch.bias[0], ch.bias[1], x[0], x[1]);
+        mx_value2<ACT, DT>(ar, s8_scaled(s.z, token, ch.scale[2]), s8_scaled(s.w, token, ch.scale[3]), c[2], c[3], ch.bias[2], ch.bias[3], x[2], x[3]);
+        if (vec) {
+            st4(e.D, DT, d, make_float4(x[0], x[1], x[2], x[3]));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < have) st_elem(e.D, DT, d + k, x[k]);
+        }
     }
 }
-__device__ __forceinline__ void store8_any(const S8GemmParams& P, const EpiArith& ar, const int32_t* sum, int64_t m0, int rows, int64_t n, bool in,
-                                            float channel, float bias, float tokens, int first) {
+__device__ __forceinline__ void store_block_any(const S8GemmParams& P, const int32_t* stage, int64_t m0, int rows, int64_t n0, float tokens,
+                                                const S8Channels& ch, int lane) {
     with_epi_act(P.epi, [&](auto act) {
         constexpr int ACT = decltype(act)::value;
         if (P.epi.d_type == DT_BF16)
-            store8<ACT, DT_BF16>(P, ar, sum, m0, rows, n, in, channel, bias, tokens, first);
+            store_block<ACT, DT_BF16>(P, stage, m0, rows, n0, tokens, ch, lane);
         else if (P.epi.d_type == DT_F16)
-            store8<ACT, DT_F16>(P, ar, sum, m0, rows, n, in, channel, bias, tokens, first);
+            store_block<ACT, DT_F16>(P, stage, m0, rows, n0, tokens, ch, lane);
         else
-            store8<ACT, DT_F32>(P, ar, sum, m0, rows, n, in, channel, bias, tokens, first);
+            store_block<ACT, DT_F32>(P, stage, m0, rows, n0, tokens, ch, lane);
     });
 }
 
@@ -148,7 +175,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* slots = smem + S * STAGE_BYTES;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING_BYTES);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING_BYTES + EPI_BYTES);
     uint64_t* empty = full + S;        // a stage's codes have been read (8 warps)
     uint64_t* ready = empty + S;       // leader: both CTAs' operands are in the slot (8 warps)
     uint64_t* slot_free = ready + NS;
@@ -280,6 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         // ---------------- sums and epilogue ----------------
         regs_up<REGS_SUMS>();
         const int quarter = warp % 4, half = (warp - 4) / 4;
+        int32_t* stage = reinterpret_cast<int32_t*>(smem + RING_BYTES) + (warp - 4) * 32 * STAGE_PITCH;
         const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
         const uint32_t l_tempty = mapa_shared(smem_u32(tempty), 0);
         uint32_t chunk = 0;
@@ -311,19 +339,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 if (lane == 0) mbar_arrive_remote_relaxed(l_tempty + 8u * b);
             }
             if (!ok) break;
-            const int64_t n = t.n0 + 128 * rank + 32 * quarter + lane, m0 = t.row0 + c0;
+            const int64_t n0 = t.n0 + 128 * rank + 32 * quarter, m0 = t.row0 + c0;
             const int rows = t.rows - c0 < cols ? t.rows - c0 : cols;
-            const bool in = n < P.epi.N;
-            const float channel = in ? s8_channel_factor(P, t.expert, n) : 0.0f, bias = bias_at(ar, n);
-            if (rows > 0 && mx_block_in_bounds(P.epi, m0, rows, t.n0 + 128 * rank + 32 * quarter < P.epi.N ? t.n0 + 128 * rank + 32 * quarter : 0, 1)) {
-                float tokens = 0.0f;
+            if (rows <= 0 || n0 >= P.epi.N) continue;
+            if (!mx_block_in_bounds(P.epi, m0, rows, n0, P.epi.N - n0 < 32 ? P.epi.N - n0 : 32)) continue;
+            const S8Channels ch = s8_channels(P, ar, t.expert, n0 + 4 * (lane & 7));
 #pragma unroll
-                for (int q = 0; q < HALF; q += 8)
-                    if (q < rows) {
-                        if (q % 32 == 0) tokens = q + lane < rows ? s8_token_factor(P, m0 + q + lane) : 0.0f;
-                        store8_any(P, ar, sum + q, m0 + q, rows - q, n, in, channel, bias, tokens, q % 32);
-                    }
-            }
+            for (int q = 0; q < HALF; q += 32)
+                if (q < rows) {
+                    const float tokens = q + lane < rows ? s8_token_factor(P, m0 + q + lane) : 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) stage[k * STAGE_PITCH + lane] = sum[q + k];
+                    __syncwarp();
+                    store_block_any(P, stage, m0 + q, rows - q, n0, tokens, ch, lane);
+                    __syncwarp();
+                }
         }
     } else {
         // ---------------- f16 operands ----------------
