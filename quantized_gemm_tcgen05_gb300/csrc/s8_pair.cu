@@ -269,30 +269,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             Tile t;
             for (int64_t i = pid; ok && pair_tile(P, blocks, i, lane, t); i += P.programs) {
                 const uint32_t idesc = make_idesc_f16(0, 256, t.tn);
-                for (int j = 0; j < nslots; ++j) {
-                    const uint32_t b = chunk & 1;
-                    if (j % SLOT_CHUNK == 0) {
-                        ok = __all_sync(0xFFFFFFFFu, wait_bar_cluster(&tempty[b], ((chunk >> 1) & 1) ^ 1, g, SITE_MMA_TMEM_EMPTY));
+                for (int j0 = 0; ok && j0 < nslots; j0 += SLOT_CHUNK, ++chunk) {
+                    const uint32_t b = chunk & 1, d = tmem + TN * b;
+                    const int n = nslots - j0 < SLOT_CHUNK ? nslots - j0 : SLOT_CHUNK;
+                    ok = __all_sync(0xFFFFFFFFu, wait_bar(&tempty[b], ((chunk >> 1) & 1) ^ 1, g, SITE_MMA_TMEM_EMPTY));
+                    for (int j = 0; ok && j < n; ++j) {
+                        // (this thread reads nothing that the other CTA wrote: its tensor core
+                        // does, there, so no acquire at cluster scope is needed)
+                        ok = __all_sync(0xFFFFFFFFu, wait_bar(&ready[slot], ph, g, SITE_MMA_OPERAND));
                         if (!ok) break;
-                    }
-                    ok = __all_sync(0xFFFFFFFFu, wait_bar_cluster(&ready[slot], ph, g, SITE_MMA_OPERAND));
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    const uint64_t xd = xd0 + (uint64_t)((uint32_t)slot * (SLOT_BYTES / 16));
-                    const uint32_t wa = tmem_w + 32 * slot, d = tmem + TN * b;
-                    const bool last = j % SLOT_CHUNK == SLOT_CHUNK - 1 || j == nslots - 1;
-                    if (elect_one()) {
+                        tc_fence_after_sync();
+                        const uint64_t xd = xd0 + (uint64_t)((uint32_t)slot * (SLOT_BYTES / 16));
+                        const uint32_t wa = tmem_w + 32 * slot;
+                        if (elect_one()) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) umma_f16_ts_pair(d, wa + 8 * q, xd + 2 * q, idesc, q || j % SLOT_CHUNK ? 1u : 0u);
-                        umma_commit_pair_mc(&slot_free[slot], 0x3);
-                        if (last) umma_commit_pair_mc(&tfull[b], 0x3);
-                    }
-                    __syncwarp();
-                    issued = true;
-                    if (last) ++chunk;
-                    if (++slot == NS) {
-                        slot = 0;
-                        ph ^= 1;
+                            for (int q = 0; q < 4; ++q) umma_f16_ts_pair(d, wa + 8 * q, xd + 2 * q, idesc, q ? 1u : (uint32_t)j);
+                            umma_commit_pair_mc(&slot_free[slot], 0x3);
+                            if (j == n - 1) umma_commit_pair_mc(&tfull[b], 0x3);
+                        }
+                        __syncwarp();
+                        issued = true;
+                        if (++slot == NS) {
+                            slot = 0;
+                            ph ^= 1;
+                        }
                     }
                 }
             }
