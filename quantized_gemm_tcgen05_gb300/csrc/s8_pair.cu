@@ -10,7 +10,7 @@
 //
 //   warps 0-3    TMA producer, (leader) MMAs, two without work
 //   warps 4-11   sums and epilogue: a 32-lane quarter and half of the columns each
-//   warps 12-19  f16 operands
+//   warps 12-27  f16 operands
 #include <atomic>
 
 #include "mx_rows.h"
@@ -20,7 +20,7 @@ namespace qg {
 
 namespace {
 
-constexpr int THREADS = 640;
+constexpr int THREADS = 896;
 constexpr int TN = S8_PAIR_TOKENS, HALF = TN / 2;
 constexpr int S = 4;   // raw stages: 128 of K
 constexpr int NS = 4;  // f16 slots: 64 of K
@@ -32,11 +32,11 @@ constexpr uint32_t EPI_BYTES = 8 * 32 * STAGE_PITCH * 4;
 constexpr uint32_t AUX_BYTES = (2 * S + 2 * NS + 5) * 8 + 16;
 constexpr uint32_t SMEM_BYTES = 1024 + RING_BYTES + EPI_BYTES + AUX_BYTES;
 constexpr int SLOT_CHUNK = 2 * S8_CHUNK;  // slots whose sums fp32 holds exactly
-static_assert(2 * TN + 32 * NS <= 512 && SMEM_BYTES <= 232448 && STAGE_BYTES % 1024 == 0 && SLOT_BYTES % 1024 == 0, "");
+static_assert(S % 2 == 0 && 2 * TN + 32 * NS <= 512 && SMEM_BYTES <= 232448 && STAGE_BYTES % 1024 == 0 && SLOT_BYTES % 1024 == 0, "");
 
-// Registers of a thread: 640 threads are launched with 96.
-constexpr int REGS_LAUNCH = 96, REGS_SUMS = 128, REGS_OPERANDS = 80, REGS_REST = 64;
-static_assert(256 * REGS_SUMS + 256 * REGS_OPERANDS + 128 * REGS_REST <= THREADS * REGS_LAUNCH, "what was launched is shared out");
+// Registers of a thread: at launch, and by role.
+constexpr int REGS_LAUNCH = 72, REGS_SUMS = 128, REGS_OPERANDS = 48, REGS_REST = 56;
+static_assert(NS == 4 && 256 * REGS_SUMS + 128 * NS * REGS_OPERANDS + 128 * REGS_REST <= THREADS * REGS_LAUNCH, "what was launched is shared out");
 template <int N>
 __device__ __forceinline__ void regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -95,10 +95,13 @@ struct HalfStage {
         }
     }
     __device__ __forceinline__ void store(uint32_t taddr, uint8_t* out, int rows, int thread) const {
-        uint32_t r[32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) s8_to_f16(w[c], r + 8 * c);
-        tmem_st_32x32b(taddr, r);
+        for (int c = 0; c < 4; c += 2) {
+            uint32_t r[16];
+            s8_to_f16(w[c], r);
+            s8_to_f16(w[c + 1], r + 8);
+            tmem_st_32x32b(taddr + 8 * c, r);
+        }
         const int r8 = thread & 7;
 #pragma unroll
         for (int k = 0; k < N; ++k) {
@@ -358,26 +361,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     } else {
         // ---------------- f16 operands ----------------
         regs_down<REGS_OPERANDS>();
-        const int half = (warp - 12) / 4, thread = threadIdx.x & 127, row = warp % 4 * 32 + lane;
-        const uint32_t lanes = (uint32_t)(warp % 4 * 32) << 16;
-        const uint32_t l_ready = mapa_shared(smem_u32(ready), 0);
-        int s = 0, slot = half;
-        uint32_t ph = 0, sph = 1;
+        const int slot = (warp - 12) / 4, half = slot & 1, thread = threadIdx.x & 127, row = warp % 4 * 32 + lane;
+        const uint32_t taddr = tmem_w + 32 * slot + ((uint32_t)(warp % 4 * 32) << 16);
+        const uint32_t l_ready = mapa_shared(smem_u32(&ready[slot]), 0);
+        uint8_t* out = slots + slot * SLOT_BYTES;
+        // slots and K-steps are counted through all tiles; a stage is always read by the
+        // same two groups, so that none meets a phase of full[] out of turn
+        uint32_t n = slot, end = 0;
         bool ok = true;
         Tile t;
         for (int64_t i = pid; ok && pair_tile(P, blocks, i, lane, t); i += P.programs) {
-            for (int k = 0; k < P.k_steps; ++k) {
-                ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[s], ph, g, SITE_DQ_RAW));
+            end += nslots;
+            for (; n < end; n += NS) {
+                const uint32_t step = n / 2, s = step % S;
+                ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[s], (step / S) & 1, g, SITE_DQ_RAW));
                 if (!ok) break;
-                const uint8_t* w = smem + (uint32_t)s * STAGE_BYTES;
+                const uint8_t* w = smem + s * STAGE_BYTES;
                 HalfStage<HALF / 8> codes;
                 codes.load(w, w + W_BYTES, half, row, t.tn / 2, thread);
-                ok = __all_sync(0xFFFFFFFFu, wait_bar(&slot_free[slot], sph, g, SITE_DQ_EMPTY));
+                ok = __all_sync(0xFFFFFFFFu, wait_bar(&slot_free[slot], ((n / NS) & 1) ^ 1, g, SITE_DQ_EMPTY));
                 if (!ok) break;
                 tc_fence_after_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[s]);
-                codes.store(tmem_w + 32 * slot + lanes, slots + slot * SLOT_BYTES, t.tn / 2, thread);
+                codes.store(taddr, out, t.tn / 2, thread);
                 tmem_st_wait();
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
@@ -386,16 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     if (leader)
                         mbar_arrive(&ready[slot]);
                     else
-                        mbar_arrive_remote_cta(l_ready + 8u * slot);
-                }
-                if (++s == S) {
-                    s = 0;
-                    ph ^= 1;
-                }
-                slot += 2;
-                if (slot >= NS) {
-                    slot -= NS;
-                    sph ^= 1;
+                        mbar_arrive_remote_cta(l_ready);
                 }
             }
         }
