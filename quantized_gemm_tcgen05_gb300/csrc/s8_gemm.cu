@@ -2,19 +2,19 @@
 // cluster.
 //
 // A stage holds one K-step: 128 codes (one 128-byte swizzle row) of 128 channels
-// and of the tile's tokens.  Two groups of four warps take the K-steps in turn and
-// turn codes into f16 operands: the channels' into a slot of TMEM, the tokens' into
-// a slot of shared memory.  The accumulator has two buffers of TN columns; after 8
-// K-steps (1024 products) four warps add the full one to 32-bit sums in shared memory
+// and of the tile's tokens.  Groups of four warps take the stages' halves in turn and
+// turn their codes into f16 operands: the channels' into a slot of TMEM, the tokens' into
+// one of shared memory.  The accumulator has two buffers of TN columns; after 16
+// slots (1024 products) other warps add the full one to 32-bit sums in their registers
 // while the MMAs go on in the other.
 //
 // The tile's K-steps are shared out over the `splits` CTAs of a cluster, whose sums
 // meet as in mx_exchange.h: every CTA finishes its share of the tokens.  Integer
 // sums, so the order does not matter.
 //
-//   warp 0      TMA producer          warps 4-7   sums
-//   warp 1      MMAs                  warps 8-15  f16 operands
-//   warps 2-3   fetch the tile's C    all         epilogue
+//   warp 0     TMA producer     warp 1   MMAs     warps 2-3  fetch the tile's C
+//   then 4 or 8 warps of sums, 8 or 16 of operands (up to 32 tokens two CTAs share an
+//   SM, each with half as many); the epilogue is all warps'
 #include <atomic>
 
 #include "mx_exchange.h"
@@ -24,24 +24,34 @@ namespace qg {
 
 namespace {
 
-constexpr int THREADS = 512;
-
 template <int TN>
 struct Cfg {
-    static constexpr int CTAS = TN == 32 ? 2 : 1;   // per SM
-    static constexpr int STAGES = 3;
-    static constexpr int SLOTS = TN == 32 ? 3 : 2;  // f16 operands
+    static constexpr bool WIDE = TN > 32;
+    static constexpr int CTAS = WIDE ? 1 : 2;       // per SM
+    static constexpr int SUM_WARPS = WIDE ? 8 : 4;
+    static constexpr int GROUPS = WIDE ? 4 : 2;     // of operand warps
+    static constexpr int THREADS = 128 + 32 * SUM_WARPS + 128 * GROUPS;
+    static constexpr int COLS = TN / (SUM_WARPS / 4);  // of a warp's sums
+    // a stage is always read by the same groups, so that none meets a phase of full[]
+    // out of turn
+    static constexpr int STAGES = WIDE ? 4 : 3;
+    static constexpr int SLOTS = WIDE ? 4 : 6;
+    static_assert(SLOTS % GROUPS == 0 && STAGES % (GROUPS / 2) == 0, "");
     static constexpr uint32_t W_BYTES = 128 * 128, X_BYTES = TN * 128, STAGE_BYTES = W_BYTES + X_BYTES;
-    static constexpr uint32_t SLOT_BYTES = TN * 256;
+    static constexpr uint32_t SLOT_BYTES = TN * 128;
     static constexpr uint32_t RING_BYTES = STAGES * STAGE_BYTES + SLOTS * SLOT_BYTES;
-    static constexpr uint32_t SUM_BYTES = TN * 512;  // [token][channel]
+    static constexpr uint32_t SUM_BYTES = TN * 512;  // [token][channel], in the ring when it is idle
     static constexpr uint32_t AUX_BYTES = (2 * STAGES + 2 * SLOTS + 6) * 8 + 16;
-    static constexpr uint32_t SMEM_BYTES = 1024 + RING_BYTES + SUM_BYTES + AUX_BYTES;
-    static constexpr uint32_t TMEM_COLS = TN == 32 ? 256 : 512;
-    static_assert(2 * TN + 64 * SLOTS <= TMEM_COLS && SMEM_BYTES <= 232448 && CTAS * (SMEM_BYTES + 1024) <= 233472, "");
-    static_assert(STAGES >= SLOTS, "a free slot tells that the stage's last use is over");
-    static_assert((TN + 8) * 512 <= RING_BYTES, "the shares received");
+    static constexpr uint32_t SMEM_BYTES = 1024 + RING_BYTES + AUX_BYTES;
+    static constexpr uint32_t TMEM_COLS = WIDE ? 512 : 256;
+    static_assert(2 * TN + 32 * SLOTS <= TMEM_COLS && SMEM_BYTES <= 232448 && CTAS * (SMEM_BYTES + 1024) <= 233472, "");
+    static_assert(SUM_BYTES + (TN + 8) * 512 <= RING_BYTES, "the sums, and the shares received");
+    // registers of a thread: at launch, and by role where they differ
+    static constexpr int REGS_LAUNCH = WIDE ? 72 : 64, REGS_SUMS = 104, REGS_OPERANDS = 56, REGS_REST = 56;
+    static_assert(!WIDE || 32 * SUM_WARPS * REGS_SUMS + 128 * GROUPS * REGS_OPERANDS + 128 * REGS_REST <= THREADS * REGS_LAUNCH,
+                  "what was launched is shared out");
 };
+constexpr int SLOT_CHUNK = 2 * S8_CHUNK;  // slots whose sums fp32 holds exactly
 
 // The steps of mx_exchange.h for sums: shares are runs of tokens, `each` but for the
 // last ones.
@@ -72,21 +82,21 @@ struct SumsLink {
 };
 
 template <int TN>
-__global__ void __launch_bounds__(THREADS, Cfg<TN>::CTAS)
+__global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
     s8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ S8GemmParams P) {
     using C = Cfg<TN>;
-    constexpr int S = C::STAGES, NS = C::SLOTS;
+    constexpr int S = C::STAGES, NS = C::SLOTS, G = C::GROUPS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* slots = smem + S * C::STAGE_BYTES;
-    int32_t* sums = reinterpret_cast<int32_t*>(smem + C::RING_BYTES);
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::RING_BYTES + C::SUM_BYTES);
-    uint64_t* empty = full + S;
+    int32_t* sums = reinterpret_cast<int32_t*>(smem);  // once the ring is idle
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::RING_BYTES);
+    uint64_t* empty = full + S;     // a stage's codes have been read (8 warps)
     uint64_t* ready = empty + S;    // a slot's operands are there (4 warps)
     uint64_t* slot_free = ready + NS;
     uint64_t* tfull = slot_free + NS;  // an accumulator buffer is complete
-    uint64_t* tempty = tfull + 2;      // ... and in the sums (4 warps)
+    uint64_t* tempty = tfull + 2;      // ... and in the sums
     uint64_t* idle = tempty + 2;       // every CTA of the cluster is through with its ring
     uint64_t* part = idle + 1;         // the sums' shares have arrived
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(part + 1);
@@ -98,7 +108,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<TN>::CTAS)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 4);
+            mbar_init(&empty[s], 8);
         }
         for (int s = 0; s < NS; ++s) {
             mbar_init(&ready[s], 4);
@@ -106,7 +116,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<TN>::CTAS)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
-            mbar_init(&tempty[b], 4);
+            mbar_init(&tempty[b], C::SUM_WARPS);
         }
         mbar_init(idle, (uint32_t)splits);
         mbar_init(part, 1);
@@ -131,6 +141,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<TN>::CTAS)
     const int64_t tile = blockIdx.x / splits;
     const int64_t tm = tile % P.tiles_m, tw = tile / P.tiles_m;
     const int k0 = (int)((int64_t)P.k_steps * rank / splits), nk = (int)((int64_t)P.k_steps * (rank + 1) / splits) - k0;
+    const int nslots = 2 * nk;
     const int64_t n0 = tw * 128;
     const Guard g{P.status, P.timeout_ns, abort_flag};
     if (!P.offsets && warp == 0 && lane == 0) {
@@ -149,104 +160,106 @@ __global__ void __launch_bounds__(THREADS, Cfg<TN>::CTAS)
         row0 = tm * tn;
         rows = (int)(P.epi.M - row0 < tn ? P.epi.M - row0 : tn);
     }
-    const int chunks = (nk + S8_CHUNK - 1) / S8_CHUNK;
 
     bool ok = live;
-    if (live && warp == 0) {
-        const uint32_t bytes = C::W_BYTES + (uint32_t)tn * 128u;
-        int s = 0;
-        uint32_t ph = 1;
-        for (int i = 0; i < nk; ++i) {
-            ok = __all_sync(0xFFFFFFFFu, wait_bar(&empty[s], ph, g, SITE_PRODUCER_EMPTY));
-            if (!ok) break;
-            uint8_t* w = smem + (uint32_t)s * C::STAGE_BYTES;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&full[s], bytes);
-                if (P.b3d)
-                    tma_load_3d(w, &tmB, &full[s], (k0 + i) * S8_KSTEP, (int32_t)n0, expert);
-                else
-                    tma_load_2d(w, &tmB, &full[s], (k0 + i) * S8_KSTEP, (int32_t)n0);
-                tma_load_2d(w + C::W_BYTES, &tmA, &full[s], (k0 + i) * S8_KSTEP, (int32_t)row0);
-            }
-            __syncwarp();
-            if (++s == S) {
-                s = 0;
-                ph ^= 1;
-            }
-        }
-    } else if (live && warp == 1) {
-        const uint64_t xd0 = make_sw128_kmajor_desc(smem_u32(slots));
-        int slot = 0;
-        uint32_t ph = 0;
-        for (int i = 0; i < nk; ++i) {
-            const int c = i / S8_CHUNK, b = c & 1;
-            if (i % S8_CHUNK == 0) {
-                ok = __all_sync(0xFFFFFFFFu, wait_bar(&tempty[b], ((c >> 1) & 1) ^ 1, g, SITE_MMA_TMEM_EMPTY));
+    int32_t sum[C::COLS];  // (of the warps that add up)
+    const int sum_half = (warp - 4) / 4;  // which of the columns
+    if (warp < 4) {
+        if constexpr (C::WIDE) regs_down<C::REGS_REST>();
+        if (live && warp == 0) {
+            const uint32_t bytes = C::W_BYTES + (uint32_t)tn * 128u;
+            int s = 0;
+            uint32_t ph = 1;
+            for (int i = 0; i < nk; ++i) {
+                ok = __all_sync(0xFFFFFFFFu, wait_bar(&empty[s], ph, g, SITE_PRODUCER_EMPTY));
                 if (!ok) break;
-            }
-            ok = __all_sync(0xFFFFFFFFu, wait_bar(&ready[slot], ph, g, SITE_MMA_OPERAND));
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint64_t xd = xd0 + (uint64_t)((uint32_t)slot * (C::SLOT_BYTES / 16));
-            const uint32_t wa = tmem_w + 64 * slot, d = tmem + TN * b;
-            const uint32_t acc = i % S8_CHUNK ? 1u : 0u;
-            if (elect_one()) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    umma_f16_ts(d, wa + 8 * q, xd + (uint64_t)((q / 4) * tn * 8 + 2 * (q % 4)), P.idesc, q ? 1u : acc);
-                umma_commit(&slot_free[slot]);
-                if (i % S8_CHUNK == S8_CHUNK - 1 || i == nk - 1) umma_commit(&tfull[b]);
-            }
-            __syncwarp();
-            if (++slot == NS) {
-                slot = 0;
-                ph ^= 1;
-            }
-        }
-    } else if (live && warp < 4) {
-        if (P.epi.beta != 0.0f && n0 < P.epi.N)
-            for (int r = threadIdx.x - 64; r < rows; r += 64) mx_prefetch_c(P.epi, row0 + r, n0, P.epi.N - n0 < 128 ? P.epi.N - n0 : 128);
-    } else if (live && warp < 8) {
-        const uint32_t quarter = (uint32_t)(warp % 4 * 32) << 16;
-        int32_t* mine = sums + warp % 4 * 32 + lane;
-        for (int c = 0; c < chunks; ++c) {
-            const int b = c & 1;
-            ok = __all_sync(0xFFFFFFFFu, wait_bar(&tfull[b], (c >> 1) & 1, g, SITE_EPI_TMEM_FULL));
-            if (!ok) break;
-            tc_fence_after_sync();
-#pragma unroll 1
-            for (int j = 0; j < rows; j += 16) {
-                uint32_t v[16];
-                tmem_ld_32x32b_x16(tmem + TN * b + j + quarter, v);
-#pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                    const int32_t x = __float2int_rn(__uint_as_float(v[q]));
-                    int32_t* to = mine + (j + q) * 128;
-                    *to = c ? *to + x : x;
+                uint8_t* w = smem + (uint32_t)s * C::STAGE_BYTES;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(&full[s], bytes);
+                    if (P.b3d)
+                        tma_load_3d(w, &tmB, &full[s], (k0 + i) * S8_KSTEP, (int32_t)n0, expert);
+                    else
+                        tma_load_2d(w, &tmB, &full[s], (k0 + i) * S8_KSTEP, (int32_t)n0);
+                    tma_load_2d(w + C::W_BYTES, &tmA, &full[s], (k0 + i) * S8_KSTEP, (int32_t)row0);
+                }
+                __syncwarp();
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1;
                 }
             }
+        } else if (live && warp == 1) {
+            const uint64_t xd0 = make_sw128_kmajor_desc(smem_u32(slots));
+            int slot = 0;
+            uint32_t ph = 0, chunk = 0;
+            for (int j0 = 0; ok && j0 < nslots; j0 += SLOT_CHUNK, ++chunk) {
+                const uint32_t b = chunk & 1, d = tmem + TN * b;
+                const int n = nslots - j0 < SLOT_CHUNK ? nslots - j0 : SLOT_CHUNK;
+                ok = __all_sync(0xFFFFFFFFu, wait_bar(&tempty[b], ((chunk >> 1) & 1) ^ 1, g, SITE_MMA_TMEM_EMPTY));
+                for (int j = 0; ok && j < n; ++j) {
+                    ok = __all_sync(0xFFFFFFFFu, wait_bar(&ready[slot], ph, g, SITE_MMA_OPERAND));
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint64_t xd = xd0 + (uint64_t)((uint32_t)slot * (C::SLOT_BYTES / 16));
+                    const uint32_t wa = tmem_w + 32 * slot;
+                    if (elect_one()) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) umma_f16_ts(d, wa + 8 * q, xd + 2 * q, P.idesc, q ? 1u : (uint32_t)j);
+                        umma_commit(&slot_free[slot]);
+                        if (j == n - 1) umma_commit(&tfull[b]);
+                    }
+                    __syncwarp();
+                    if (++slot == NS) {
+                        slot = 0;
+                        ph ^= 1;
+                    }
+                }
+            }
+        } else if (live && warp > 1) {
+            if (P.epi.beta != 0.0f && n0 < P.epi.N)
+                for (int r = threadIdx.x - 64; r < rows; r += 64) mx_prefetch_c(P.epi, row0 + r, n0, P.epi.N - n0 < 128 ? P.epi.N - n0 : 128);
+        }
+    } else if (warp < 4 + C::SUM_WARPS) {
+        if constexpr (C::WIDE) regs_up<C::REGS_SUMS>();
+        const uint32_t taddr = tmem + sum_half * C::COLS + ((uint32_t)(warp % 4 * 32) << 16);
+        const int cols = rows - sum_half * C::COLS;
+#pragma unroll
+        for (int q = 0; q < C::COLS; ++q) sum[q] = 0;
+        uint32_t chunk = 0;
+        for (int j0 = 0; ok && j0 < nslots; j0 += SLOT_CHUNK, ++chunk) {
+            const uint32_t b = chunk & 1;
+            ok = __all_sync(0xFFFFFFFFu, wait_bar(&tfull[b], (chunk >> 1) & 1, g, SITE_EPI_TMEM_FULL));
+            if (!ok) break;
+            tc_fence_after_sync();
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < C::COLS; q += 16)
+                if (q < cols) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(taddr + TN * b + q, v);
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) sum[q + r] += __float2int_rn(__uint_as_float(v[r]));
+                }
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(&tempty[b]);
         }
-    } else if (live) {
-        const int group = (warp - 8) / 4, thread = threadIdx.x & 127, row = warp % 4 * 32 + lane;
-        const uint32_t quarter = (uint32_t)(warp % 4 * 32) << 16;
-        for (int i = group; i < nk; i += 2) {
-            const int s = i % S, slot = i % NS;
-            // The slot first: it is free when the MMAs of K-step i - NS are done, and so
-            // when K-step i - S has landed.  A wait for this phase of full[s] that came
-            // before its last one had ended would not wait: stages are used by both
-            // groups, and copies may land out of order.
-            ok = __all_sync(0xFFFFFFFFu, wait_bar(&slot_free[slot], ((i / NS) & 1) ^ 1, g, SITE_DQ_EMPTY));
+    } else {
+        if constexpr (C::WIDE) regs_down<C::REGS_OPERANDS>();
+        const int group = (warp - 4 - C::SUM_WARPS) / 4, half = group & 1;
+        const uint32_t taddr = tmem_w + ((uint32_t)(warp % 4 * 32) << 16);
+        HalfStage<TN / 8> codes(half, warp % 4 * 32 + lane, threadIdx.x & 127);
+        for (int n = group; ok && n < nslots; n += G) {
+            const int step = n / 2, s = step % S, slot = n % NS;
+            ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[s], (step / S) & 1, g, SITE_DQ_RAW));
             if (!ok) break;
-            ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[s], (i / S) & 1, g, SITE_DQ_RAW));
+            const uint32_t w = smem_u32(smem) + (uint32_t)s * C::STAGE_BYTES;
+            codes.load(w, w + C::W_BYTES, tn);
+            ok = __all_sync(0xFFFFFFFFu, wait_bar(&slot_free[slot], ((n / NS) & 1) ^ 1, g, SITE_DQ_EMPTY));
             if (!ok) break;
             tc_fence_after_sync();
             __syncwarp();
-            const uint8_t* w = smem + (uint32_t)s * C::STAGE_BYTES;
-            s8_tokens_to_f16(w + C::W_BYTES, slots + slot * C::SLOT_BYTES, tn, thread);
-            s8_weights_to_tmem(w, tmem_w + 64 * slot + quarter, row);
+            codes.store(taddr + 32 * slot, smem_u32(slots) + slot * C::SLOT_BYTES, tn);
             tmem_st_wait();
             fence_proxy_async_smem();
             tc_fence_before_sync();
@@ -262,6 +275,21 @@ __global__ void __launch_bounds__(THREADS, Cfg<TN>::CTAS)
         // gave up: let copies in flight land and issued MMAs finish before shared memory and TMEM go
         mx_settle();
     }
+    if (live && warp >= 4 && warp < 4 + C::SUM_WARPS) {
+        int32_t* mine = sums + sum_half * C::COLS * 128 + warp % 4 * 32 + lane;
+#pragma unroll
+        for (int q = 0; q < C::COLS; ++q)
+            if (sum_half * C::COLS + q < rows) mine[q * 128] = sum[q];
+    }
+    if constexpr (C::WIDE) {  // the epilogue is everybody's again
+        if (warp >= 4 && warp < 4 + C::SUM_WARPS)
+            regs_down<C::REGS_LAUNCH>();
+        else
+            regs_up<C::REGS_LAUNCH>();
+    }
+    if (splits > 1) fence_proxy_async_smem();  // the sums are visible to the bulk copies
+    __syncthreads();
+    uint8_t* recv = smem + C::SUM_BYTES;
     // every thread keeps to four channels
     const int64_t n = n0 + 4 * lane;
     EpiArith ar = epi_arith(P.epi);
@@ -269,22 +297,20 @@ __global__ void __launch_bounds__(THREADS, Cfg<TN>::CTAS)
     if (splits == 1) {
         if (all_ok) {
             const S8Channels ch = s8_channels(P, ar, expert, n);
-            for (int m = warp; m < rows; m += THREADS / 32) s8_finish4(P, ar, ch, row0 + m, n, reinterpret_cast<const int4*>(sums + m * 128)[lane]);
+            for (int m = warp; m < rows; m += C::THREADS / 32) s8_finish4(P, ar, ch, row0 + m, n, reinterpret_cast<const int4*>(sums + m * 128)[lane]);
         }
     } else if (live) {
-        fence_proxy_async_smem();  // the sums are visible to the bulk copies
-        __syncthreads();
         // (whether this CTA's part is right or not: the others wait for it)
-        SumsLink link{idle, part, warning, smem_u32(sums), smem_u32(smem), splits, rank, rows, (rows + splits - 1) / splits, g};
+        SumsLink link{idle, part, warning, smem_u32(sums), smem_u32(recv), splits, rank, rows, (rows + splits - 1) / splits, g};
         ok = mx_exchange(link, splits, threadIdx.x == 0);
         all_ok = __syncthreads_and(all_ok && ok ? 1 : 0) != 0;
         if (all_ok) {
             const S8Channels ch = s8_channels(P, ar, expert, n);
             const int count = link.count(rank), first = link.first(rank);
-            for (int m = warp; m < count; m += THREADS / 32) {
+            for (int m = warp; m < count; m += C::THREADS / 32) {
                 int4 sum = make_int4(0, 0, 0, 0);
                 for (int z = 0; z < splits; ++z) {
-                    const int4 p = reinterpret_cast<const int4*>(smem + (uint32_t)(z * count + m) * 512u)[lane];
+                    const int4 p = reinterpret_cast<const int4*>(recv + (uint32_t)(z * count + m) * 512u)[lane];
                     sum.x += p.x;
                     sum.y += p.y;
                     sum.z += p.z;
@@ -315,13 +341,19 @@ cudaError_t launch_t(const S8Maps& m, const S8GemmParams& p, int grid, cudaStrea
     if (e != cudaSuccess) return e;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(configured.load() & bit)) {
+        // the split of registers above holds for this many at launch; with fewer, the
+        // warps that ask for more would wait for ever
+        cudaFuncAttributes a;
+        e = cudaFuncGetAttributes(&a, s8_gemm_kernel<TN>);
+        if (e != cudaSuccess) return e;
+        if (Cfg<TN>::WIDE && a.numRegs != Cfg<TN>::REGS_LAUNCH) return cudaErrorInvalidConfiguration;
         e = cudaFuncSetAttribute(s8_gemm_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<TN>::SMEM_BYTES);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(Cfg<TN>::THREADS);
     cfg.dynamicSmemBytes = Cfg<TN>::SMEM_BYTES;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];

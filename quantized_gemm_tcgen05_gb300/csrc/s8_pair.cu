@@ -35,17 +35,8 @@ constexpr int SLOT_CHUNK = 2 * S8_CHUNK;  // slots whose sums fp32 holds exactly
 static_assert(S % 2 == 0 && 2 * TN + 32 * NS <= 512 && SMEM_BYTES <= 232448 && STAGE_BYTES % 1024 == 0 && SLOT_BYTES % 1024 == 0, "");
 
 // Registers of a thread: at launch, and by role.
-constexpr int REGS_LAUNCH = 72, REGS_SUMS = 128, REGS_OPERANDS = 48, REGS_REST = 56;
+constexpr int REGS_LAUNCH = 72, REGS_SUMS = 128, REGS_OPERANDS = 56, REGS_REST = 24;
 static_assert(NS == 4 && 256 * REGS_SUMS + 128 * NS * REGS_OPERANDS + 128 * REGS_REST <= THREADS * REGS_LAUNCH, "what was launched is shared out");
-template <int N>
-__device__ __forceinline__ void regs_up() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_down() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 struct Tile {
     int64_t n0, row0;
     int expert, rows, tn;  // rows that exist; the MMA's columns: a multiple of 32
@@ -75,47 +66,6 @@ __device__ __forceinline__ int64_t expert_blocks(const S8GemmParams& P, int lane
     for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, d);
     return n < P.tiles_m ? n : P.tiles_m;
 }
-
-// Half of a stage, 64 codes of 128 channels and of `rows` tokens (a multiple of 16,
-// at most 8 * OCTETS): a thread's codes, and their way into 32 TMEM columns and an f16 tile.
-// The tokens' four chunks of 16 codes and eight rows go to eight threads each, so that
-// neither side has bank conflicts.
-template <int OCTETS>
-struct HalfStage {
-    static constexpr int N = OCTETS * 4 / 16;
-    uint4 w[4], x[N];
-    __device__ __forceinline__ void load(const uint8_t* wraw, const uint8_t* xraw, int half, int row, int rows, int thread) {
-        const int x7 = row & 7, r8 = thread & 7;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) w[c] = *reinterpret_cast<const uint4*>(wraw + row * 128 + (((4 * half + c) ^ x7) << 4));
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int i = (thread >> 3) + 16 * k;
-            if (i < rows / 2) x[k] = *reinterpret_cast<const uint4*>(xraw + ((i >> 2) * 8 + r8) * 128 + (((4 * half + (i & 3)) ^ r8) << 4));
-        }
-    }
-    __device__ __forceinline__ void store(uint32_t taddr, uint8_t* out, int rows, int thread) const {
-#pragma unroll
-        for (int c = 0; c < 4; c += 2) {
-            uint32_t r[16];
-            s8_to_f16(w[c], r);
-            s8_to_f16(w[c + 1], r + 8);
-            tmem_st_32x32b(taddr + 8 * c, r);
-        }
-        const int r8 = thread & 7;
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int i = (thread >> 3) + 16 * k, c = 2 * (i & 3);
-            if (i < rows / 2) {
-                uint32_t h[8];
-                s8_to_f16(x[k], h);
-                uint8_t* to = out + ((i >> 2) * 8 + r8) * 128;
-                *reinterpret_cast<uint4*>(to + ((c ^ r8) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(to + (((c + 1) ^ r8) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
-            }
-        }
-    }
-};
 
 // A block of 32 tokens (m0 ..) x 32 channels (n0 ..) of finished sums, in `stage` with
 // a token a row: a lane has the same four channels of eight tokens, so that a token's
@@ -364,10 +314,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         const int slot = (warp - 12) / 4, half = slot & 1, thread = threadIdx.x & 127, row = warp % 4 * 32 + lane;
         const uint32_t taddr = tmem_w + 32 * slot + ((uint32_t)(warp % 4 * 32) << 16);
         const uint32_t l_ready = mapa_shared(smem_u32(&ready[slot]), 0);
-        uint8_t* out = slots + slot * SLOT_BYTES;
+        const uint32_t out = smem_u32(slots) + slot * SLOT_BYTES;
         // slots and K-steps are counted through all tiles; a stage is always read by the
         // same two groups, so that none meets a phase of full[] out of turn
         uint32_t n = slot, end = 0;
+        HalfStage<HALF / 8> codes(half, row, thread);
         bool ok = true;
         Tile t;
         for (int64_t i = pid; ok && pair_tile(P, blocks, i, lane, t); i += P.programs) {
@@ -376,20 +327,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 const uint32_t step = n / 2, s = step % S;
                 ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[s], (step / S) & 1, g, SITE_DQ_RAW));
                 if (!ok) break;
-                const uint8_t* w = smem + s * STAGE_BYTES;
-                HalfStage<HALF / 8> codes;
-                codes.load(w, w + W_BYTES, half, row, t.tn / 2, thread);
+                const uint32_t w = smem_u32(smem) + s * STAGE_BYTES;
+                codes.load(w, w + W_BYTES, t.tn / 2);
                 ok = __all_sync(0xFFFFFFFFu, wait_bar(&slot_free[slot], ((n / NS) & 1) ^ 1, g, SITE_DQ_EMPTY));
                 if (!ok) break;
                 tc_fence_after_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[s]);
-                codes.store(taddr, out, t.tn / 2, thread);
+                codes.store(taddr, out, t.tn / 2);
                 tmem_st_wait();
                 fence_proxy_async_smem();
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
+                    mbar_arrive(&empty[s]);
                     if (leader)
                         mbar_arrive(&ready[slot]);
                     else

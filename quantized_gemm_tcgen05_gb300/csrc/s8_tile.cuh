@@ -12,6 +12,16 @@
 
 namespace qg {
 
+// Registers of a thread from here on, for whole groups of four warps.
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Sixteen codes to f16, in order: a byte b + 128 under the exponent of 1024 is the
 // f16 value 1152 + b, and the difference to 1152 is exact.
 __device__ __forceinline__ uint32_t s8_pair_f16(uint32_t biased, uint32_t select) {
@@ -29,35 +39,59 @@ __device__ __forceinline__ void s8_to_f16(const uint4& codes, uint32_t* out) {
     }
 }
 
-// 128 rows of 128 codes (swizzled) to 64 TMEM columns of f16 pairs; a warp has the
-// rows of its 32-lane quarter.  `taddr` includes the quarter's lane.
-__device__ __forceinline__ void s8_weights_to_tmem(const uint8_t* raw, uint32_t taddr, int row) {
-    const uint8_t* base = raw + row * 128;
-    const int x = row & 7;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        uint32_t r[32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) s8_to_f16(*reinterpret_cast<const uint4*>(base + (((4 * half + c) ^ x) << 4)), r + 8 * c);
-        tmem_st_32x32b(taddr + 32 * half, r);
-    }
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t at, const uint32_t* v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
 
-// `rows` rows (a multiple of 8) of 128 codes (swizzled) to two f16 operand tiles of
-// 64 columns (swizzled), rows * 128 bytes each.  128 threads, eight rows of a
-// 16-code chunk to eight threads: neither side has bank conflicts.
-__device__ __forceinline__ void s8_tokens_to_f16(const uint8_t* raw, uint8_t* out, int rows, int thread) {
-    const int r8 = thread & 7;
-    for (int i = thread >> 3; i < rows; i += 16) {  // (eight chunks of rows / 8 octets)
-        const int c = i & 7, row = (i >> 3) * 8 + r8;
-        uint32_t h[8];
-        s8_to_f16(*reinterpret_cast<const uint4*>(raw + row * 128 + ((c ^ r8) << 4)), h);
-        uint8_t* tile = out + (c >> 2) * rows * 128 + row * 128;
-        const int d = 2 * (c & 3);
-        *reinterpret_cast<uint4*>(tile + ((d ^ r8) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(tile + (((d + 1) ^ r8) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+// Half of a stage (64 codes of 128 channels and of `rows` tokens, a multiple of 16, at
+// most 8 * OCTETS; 128-byte rows of 128 codes, swizzled) to f16: the channels' into 32
+// TMEM columns, the tokens' into a swizzled operand tile.  A group of 128 threads: a
+// thread has a channel, and with seven others eight tokens' chunks of 16 codes, so that
+// neither side has bank conflicts.
+template <int OCTETS>
+struct HalfStage {
+    static constexpr int N = (OCTETS + 3) / 4;
+    uint4 w[4], x[N];
+    uint32_t w_at, x_at, out_at;  // offsets in the stage and in the tile
+    int octet;
+    __device__ __forceinline__ HalfStage(int half, int row, int thread) {
+        const int r8 = thread & 7, c = thread >> 3 & 3;
+        octet = thread >> 5;  // ... and every fourth one after it
+        w_at = (uint32_t)(row * 128 + (((4 * half) ^ (row & 7)) << 4));
+        x_at = (uint32_t)((octet * 8 + r8) * 128 + (((4 * half + c) ^ r8) << 4));
+        out_at = (uint32_t)((octet * 8 + r8) * 128 + (((2 * c) ^ r8) << 4));
     }
-}
+    // Shared-memory addresses of a stage's two tiles, and of the tokens' tile.
+    __device__ __forceinline__ void load(uint32_t wraw, uint32_t xraw, int rows) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) w[c] = lds128((wraw + w_at) ^ (c << 4));
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (octet + 4 * k < rows / 8) x[k] = lds128(xraw + x_at + 4096 * k);
+    }
+    __device__ __forceinline__ void store(uint32_t taddr, uint32_t out, int rows) const {
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+            uint32_t r[16];
+            s8_to_f16(w[c], r);
+            s8_to_f16(w[c + 1], r + 8);
+            tmem_st_32x32b(taddr + 8 * c, r);
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (octet + 4 * k < rows / 8) {
+                uint32_t h[8];
+                s8_to_f16(x[k], h);
+                sts128(out + out_at + 4096 * k, h);
+                sts128((out + out_at + 4096 * k) ^ 16u, h + 4);
+            }
+    }
+};
 
 // Four channels n .. n + 3 of one token: the values, and their store.
 struct S8Channels {
