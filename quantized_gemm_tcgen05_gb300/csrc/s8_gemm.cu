@@ -32,20 +32,27 @@ struct Cfg {
     static constexpr int GROUPS = WIDE ? 4 : 2;     // of operand warps
     static constexpr int THREADS = 128 + 32 * SUM_WARPS + 128 * GROUPS;
     static constexpr int COLS = TN / (SUM_WARPS / 4);  // of a warp's sums
-    // a stage is always read by the same groups, so that none meets a phase of full[]
-    // out of turn
-    static constexpr int STAGES = WIDE ? 4 : 3;
-    static constexpr int SLOTS = WIDE ? 4 : 6;
-    static_assert(SLOTS % GROUPS == 0 && STAGES % (GROUPS / 2) == 0, "");
-    static constexpr uint32_t W_BYTES = 128 * 128, X_BYTES = TN * 128, STAGE_BYTES = W_BYTES + X_BYTES;
-    static constexpr uint32_t SLOT_BYTES = TN * 128;
-    static constexpr uint32_t RING_BYTES = STAGES * STAGE_BYTES + SLOTS * SLOT_BYTES;
-    static constexpr uint32_t SUM_BYTES = TN * 512;  // [token][channel], in the ring when it is idle
-    static constexpr uint32_t AUX_BYTES = (2 * STAGES + 2 * SLOTS + 6) * 8 + 16;
-    static constexpr uint32_t SMEM_BYTES = 1024 + RING_BYTES + AUX_BYTES;
+    static constexpr int MAX_SLOTS = WIDE ? 8 : 6;
+    QG_HD static int slots(int tn) { return WIDE ? (tn <= 96 ? 8 : 4) : 6; }
+    static constexpr int MAX_STAGES = 12;
+    static constexpr uint32_t W_BYTES = 128 * 128;
+    static constexpr uint32_t AUX_BYTES = (2 * MAX_STAGES + 2 * MAX_SLOTS + 6) * 8 + 16;
+    static constexpr uint32_t BUDGET = 233472 / CTAS - 1024;  // of a CTA's shared memory
     static constexpr uint32_t TMEM_COLS = WIDE ? 512 : 256;
-    static_assert(2 * TN + 32 * SLOTS <= TMEM_COLS && SMEM_BYTES <= 232448 && CTAS * (SMEM_BYTES + 1024) <= 233472, "");
-    static_assert(SUM_BYTES + (TN + 8) * 512 <= RING_BYTES, "the sums, and the shares received");
+    static_assert(2 * TN + 32 * MAX_SLOTS <= TMEM_COLS && MAX_SLOTS % GROUPS == 0, "");
+    // The ring holds as many stages as there is room for, by the tile's tokens: what
+    // is in flight bounds the kernel (with 4 stages of 26 KB a K-step took 0.55 us,
+    // whatever the other warps did).  A stage is always read by the same groups, so that
+    // none meets a phase of full[] out of turn: their number is a multiple of GROUPS / 2.
+    QG_HD static uint32_t stage_bytes(int tn) { return W_BYTES + (uint32_t)tn * 128u; }
+    QG_HD static uint32_t slot_bytes(int tn) { return (uint32_t)tn * 128u; }
+    QG_HD static int stages(int tn) {
+        const int n = (int)((BUDGET - 1024 - AUX_BYTES - slots(tn) * slot_bytes(tn)) / stage_bytes(tn));
+        return (n < MAX_STAGES ? n : MAX_STAGES) / (GROUPS / 2) * (GROUPS / 2);
+    }
+    QG_HD static uint32_t ring_bytes(int tn) { return (uint32_t)stages(tn) * stage_bytes(tn) + slots(tn) * slot_bytes(tn); }
+    QG_HD static uint32_t sum_bytes(int tn) { return (uint32_t)tn * 512u; }  // [token][channel], in the ring when it is idle
+    static uint32_t smem_bytes(int tn) { return 1024 + ring_bytes(tn) + AUX_BYTES; }
     // registers of a thread: at launch, and by role where they differ
     static constexpr int REGS_LAUNCH = WIDE ? 72 : 64, REGS_SUMS = 104, REGS_OPERANDS = 56, REGS_REST = 56;
     static_assert(!WIDE || 32 * SUM_WARPS * REGS_SUMS + 128 * GROUPS * REGS_OPERANDS + 128 * REGS_REST <= THREADS * REGS_LAUNCH,
@@ -86,16 +93,19 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
     s8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                    const __grid_constant__ S8GemmParams P) {
     using C = Cfg<TN>;
-    constexpr int S = C::STAGES, NS = C::SLOTS, G = C::GROUPS;
+    constexpr int G = C::GROUPS;
+    const int splits = P.splits, tn = P.tile_rows;
+    const int S = C::stages(tn), NS = C::slots(tn);
+    const uint32_t stage_bytes = C::stage_bytes(tn), slot_bytes = C::slot_bytes(tn), ring_bytes = C::ring_bytes(tn);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* slots = smem + S * C::STAGE_BYTES;
+    uint8_t* slots = smem + S * stage_bytes;
     int32_t* sums = reinterpret_cast<int32_t*>(smem);  // once the ring is idle
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::RING_BYTES);
-    uint64_t* empty = full + S;     // a stage's codes have been read (8 warps)
-    uint64_t* ready = empty + S;    // a slot's operands are there (4 warps)
-    uint64_t* slot_free = ready + NS;
-    uint64_t* tfull = slot_free + NS;  // an accumulator buffer is complete
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes);
+    uint64_t* empty = full + C::MAX_STAGES;  // a stage's codes have been read (8 warps)
+    uint64_t* ready = empty + C::MAX_STAGES;  // a K-step's operands are in its two slots (8 warps)
+    uint64_t* slot_free = ready + C::MAX_SLOTS;
+    uint64_t* tfull = slot_free + C::MAX_SLOTS;  // an accumulator buffer is complete
     uint64_t* tempty = tfull + 2;      // ... and in the sums
     uint64_t* idle = tempty + 2;       // every CTA of the cluster is through with its ring
     uint64_t* part = idle + 1;         // the sums' shares have arrived
@@ -104,14 +114,13 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
     volatile uint32_t* warning = tmem_slot + 2;  // a CTA of the cluster has given up
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int splits = P.splits, tn = P.tile_rows;
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 8);
         }
         for (int s = 0; s < NS; ++s) {
-            mbar_init(&ready[s], 4);
+            mbar_init(&ready[s], 8);
             mbar_init(&slot_free[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -167,15 +176,14 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
     if (warp < 4) {
         if constexpr (C::WIDE) regs_down<C::REGS_REST>();
         if (live && warp == 0) {
-            const uint32_t bytes = C::W_BYTES + (uint32_t)tn * 128u;
             int s = 0;
             uint32_t ph = 1;
             for (int i = 0; i < nk; ++i) {
                 ok = __all_sync(0xFFFFFFFFu, wait_bar(&empty[s], ph, g, SITE_PRODUCER_EMPTY));
                 if (!ok) break;
-                uint8_t* w = smem + (uint32_t)s * C::STAGE_BYTES;
+                uint8_t* w = smem + (uint32_t)s * stage_bytes;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(&full[s], bytes);
+                    mbar_arrive_expect_tx(&full[s], stage_bytes);
                     if (P.b3d)
                         tma_load_3d(w, &tmB, &full[s], (k0 + i) * S8_KSTEP, (int32_t)n0, expert);
                     else
@@ -196,20 +204,24 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
                 const uint32_t b = chunk & 1, d = tmem + TN * b;
                 const int n = nslots - j0 < SLOT_CHUNK ? nslots - j0 : SLOT_CHUNK;
                 ok = __all_sync(0xFFFFFFFFu, wait_bar(&tempty[b], ((chunk >> 1) & 1) ^ 1, g, SITE_MMA_TMEM_EMPTY));
-                for (int j = 0; ok && j < n; ++j) {
-                    ok = __all_sync(0xFFFFFFFFu, wait_bar(&ready[slot], ph, g, SITE_MMA_OPERAND));
+                // two slots at a time: waiting and issuing take this warp some 500 cycles a turn
+                for (int j = 0; ok && j < n; j += 2) {
+                    ok = __all_sync(0xFFFFFFFFu, wait_bar(&ready[slot / 2], ph, g, SITE_MMA_OPERAND));
                     if (!ok) break;
                     tc_fence_after_sync();
-                    const uint64_t xd = xd0 + (uint64_t)((uint32_t)slot * (C::SLOT_BYTES / 16));
+                    const uint64_t xd = xd0 + (uint64_t)((uint32_t)slot * (slot_bytes / 16));
                     const uint32_t wa = tmem_w + 32 * slot;
                     if (elect_one()) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) umma_f16_ts(d, wa + 8 * q, xd + 2 * q, P.idesc, q ? 1u : (uint32_t)j);
                         umma_commit(&slot_free[slot]);
-                        if (j == n - 1) umma_commit(&tfull[b]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) umma_f16_ts(d, wa + 32 + 8 * q, xd + slot_bytes / 16 + 2 * q, P.idesc, 1u);
+                        umma_commit(&slot_free[slot + 1]);
+                        if (j == n - 2) umma_commit(&tfull[b]);
                     }
                     __syncwarp();
-                    if (++slot == NS) {
+                    if ((slot += 2) == NS) {
                         slot = 0;
                         ph ^= 1;
                     }
@@ -249,24 +261,35 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
         const int group = (warp - 4 - C::SUM_WARPS) / 4, half = group & 1;
         const uint32_t taddr = tmem_w + ((uint32_t)(warp % 4 * 32) << 16);
         HalfStage<TN / 8> codes(half, warp % 4 * 32 + lane, threadIdx.x & 127);
+        int s = group / 2, slot = group;
+        uint32_t ph = 0, sph = 1;
         for (int n = group; ok && n < nslots; n += G) {
-            const int step = n / 2, s = step % S, slot = n % NS;
-            ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[s], (step / S) & 1, g, SITE_DQ_RAW));
+            ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[s], ph, g, SITE_DQ_RAW));
             if (!ok) break;
-            const uint32_t w = smem_u32(smem) + (uint32_t)s * C::STAGE_BYTES;
+            const uint32_t w = smem_u32(smem) + (uint32_t)s * stage_bytes;
             codes.load(w, w + C::W_BYTES, tn);
-            ok = __all_sync(0xFFFFFFFFu, wait_bar(&slot_free[slot], ((n / NS) & 1) ^ 1, g, SITE_DQ_EMPTY));
+            ok = __all_sync(0xFFFFFFFFu, wait_bar(&slot_free[slot], sph, g, SITE_DQ_EMPTY));
             if (!ok) break;
             tc_fence_after_sync();
             __syncwarp();
-            codes.store(taddr + 32 * slot, smem_u32(slots) + slot * C::SLOT_BYTES, tn);
+            codes.store(taddr + 32 * slot, smem_u32(slots) + slot * slot_bytes, tn);
             tmem_st_wait();
             fence_proxy_async_smem();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&empty[s]);
-                mbar_arrive(&ready[slot]);
+                mbar_arrive(&ready[slot / 2]);
+            }
+            s += G / 2;
+            if (s >= S) {
+                s -= S;
+                ph ^= 1;
+            }
+            slot += G;
+            if (slot >= NS) {
+                slot -= NS;
+                sph ^= 1;
             }
         }
     }
@@ -289,7 +312,7 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
     }
     if (splits > 1) fence_proxy_async_smem();  // the sums are visible to the bulk copies
     __syncthreads();
-    uint8_t* recv = smem + C::SUM_BYTES;
+    uint8_t* recv = smem + C::sum_bytes(tn);
     // every thread keeps to four channels
     const int64_t n = n0 + 4 * lane;
     EpiArith ar = epi_arith(P.epi);
@@ -347,14 +370,14 @@ cudaError_t launch_t(const S8Maps& m, const S8GemmParams& p, int grid, cudaStrea
         e = cudaFuncGetAttributes(&a, s8_gemm_kernel<TN>);
         if (e != cudaSuccess) return e;
         if (Cfg<TN>::WIDE && a.numRegs != Cfg<TN>::REGS_LAUNCH) return cudaErrorInvalidConfiguration;
-        e = cudaFuncSetAttribute(s8_gemm_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<TN>::SMEM_BYTES);
+        e = cudaFuncSetAttribute(s8_gemm_kernel<TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<TN>::BUDGET);
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(Cfg<TN>::THREADS);
-    cfg.dynamicSmemBytes = Cfg<TN>::SMEM_BYTES;
+    cfg.dynamicSmemBytes = Cfg<TN>::smem_bytes(p.tile_rows);
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     int n = 0;

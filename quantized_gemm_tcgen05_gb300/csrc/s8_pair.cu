@@ -130,8 +130,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     uint8_t* slots = smem + S * STAGE_BYTES;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + RING_BYTES + EPI_BYTES);
     uint64_t* empty = full + S;        // a stage's codes have been read (8 warps)
-    uint64_t* ready = empty + S;       // leader: both CTAs' operands are in the slot (8 warps)
-    uint64_t* slot_free = ready + NS;
+    uint64_t* ready = empty + S;       // leader: both CTAs' operands of a K-step are in its two slots (16 warps)
+    uint64_t* slot_free = ready + NS / 2;
     uint64_t* tfull = slot_free + NS;
     uint64_t* tempty = tfull + 2;      // leader: a buffer is in both CTAs' sums (16 warps)
     uint64_t* done = tempty + 2;
@@ -146,10 +146,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 8);
         }
-        for (int s = 0; s < NS; ++s) {
-            mbar_init(&ready[s], 8);
-            mbar_init(&slot_free[s], 1);
-        }
+        for (int s = 0; s < NS / 2; ++s) mbar_init(&ready[s], 16);
+        for (int s = 0; s < NS; ++s) mbar_init(&slot_free[s], 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], 16);
@@ -226,10 +224,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     const uint32_t b = chunk & 1, d = tmem + TN * b;
                     const int n = nslots - j0 < SLOT_CHUNK ? nslots - j0 : SLOT_CHUNK;
                     ok = __all_sync(0xFFFFFFFFu, wait_bar(&tempty[b], ((chunk >> 1) & 1) ^ 1, g, SITE_MMA_TMEM_EMPTY));
-                    for (int j = 0; ok && j < n; ++j) {
+                    // Two slots at a time: waiting and issuing take this warp some 500 cycles
+                    // a turn, eight MMAs 768.
+                    for (int j = 0; ok && j < n; j += 2) {
                         // (this thread reads nothing that the other CTA wrote: its tensor core
                         // does, there, so no acquire at cluster scope is needed)
-                        ok = __all_sync(0xFFFFFFFFu, wait_bar(&ready[slot], ph, g, SITE_MMA_OPERAND));
+                        ok = __all_sync(0xFFFFFFFFu, wait_bar(&ready[slot / 2], ph, g, SITE_MMA_OPERAND));
                         if (!ok) break;
                         tc_fence_after_sync();
                         const uint64_t xd = xd0 + (uint64_t)((uint32_t)slot * (SLOT_BYTES / 16));
@@ -238,11 +238,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
                             for (int q = 0; q < 4; ++q) umma_f16_ts_pair(d, wa + 8 * q, xd + 2 * q, idesc, q ? 1u : (uint32_t)j);
                             umma_commit_pair_mc(&slot_free[slot], 0x3);
-                            if (j == n - 1) umma_commit_pair_mc(&tfull[b], 0x3);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) umma_f16_ts_pair(d, wa + 32 + 8 * q, xd + SLOT_BYTES / 16 + 2 * q, idesc, 1u);
+                            umma_commit_pair_mc(&slot_free[slot + 1], 0x3);
+                            if (j == n - 2) umma_commit_pair_mc(&tfull[b], 0x3);
                         }
                         __syncwarp();
                         issued = true;
-                        if (++slot == NS) {
+                        if ((slot += 2) == NS) {
                             slot = 0;
                             ph ^= 1;
                         }
@@ -313,7 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         regs_down<REGS_OPERANDS>();
         const int slot = (warp - 12) / 4, half = slot & 1, thread = threadIdx.x & 127, row = warp % 4 * 32 + lane;
         const uint32_t taddr = tmem_w + 32 * slot + ((uint32_t)(warp % 4 * 32) << 16);
-        const uint32_t l_ready = mapa_shared(smem_u32(&ready[slot]), 0);
+        const uint32_t l_ready = mapa_shared(smem_u32(&ready[slot / 2]), 0);
         const uint32_t out = smem_u32(slots) + slot * SLOT_BYTES;
         // slots and K-steps are counted through all tiles; a stage is always read by the
         // same two groups, so that none meets a phase of full[] out of turn
@@ -341,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 if (lane == 0) {
                     mbar_arrive(&empty[s]);
                     if (leader)
-                        mbar_arrive(&ready[slot]);
+                        mbar_arrive(&ready[slot / 2]);
                     else
                         mbar_arrive_remote_cta(l_ready);
                 }
