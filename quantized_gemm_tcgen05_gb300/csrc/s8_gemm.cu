@@ -36,7 +36,7 @@ struct Cfg {
     QG_HD static int slots(int tn) { return WIDE ? (tn <= 96 ? 8 : 4) : 6; }
     static constexpr int MAX_STAGES = 12;
     static constexpr uint32_t W_BYTES = 128 * 128;
-    static constexpr uint32_t AUX_BYTES = (2 * MAX_STAGES + 2 * MAX_SLOTS + 6) * 8 + 16;
+    static constexpr uint32_t AUX_BYTES = (2 * MAX_STAGES + 2 * MAX_SLOTS + 6) * 8 + 16 + (256 + TN) * 4;
     static constexpr uint32_t BUDGET = 233472 / CTAS - 1024;  // of a CTA's shared memory
     static constexpr uint32_t TMEM_COLS = WIDE ? 512 : 256;
     static_assert(2 * TN + 32 * MAX_SLOTS <= TMEM_COLS && MAX_SLOTS % GROUPS == 0, "");
@@ -112,6 +112,10 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(part + 1);
     volatile uint32_t* abort_flag = tmem_slot + 1;
     volatile uint32_t* warning = tmem_slot + 2;  // a CTA of the cluster has given up
+    // what the epilogue multiplies and adds: fetched while the main loop runs
+    float* channel_factor = reinterpret_cast<float*>(tmem_slot + 4);
+    float* channel_bias = channel_factor + 128;
+    float* token_factor = channel_bias + 128;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     if (threadIdx.x == 0) {
@@ -228,6 +232,12 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
                 }
             }
         } else if (live && warp > 1) {
+            const EpiArith ar = epi_arith(P.epi);
+            for (int i = threadIdx.x - 64; i < 128; i += 64) {
+                channel_factor[i] = n0 + i < P.epi.N ? s8_channel_factor(P, expert, n0 + i) : 0.0f;
+                channel_bias[i] = bias_at(ar, n0 + i);
+            }
+            for (int i = threadIdx.x - 64; i < rows; i += 64) token_factor[i] = s8_token_factor(P, row0 + i);
             if (P.epi.beta != 0.0f && n0 < P.epi.N)
                 for (int r = threadIdx.x - 64; r < rows; r += 64) mx_prefetch_c(P.epi, row0 + r, n0, P.epi.N - n0 < 128 ? P.epi.N - n0 : 128);
         }
@@ -317,18 +327,22 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
     const int64_t n = n0 + 4 * lane;
     EpiArith ar = epi_arith(P.epi);
     ar.alpha = 1.0f;
+    S8Channels ch;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        ch.scale[j] = channel_factor[4 * lane + j];
+        ch.bias[j] = channel_bias[4 * lane + j];
+    }
     if (splits == 1) {
-        if (all_ok) {
-            const S8Channels ch = s8_channels(P, ar, expert, n);
-            for (int m = warp; m < rows; m += C::THREADS / 32) s8_finish4(P, ar, ch, row0 + m, n, reinterpret_cast<const int4*>(sums + m * 128)[lane]);
-        }
+        if (all_ok)
+            for (int m = warp; m < rows; m += C::THREADS / 32)
+                s8_finish4(P, ar, ch, token_factor[m], row0 + m, n, reinterpret_cast<const int4*>(sums + m * 128)[lane]);
     } else if (live) {
         // (whether this CTA's part is right or not: the others wait for it)
         SumsLink link{idle, part, warning, smem_u32(sums), smem_u32(recv), splits, rank, rows, (rows + splits - 1) / splits, g};
         ok = mx_exchange(link, splits, threadIdx.x == 0);
         all_ok = __syncthreads_and(all_ok && ok ? 1 : 0) != 0;
         if (all_ok) {
-            const S8Channels ch = s8_channels(P, ar, expert, n);
             const int count = link.count(rank), first = link.first(rank);
             for (int m = warp; m < count; m += C::THREADS / 32) {
                 int4 sum = make_int4(0, 0, 0, 0);
@@ -339,7 +353,7 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
                     sum.z += p.z;
                     sum.w += p.w;
                 }
-                s8_finish4(P, ar, ch, row0 + first + m, n, sum);
+                s8_finish4(P, ar, ch, token_factor[first + m], row0 + first + m, n, sum);
             }
         }
     }

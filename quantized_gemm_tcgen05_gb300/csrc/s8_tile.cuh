@@ -93,7 +93,7 @@ struct HalfStage {
     }
 };
 
-// Four channels n .. n + 3 of one token: the values, and their store.
+// Four channels n .. n + 3: their factors and biases.
 struct S8Channels {
     float scale[4], bias[4];
 };
@@ -106,11 +106,12 @@ __device__ __forceinline__ S8Channels s8_channels(const S8GemmParams& P, const E
     }
     return c;
 }
-__device__ __forceinline__ void s8_finish4(const S8GemmParams& P, const EpiArith& ar, const S8Channels& ch, int64_t m, int64_t n, const int4& sum) {
+// Their values of token m, whose factor is `token`, and their store.
+__device__ __forceinline__ void s8_finish4(const S8GemmParams& P, const EpiArith& ar, const S8Channels& ch, float token, int64_t m, int64_t n,
+                                           const int4& sum) {
     const EpiParams& e = P.epi;
     const int have = e.N - n < 4 ? (int)(e.N - n) : 4;
     if (have <= 0 || !mx_block_in_bounds(e, m, 1, n, have)) return;
-    const float token = s8_token_factor(P, m);
     const int32_t s[4] = {sum.x, sum.y, sum.z, sum.w};
     float v[4], c[4] = {0.0f, 0.0f, 0.0f, 0.0f}, x[4];
 #pragma unroll
