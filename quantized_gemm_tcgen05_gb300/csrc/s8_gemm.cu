@@ -2,9 +2,9 @@
 // cluster.
 //
 // A stage holds one K-step: 128 codes (one 128-byte swizzle row) of 128 channels
-// and of the tile's tokens.  Groups of four warps take the stages' halves in turn and
-// turn their codes into f16 operands: the channels' into a slot of TMEM, the tokens' into
-// one of shared memory.  The accumulator has two buffers of TN columns; after 16
+// and of the tile's tokens.  Groups of four warps take the stages in turn, or their
+// halves, and turn their codes into f16 operands: the channels' into a slot of TMEM, the
+// tokens' into one of shared memory.  The accumulator has two buffers of TN columns; after 16
 // slots (1024 products) other warps add the full one to 32-bit sums in their registers
 // while the MMAs go on in the other.
 //
@@ -29,26 +29,27 @@ struct Cfg {
     static constexpr bool WIDE = TN > 32;
     static constexpr int CTAS = WIDE ? 1 : 2;       // per SM
     static constexpr int SUM_WARPS = WIDE ? 8 : 4;
-    static constexpr int GROUPS = WIDE ? 4 : 2;     // of operand warps
+    static constexpr int GROUPS = WIDE ? 4 : 2;     // of operand warps: two take a stage's halves, or one both
+    static constexpr int HALVES = WIDE ? 1 : 2;
     static constexpr int THREADS = 128 + 32 * SUM_WARPS + 128 * GROUPS;
     static constexpr int COLS = TN / (SUM_WARPS / 4);  // of a warp's sums
     static constexpr int MAX_SLOTS = WIDE ? 8 : 6;
     QG_HD static int slots(int tn) { return WIDE ? (tn <= 96 ? 8 : 4) : 6; }
     static constexpr int MAX_STAGES = 12;
     static constexpr uint32_t W_BYTES = 128 * 128;
-    static constexpr uint32_t AUX_BYTES = (2 * MAX_STAGES + 2 * MAX_SLOTS + 6) * 8 + 16 + (256 + TN) * 4;
+    static constexpr uint32_t AUX_BYTES = (2 * MAX_STAGES + MAX_SLOTS + 6) * 8 + 16 + (256 + TN) * 4;
     static constexpr uint32_t BUDGET = 233472 / CTAS - 1024;  // of a CTA's shared memory
     static constexpr uint32_t TMEM_COLS = WIDE ? 512 : 256;
     static_assert(2 * TN + 32 * MAX_SLOTS <= TMEM_COLS && MAX_SLOTS % GROUPS == 0, "");
     // The ring holds as many stages as there is room for, by the tile's tokens: what
     // is in flight bounds the kernel (with 4 stages of 26 KB a K-step took 0.55 us,
-    // whatever the other warps did).  A stage is always read by the same groups, so that
-    // none meets a phase of full[] out of turn: their number is a multiple of GROUPS / 2.
+    // whatever the other warps did).  Their number is even: then a stage is always read by
+    // the same groups, and none meets a phase of full[] out of turn.
     QG_HD static uint32_t stage_bytes(int tn) { return W_BYTES + (uint32_t)tn * 128u; }
     QG_HD static uint32_t slot_bytes(int tn) { return (uint32_t)tn * 128u; }
     QG_HD static int stages(int tn) {
         const int n = (int)((BUDGET - 1024 - AUX_BYTES - slots(tn) * slot_bytes(tn)) / stage_bytes(tn));
-        return (n < MAX_STAGES ? n : MAX_STAGES) / (GROUPS / 2) * (GROUPS / 2);
+        return (n < MAX_STAGES ? n : MAX_STAGES) / 2 * 2;
     }
     QG_HD static uint32_t ring_bytes(int tn) { return (uint32_t)stages(tn) * stage_bytes(tn) + slots(tn) * slot_bytes(tn); }
     QG_HD static uint32_t sum_bytes(int tn) { return (uint32_t)tn * 512u; }  // [token][channel], in the ring when it is idle
@@ -102,10 +103,10 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
     uint8_t* slots = smem + S * stage_bytes;
     int32_t* sums = reinterpret_cast<int32_t*>(smem);  // once the ring is idle
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + ring_bytes);
-    uint64_t* empty = full + C::MAX_STAGES;  // a stage's codes have been read (8 warps)
-    uint64_t* ready = empty + C::MAX_STAGES;  // a K-step's operands are in its two slots (8 warps)
-    uint64_t* slot_free = ready + C::MAX_SLOTS;
-    uint64_t* tfull = slot_free + C::MAX_SLOTS;  // an accumulator buffer is complete
+    uint64_t* empty = full + C::MAX_STAGES;  // a stage's codes have been read
+    uint64_t* ready = empty + C::MAX_STAGES;  // a K-step's operands are in its two slots
+    uint64_t* slot_free = ready + C::MAX_SLOTS / 2;
+    uint64_t* tfull = slot_free + C::MAX_SLOTS / 2;  // an accumulator buffer is complete
     uint64_t* tempty = tfull + 2;      // ... and in the sums
     uint64_t* idle = tempty + 2;       // every CTA of the cluster is through with its ring
     uint64_t* part = idle + 1;         // the sums' shares have arrived
@@ -121,10 +122,10 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 8);
+            mbar_init(&empty[s], 8 / C::HALVES);
         }
-        for (int s = 0; s < NS; ++s) {
-            mbar_init(&ready[s], 8);
+        for (int s = 0; s < NS / 2; ++s) {
+            mbar_init(&ready[s], 8 / C::HALVES);
             mbar_init(&slot_free[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -202,31 +203,29 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
             }
         } else if (live && warp == 1) {
             const uint64_t xd0 = make_sw128_kmajor_desc(smem_u32(slots));
-            int slot = 0;
+            int pair = 0;  // of slots
             uint32_t ph = 0, chunk = 0;
             for (int j0 = 0; ok && j0 < nslots; j0 += SLOT_CHUNK, ++chunk) {
                 const uint32_t b = chunk & 1, d = tmem + TN * b;
                 const int n = nslots - j0 < SLOT_CHUNK ? nslots - j0 : SLOT_CHUNK;
                 ok = __all_sync(0xFFFFFFFFu, wait_bar(&tempty[b], ((chunk >> 1) & 1) ^ 1, g, SITE_MMA_TMEM_EMPTY));
-                // two slots at a time: waiting and issuing take this warp some 500 cycles a turn
                 for (int j = 0; ok && j < n; j += 2) {
-                    ok = __all_sync(0xFFFFFFFFu, wait_bar(&ready[slot / 2], ph, g, SITE_MMA_OPERAND));
+                    ok = __all_sync(0xFFFFFFFFu, wait_bar(&ready[pair], ph, g, SITE_MMA_OPERAND));
                     if (!ok) break;
                     tc_fence_after_sync();
-                    const uint64_t xd = xd0 + (uint64_t)((uint32_t)slot * (slot_bytes / 16));
-                    const uint32_t wa = tmem_w + 32 * slot;
+                    const uint64_t xd = xd0 + (uint64_t)((uint32_t)pair * (slot_bytes / 8));
+                    const uint32_t wa = tmem_w + 64 * pair;
                     if (elect_one()) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) umma_f16_ts(d, wa + 8 * q, xd + 2 * q, P.idesc, q ? 1u : (uint32_t)j);
-                        umma_commit(&slot_free[slot]);
 #pragma unroll
                         for (int q = 0; q < 4; ++q) umma_f16_ts(d, wa + 32 + 8 * q, xd + slot_bytes / 16 + 2 * q, P.idesc, 1u);
-                        umma_commit(&slot_free[slot + 1]);
+                        umma_commit(&slot_free[pair]);
                         if (j == n - 2) umma_commit(&tfull[b]);
                     }
                     __syncwarp();
-                    if ((slot += 2) == NS) {
-                        slot = 0;
+                    if (++pair == NS / 2) {
+                        pair = 0;
                         ph ^= 1;
                     }
                 }
@@ -268,37 +267,39 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
         }
     } else {
         if constexpr (C::WIDE) regs_down<C::REGS_OPERANDS>();
-        const int group = (warp - 4 - C::SUM_WARPS) / 4, half = group & 1;
-        const uint32_t taddr = tmem_w + ((uint32_t)(warp % 4 * 32) << 16);
-        HalfStage<TN / 8> codes(half, warp % 4 * 32 + lane, threadIdx.x & 127);
-        int s = group / 2, slot = group;
+        const int group = (warp - 4 - C::SUM_WARPS) / 4, half = C::HALVES == 1 ? group & 1 : 0, first = C::HALVES == 1 ? group / 2 : group;
+        const uint32_t taddr = tmem_w + 32 * half + ((uint32_t)(warp % 4 * 32) << 16), out = smem_u32(slots) + half * slot_bytes;
+        const HalfStage<TN / 8> codes(half, warp % 4 * 32 + lane, threadIdx.x & 127);
+        // (The phase of slot_free before the one waited for has ended: this group has seen the
+        // MMAs of K-step i - 2 - NS / 2 or later end.)
+        int s = first, pair = first;
         uint32_t ph = 0, sph = 1;
-        for (int n = group; ok && n < nslots; n += G) {
+        for (int i = first; ok && i < nk; i += 2) {
             ok = __all_sync(0xFFFFFFFFu, wait_bar(&full[s], ph, g, SITE_DQ_RAW));
             if (!ok) break;
-            const uint32_t w = smem_u32(smem) + (uint32_t)s * stage_bytes;
-            codes.load(w, w + C::W_BYTES, tn);
-            ok = __all_sync(0xFFFFFFFFu, wait_bar(&slot_free[slot], sph, g, SITE_DQ_EMPTY));
+            ok = __all_sync(0xFFFFFFFFu, wait_bar(&slot_free[pair], sph, g, SITE_DQ_EMPTY));
             if (!ok) break;
             tc_fence_after_sync();
             __syncwarp();
-            codes.store(taddr + 32 * slot, smem_u32(slots) + slot * slot_bytes, tn);
+            const uint32_t w = smem_u32(smem) + (uint32_t)s * stage_bytes, ta = taddr + 64 * pair, to = out + 2 * pair * slot_bytes;
+#pragma unroll
+            for (int h = 0; h < C::HALVES; ++h) codes.convert(w, w + C::W_BYTES, ta + 32 * h, to + h * slot_bytes, tn, 64u * h);
             tmem_st_wait();
             fence_proxy_async_smem();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(&empty[s]);
-                mbar_arrive(&ready[slot / 2]);
+                mbar_arrive(&ready[pair]);
             }
-            s += G / 2;
+            s += 2;
             if (s >= S) {
                 s -= S;
                 ph ^= 1;
             }
-            slot += G;
-            if (slot >= NS) {
-                slot -= NS;
+            pair += 2;
+            if (pair >= NS / 2) {
+                pair -= NS / 2;
                 sph ^= 1;
             }
         }

@@ -53,6 +53,9 @@ __device__ __forceinline__ void sts128(uint32_t at, const uint32_t* v) {
 // TMEM columns, the tokens' into a swizzled operand tile.  A group of 128 threads: a
 // thread has a channel, and with seven others eight tokens' chunks of 16 codes, so that
 // neither side has bank conflicts.
+// Codes are loaded just before their conversion, or all of them early (load), which takes
+// registers: the CTA-pair kernel gains 4 us of 114 by it (4096^3), the one-tile kernel
+// loses 10% where they spill.
 template <int OCTETS>
 struct HalfStage {
     static constexpr int N = (OCTETS + 3) / 4;
@@ -84,12 +87,35 @@ struct HalfStage {
         }
 #pragma unroll
         for (int k = 0; k < N; ++k)
-            if (octet + 4 * k < rows / 8) {
-                uint32_t h[8];
-                s8_to_f16(x[k], h);
-                sts128(out + out_at + 4096 * k, h);
-                sts128((out + out_at + 4096 * k) ^ 16u, h + 4);
-            }
+            if (octet + 4 * k < rows / 8) put(x[k], out + out_at + 4096 * k);
+    }
+    // Both, piece by piece; flip: 64 for the stage's other half.
+    __device__ __forceinline__ void convert(uint32_t wraw, uint32_t xraw, uint32_t taddr, uint32_t out, int rows, uint32_t flip) const {
+        uint4 v[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = lds128((wraw + w_at) ^ (flip | c << 4));
+#pragma unroll
+        for (int c = 0; c < 4; c += 2) {
+            uint32_t r[16];
+            s8_to_f16(v[c], r);
+            s8_to_f16(v[c + 1], r + 8);
+            tmem_st_32x32b(taddr + 8 * c, r);
+        }
+#pragma unroll
+        for (int k = 0; k < N; k += 2) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (k + q < N && octet + 4 * (k + q) < rows / 8) v[q] = lds128((xraw + x_at + 4096 * (k + q)) ^ flip);
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (k + q < N && octet + 4 * (k + q) < rows / 8) put(v[q], out + out_at + 4096 * (k + q));
+        }
+    }
+    static __device__ __forceinline__ void put(const uint4& codes, uint32_t to) {
+        uint32_t h[8];
+        s8_to_f16(codes, h);
+        sts128(to, h);
+        sts128(to ^ 16u, h + 4);
     }
 };
 
