@@ -3,6 +3,7 @@
 #include "gemm_s8.h"
 
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdio.h>
 #include <stdlib.h>
 #include <string.h>
@@ -144,25 +145,67 @@ bool forced_kernel(S8Choice* c) {
     return true;
 }
 
-S8Choice choose(const S8GemmParams& p, int sm_count, int clusters, int forced_split) {
-    const int64_t each = rows_each(p);
-    S8Choice c{each <= 4 ? S8_GEMV : S8_TILE, each <= 32 ? 32 : 128, 0, 1};
-    if (each > 256 && !forced_split && clusters > 0) c.kernel = S8_PAIR;
-    forced_kernel(&c);
-    if (c.kernel == S8_PAIR && clusters < 1) c.kernel = S8_TILE;
+// Estimated time of a choice, microseconds.  Measured on GB300 (152 SMs), back-to-back
+// launches, cold operands:
+//   one tile, up to 32 tokens    5 us for set-up, first data and epilogue; a K-step of
+//     128 0.40 us, 0.50 where two CTAs share an SM, 0.08 more with 32 tokens than with 16;
+//     K slices 3 us (8x4096x4096 9.2 us in eight, 16x4096x14336 16.0 in eight, 22 in four,
+//     256x4096x4096 24.7, 512x4096x4096 47.8)
+//   one tile, up to 128 tokens   7.5 us; a K-step 0.36 us and 0.0025 a token
+//     (77x11002x4104 26.6, 128x14336x4096 28.8, 256x4096x4096 22.2 in two slices)
+//   CTA pair                     9 us once; a K-step of a wave of tiles 0.51 us with 96
+//     tokens, 0.53 with 128, 0.61 with 160, 0.65 with 192 (4096^3: 168, 129, 126, 114 us)
+double estimate(const S8GemmParams& p, int sm_count, int clusters, const S8Choice& c) {
+    const double n = (double)p.epi.N, k = (double)p.K;
+    const int64_t steps = ceil_div(p.K, S8_KSTEP);
+    // tiles of experts: half a tile each is expected to be cut off
+    const double rows = (double)p.epi.M / c.rows + (p.num_experts ? 0.5 * (double)std::min<int64_t>(p.num_experts, p.epi.M) : 0.0);
+    const double tokens = p.num_experts ? rows : (double)ceil_div(p.epi.M, c.rows);
+    const double memory = 3.0 + n * k * (double)std::max<int64_t>(1, std::min<int64_t>(p.num_experts, p.epi.M)) / 6.0e6;
     if (c.kernel == S8_PAIR) {
-        c.rows = (int)std::min<int64_t>(S8_PAIR_TOKENS, ceil_div(each, 32) * 32);
-        return c;
+        const double waves = ceil(tokens * (double)ceil_div(p.epi.N, 256) / clusters);
+        const double step = c.rows <= 96 ? 0.51 : c.rows <= 128 ? 0.53 : c.rows <= 160 ? 0.61 : 0.65;
+        return std::max(memory, 9.0 + waves * (double)steps * step);
     }
-    if (c.kernel == S8_GEMV) {
-        c.rows = each <= 1 ? 1 : each <= 2 ? 2 : each <= 4 ? 4 : 8;
-        return c;
+    const double ctas = tokens * (double)ceil_div(p.epi.N, 128) * c.splits;
+    const double cut = c.splits > 1 ? 3.0 : 0.0, each = (double)ceil_div(steps, c.splits);
+    if (c.width == 32) {
+        const double step = (ctas > sm_count ? 0.50 : 0.40) + (c.rows > 16 ? 0.08 : 0.0);
+        return std::max(memory, ceil(ctas / (2.0 * sm_count)) * (5.0 + each * step) + cut);
     }
-    c.rows = (int)(ceil_div(ceil_div(each, ceil_div(each, c.width)), 16) * 16);
-    const int64_t tiles = token_tiles(p, c.rows) * ceil_div(p.epi.N, 128), steps = ceil_div(p.K, S8_KSTEP);
-    const int64_t slots = (int64_t)sm_count * (c.width == 32 ? 2 : 1);
-    while (c.splits < 8 && 2 * c.splits <= steps && (forced_split ? c.splits < forced_split : tiles * c.splits * 2 <= slots)) c.splits *= 2;
-    return c;
+    return std::max(memory, ceil(ctas / sm_count) * (7.5 + each * (0.36 + 0.0025 * c.rows)) + cut);
+}
+
+S8Choice choose(const S8GemmParams& p, int sm_count, int clusters, int forced_split) {
+    const int64_t each = rows_each(p), steps = ceil_div(p.K, S8_KSTEP);
+    S8Choice forced{S8_GEMV, 0, 0, 1}, best{S8_TILE, 32, 16, 1};
+    const bool pinned = forced_kernel(&forced);
+    if (pinned ? forced.kernel == S8_GEMV : each <= 1 && !forced_split) {
+        best.kernel = S8_GEMV;  // 1x4096x14336 13.3 us, in tiles 15.4
+        best.rows = each <= 1 ? 1 : each <= 2 ? 2 : each <= 4 ? 4 : 8;
+        return best;
+    }
+    double best_us = -1.0;
+    auto consider = [&](const S8Choice& c) {
+        const double us = estimate(p, sm_count, clusters, c);
+        // a forced number of slices goes before time, as far as K has steps for it
+        const bool better = forced_split && c.splits != best.splits ? c.splits > best.splits : us < best_us;
+        if (best_us < 0 || better) {
+            best_us = us;
+            best = c;
+        }
+    };
+    for (int width : {32, 128}) {
+        if (pinned && (forced.kernel != S8_TILE || forced.width != width)) continue;
+        const int rows = (int)(ceil_div(ceil_div(each, ceil_div(each, width)), 16) * 16);
+        for (int splits : {1, 2, 4, 8}) {
+            if (splits > steps || (forced_split && splits > forced_split)) continue;
+            consider({S8_TILE, width, rows, splits});
+        }
+    }
+    if (clusters > 0 && (pinned ? forced.kernel == S8_PAIR : !forced_split && each > 16))
+        for (int rows : {96, 128, 160, 192}) consider({S8_PAIR, 0, (int)std::min<int64_t>(rows, ceil_div(each, 32) * 32), 1});
+    return best;
 }
 
 // Tensor map over int8 codes: [matrices][lines][codes of a line], boxes of one
