@@ -70,8 +70,8 @@ __device__ __forceinline__ void s8_store16(uint8_t* y, int c0, int cols, int yve
 
 // A block a row: NC chunks of 16 values a thread stay in registers between the
 // maximum and the codes.
-template <typename T, int NC>
-__global__ void __launch_bounds__(1024) row_quantize_kernel(const __grid_constant__ RowsParams p) {
+template <typename T, int NC, bool ALIGNED, int THREADS>
+__global__ void __launch_bounds__(THREADS) row_quantize_kernel(const __grid_constant__ RowsParams p) {
     __shared__ float red[32];
     griddep_launch_dependents();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(1024) row_quantize_kernel(const __grid_constan
     const T* x = static_cast<const T*>(p.X) + blockIdx.y * p.x_bstride + r * p.ldx;
     Raw16<T> raw[NC];
 #pragma unroll
-    for (int i = 0; i < NC; ++i) raw[i] = mx_load16<false>(x, (i * (int)blockDim.x + (int)threadIdx.x) * 16, cols, p.vec, p.X, p.x_end);
+    for (int i = 0; i < NC; ++i) raw[i] = mx_load16<ALIGNED>(x, (i * (int)blockDim.x + (int)threadIdx.x) * 16, cols, p.vec, p.X, p.x_end);
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < NC; ++i) amax = max_nan(amax, mx_amax16(mx_values<T>(raw[i])));
@@ -162,9 +162,15 @@ cudaError_t quantize_t(const RowsParams& p, cudaStream_t st) {
     const int64_t chunks = ceil_div(p.cols, 16);
     dim3 grid((unsigned)p.rows, (unsigned)p.num);
     auto threads = [&](int nc) { return (int)(ceil_div(ceil_div(chunks, nc), 32) * 32); };
-    if (chunks <= 256) return launch_pdl3(row_quantize_kernel<T, 1>, grid, threads(1), st, p);
-    if (chunks <= 2048) return launch_pdl3(row_quantize_kernel<T, 2>, grid, threads(2), st, p);
-    return launch_pdl3(row_quantize_long_kernel<T>, grid, 1024, st, p);
+    if (chunks > 2048) return launch_pdl3(row_quantize_long_kernel<T>, grid, 1024, st, p);
+    if (p.vec) {
+        if (chunks <= 512) return launch_pdl3(row_quantize_kernel<T, 1, true, 512>, grid, threads(1), st, p);
+        if (chunks <= 1024) return launch_pdl3(row_quantize_kernel<T, 2, true, 1024>, grid, threads(2), st, p);
+        return launch_pdl3(row_quantize_kernel<T, 2, true, 1024>, grid, threads(2), st, p);
+    }
+    if (chunks <= 512) return launch_pdl3(row_quantize_kernel<T, 1, false, 512>, grid, threads(1), st, p);
+    if (chunks <= 1024) return launch_pdl3(row_quantize_kernel<T, 1, false, 1024>, grid, threads(1), st, p);
+    return launch_pdl3(row_quantize_kernel<T, 2, false, 1024>, grid, threads(2), st, p);
 }
 
 // Bytes copied in units of U: a block a row.
@@ -192,7 +198,7 @@ __global__ void __launch_bounds__(256) row_copy_kernel(const __grid_constant__ R
 }
 
 // A thread has 16 columns of a token; four of its rows are in flight together.
-template <typename T>
+template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ CombineParams p) {
     griddep_launch_dependents();
     const int64_t t = blockIdx.x;
@@ -200,7 +206,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Co
     griddep_wait();
     const bool use_c = p.beta != 0.0f;
     Raw16<T> c;
-    if (use_c) c = mx_load16<false>(static_cast<const T*>(p.C) + t * p.ldc, c0, cols, p.vec, p.C, p.c_end);
+    if (use_c) c = mx_load16<ALIGNED>(static_cast<const T*>(p.C) + t * p.ldc, c0, cols, p.vec, p.C, p.c_end);
     Row16 sum;
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum.p[i] = 0;
@@ -215,7 +221,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Co
             const int64_t row = some ? (int64_t)p.map[at] : -1;
             w[q] = some ? p.weights[at] : 0.0f;
             in[q] = row >= 0 && row < p.y_rows;
-            if (in[q]) y[q] = mx_load16<false>(static_cast<const T*>(p.Y) + row * p.ldy, c0, cols, p.vec, p.Y, p.y_end);
+            if (in[q]) y[q] = mx_load16<ALIGNED>(static_cast<const T*>(p.Y) + row * p.ldy, c0, cols, p.vec, p.Y, p.y_end);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -238,7 +244,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Co
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum.p[i] = fma2(b2, v.p[i], sum.p[i]);
     }
-    mx_store16<false>(static_cast<T*>(p.D) + t * p.ldd, c0, cols, p.vec, mx_round<T>(sum), lane);
+    mx_store16<ALIGNED>(static_cast<T*>(p.D) + t * p.ldd, c0, cols, p.vec, mx_round<T>(sum), lane);
 }
 
 }  // namespace
@@ -269,9 +275,9 @@ cudaError_t launch_row_copy(const RowsParams& p, cudaStream_t st) {
 cudaError_t launch_combine(const CombineParams& p, cudaStream_t st) {
     dim3 grid((unsigned)p.tokens, (unsigned)ceil_div(p.cols, 128 * 16));
     switch (p.type) {
-        case DT_F32: return launch_pdl3(combine_kernel<float>, grid, 128, st, p);
-        case DT_F16: return launch_pdl3(combine_kernel<__half>, grid, 128, st, p);
-        case DT_BF16: return launch_pdl3(combine_kernel<__nv_bfloat16>, grid, 128, st, p);
+        case DT_F32: return p.vec ? launch_pdl3(combine_kernel<float, true>, grid, 128, st, p) : launch_pdl3(combine_kernel<float, false>, grid, 128, st, p);
+        case DT_F16: return p.vec ? launch_pdl3(combine_kernel<__half, true>, grid, 128, st, p) : launch_pdl3(combine_kernel<__half, false>, grid, 128, st, p);
+        case DT_BF16: return p.vec ? launch_pdl3(combine_kernel<__nv_bfloat16, true>, grid, 128, st, p) : launch_pdl3(combine_kernel<__nv_bfloat16, false>, grid, 128, st, p);
         default: return cudaErrorInvalidValue;
     }
 }
