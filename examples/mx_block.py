@@ -124,9 +124,12 @@ def main():
     w = Weights(h, a.hidden, a.inner, a.experts, qg.GEMM_NVFP4 if a.format == "nvfp4" else qg.GEMM_MXFP4)
     offsets = None
     if a.experts:
-        pick = torch.randint(0, a.experts, (a.tokens,), device="cuda")
-        count = torch.bincount(pick, minlength=a.experts)
-        offsets = torch.cat([torch.zeros(1, dtype=torch.int64, device="cuda"), count.cumsum(0)]).int()
+        # one expert a token, by random logits; the block's rows are the tokens in that order
+        logits = torch.randn(a.tokens, a.experts, device="cuda")
+        new = lambda *shape: torch.empty(*shape, dtype=torch.int32, device="cuda")  # noqa: E731
+        ids, rows, offsets, weights = new(a.tokens, 1), new(a.tokens, 1), new(a.experts + 1), torch.empty(a.tokens, 1, device="cuda")
+        check(qg.gemm_moe_route(h, qg.gemm_route_t(topk=1, scale=1.0), qg.ptr(logits), qg.row_major(logits), qg.ptr(ids), qg.ptr(weights),
+                                qg.ptr(rows), qg.ptr(offsets), qg.Workspace().c, qg.current_stream()), "gemm_moe_route")
     b = Block(h, w, a.tokens, offsets)
     x = torch.randn(a.tokens, a.hidden, device="cuda").bfloat16()
     b.step(x)
