@@ -70,7 +70,7 @@ __device__ __forceinline__ int64_t expert_blocks(const S8GemmParams& P, int lane
 // A block of 32 tokens (m0 ..) x 32 channels (n0 ..) of finished sums, in `stage` with
 // a token a row: a lane has the same four channels of eight tokens, so that a token's
 // 32 channels are stored together.  tokens: the factor of token `lane`.
-template <int ACT, int DT>
+template <int ACT, int DT, bool USE_C>
 __device__ __forceinline__ void store_block(const S8GemmParams& P, const int32_t* stage, int64_t m0, int rows, int64_t n0, float tokens,
                                             const S8Channels& ch, int lane) {
     const EpiParams& e = P.epi;
@@ -78,34 +78,49 @@ __device__ __forceinline__ void store_block(const S8GemmParams& P, const int32_t
     ar.alpha = 1.0f;
     const int64_t n = n0 + 4 * (lane & 7);
     const int have = e.N - n < 4 ? (int)(e.N - n) : 4;
-    const bool vec = P.vec4 && have == 4, use_c = ar.beta != 0.0f;
-    const int64_t d_step = 4 * e.ldd, c_step = 4 * e.ldc;
-    int64_t d = (m0 + lane / 8) * e.ldd + n, cat = (m0 + lane / 8) * e.ldc + n;
+    const bool vec = P.vec4 && have == 4;
+    if constexpr (!USE_C) ar.beta = 0.0f;
+    const int64_t r0 = m0 + lane / 8;
+    // four rows' C in flight together: one by one, each after the last one's store,
+    // they took 4096^3 from 114 us to 181
+#pragma unroll 1
+    for (int q0 = 0; q0 < 8; q0 += 4) {
+        float c[4][4];
 #pragma unroll
-    for (int q = 0; q < 8; ++q, d += d_step, cat += c_step) {
-        const int r = 4 * q + lane / 8;
-        const float token = __shfl_sync(0xFFFFFFFFu, tokens, r);
-        if (r >= rows || have <= 0) continue;
-        const int4 s = *reinterpret_cast<const int4*>(stage + r * STAGE_PITCH + 4 * (lane & 7));
-        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f}, x[4];
-        if (use_c) {
+        for (int q = 0; q < 4; ++q) {
+            const int r = 4 * (q0 + q) + lane / 8;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) c[q][k] = 0.0f;
+            if (!USE_C || r >= rows || have <= 0) continue;
+            const int64_t at = (r0 + 4 * (q0 + q)) * e.ldc + n;
             if (vec) {
-                const float4 f = ld4(e.C, DT, cat);
-                c[0] = f.x, c[1] = f.y, c[2] = f.z, c[3] = f.w;
+                const float4 f = ld4(e.C, DT, at);
+                c[q][0] = f.x, c[q][1] = f.y, c[q][2] = f.z, c[q][3] = f.w;
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (k < have) c[k] = ld_elem(e.C, DT, cat + k);
+                    if (k < have) c[q][k] = ld_elem(e.C, DT, at + k);
             }
         }
-        mx_value2<ACT, DT>(ar, s8_scaled(s.x, token, ch.scale[0]), s8_scaled(s.y, token, ch.scale[1]), c[0], c[1], ch.bias[0], ch.bias[1], x[0], x[1]);
-        mx_value2<ACT, DT>(ar, s8_scaled(s.z, token, ch.scale[2]), s8_scaled(s.w, token, ch.scale[3]), c[2], c[3], ch.bias[2], ch.bias[3], x[2], x[3]);
-        if (vec) {
-            st4(e.D, DT, d, make_float4(x[0], x[1], x[2], x[3]));
-        } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (k < have) st_elem(e.D, DT, d + k, x[k]);
+        for (int q = 0; q < 4; ++q) {
+            const int r = 4 * (q0 + q) + lane / 8;
+            const float token = __shfl_sync(0xFFFFFFFFu, tokens, r);
+            if (r >= rows || have <= 0) continue;
+            const int4 s = *reinterpret_cast<const int4*>(stage + r * STAGE_PITCH + 4 * (lane & 7));
+            float x[4];
+            mx_value2<ACT, DT>(ar, s8_scaled(s.x, token, ch.scale[0]), s8_scaled(s.y, token, ch.scale[1]), c[q][0], c[q][1], ch.bias[0], ch.bias[1],
+                               x[0], x[1]);
+            mx_value2<ACT, DT>(ar, s8_scaled(s.z, token, ch.scale[2]), s8_scaled(s.w, token, ch.scale[3]), c[q][2], c[q][3], ch.bias[2], ch.bias[3],
+                               x[2], x[3]);
+            const int64_t at = (r0 + 4 * (q0 + q)) * e.ldd + n;
+            if (vec) {
+                st4(e.D, DT, at, make_float4(x[0], x[1], x[2], x[3]));
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < have) st_elem(e.D, DT, at + k, x[k]);
+            }
         }
     }
 }
@@ -113,12 +128,19 @@ __device__ __forceinline__ void store_block_any(const S8GemmParams& P, const int
                                                 const S8Channels& ch, int lane) {
     with_epi_act(P.epi, [&](auto act) {
         constexpr int ACT = decltype(act)::value;
-        if (P.epi.d_type == DT_BF16)
-            store_block<ACT, DT_BF16>(P, stage, m0, rows, n0, tokens, ch, lane);
-        else if (P.epi.d_type == DT_F16)
-            store_block<ACT, DT_F16>(P, stage, m0, rows, n0, tokens, ch, lane);
+        auto typed = [&](auto use_c) {
+            constexpr bool USE_C = decltype(use_c)::value;
+            if (P.epi.d_type == DT_BF16)
+                store_block<ACT, DT_BF16, USE_C>(P, stage, m0, rows, n0, tokens, ch, lane);
+            else if (P.epi.d_type == DT_F16)
+                store_block<ACT, DT_F16, USE_C>(P, stage, m0, rows, n0, tokens, ch, lane);
+            else
+                store_block<ACT, DT_F32, USE_C>(P, stage, m0, rows, n0, tokens, ch, lane);
+        };
+        if (P.epi.beta != 0.0f)
+            typed(std::true_type{});
         else
-            store_block<ACT, DT_F32>(P, stage, m0, rows, n0, tokens, ch, lane);
+            typed(std::false_type{});
     });
 }
 
@@ -273,6 +295,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         bool ok = true;
         for (int64_t i = pid; ok && pair_tile(P, blocks, i, lane, t); i += P.programs) {
             const int cols = t.tn / 2, c0 = half * cols;  // this warp's columns: a multiple of 16
+            const int64_t n0 = t.n0 + 128 * rank + 32 * quarter, m0 = t.row0 + c0;
+            const int rows = t.rows - c0 < cols ? t.rows - c0 : cols;
+            if (P.epi.beta != 0.0f && n0 < P.epi.N)
+                for (int r = lane; r < rows; r += 32) mx_prefetch_c(P.epi, m0 + r, n0, P.epi.N - n0 < 32 ? P.epi.N - n0 : 32);
             int32_t sum[HALF];
 #pragma unroll
             for (int q = 0; q < HALF; ++q) sum[q] = 0;
@@ -295,8 +321,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 if (lane == 0) mbar_arrive_remote_relaxed(l_tempty + 8u * b);
             }
             if (!ok) break;
-            const int64_t n0 = t.n0 + 128 * rank + 32 * quarter, m0 = t.row0 + c0;
-            const int rows = t.rows - c0 < cols ? t.rows - c0 : cols;
             if (rows <= 0 || n0 >= P.epi.N) continue;
             if (!mx_block_in_bounds(P.epi, m0, rows, n0, P.epi.N - n0 < 32 ? P.epi.N - n0 : 32)) continue;
             const S8Channels ch = s8_channels(P, ar, t.expert, n0 + 4 * (lane & 7));
