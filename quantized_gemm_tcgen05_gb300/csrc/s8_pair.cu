@@ -80,26 +80,47 @@ __device__ __forceinline__ void store_block(const S8GemmParams& P, const int32_t
     const int have = e.N - n < 4 ? (int)(e.N - n) : 4;
     const bool vec = P.vec4 && have == 4;
     if constexpr (!USE_C) ar.beta = 0.0f;
+    const bool whole = P.vec4 && n0 + 32 <= e.N && rows > 0;  // every lane's four channels exist
     const int64_t r0 = m0 + lane / 8;
-    // four rows' C in flight together: one by one, each after the last one's store,
-    // they took 4096^3 from 114 us to 181
+    // four rows' C in flight together (one by one, each after the last one's store, they
+    // took 4096^3 from 114 us to 181)
 #pragma unroll 1
     for (int q0 = 0; q0 < 8; q0 += 4) {
-        float c[4][4];
+        float c[4][4] = {};
+        if (USE_C && whole) {
+            // (no branch between the loads, and no conversion: the first one would wait)
+            using Raw = std::conditional_t<DT == DT_F32, uint4, uint2>;
+            Raw raw[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int r = 4 * (q0 + q) + lane / 8;
+            for (int q = 0; q < 4; ++q) {
+                const int r = 4 * (q0 + q) + lane / 8, in = r < rows ? r : rows - 1;
+                const int64_t at = (m0 + in) * e.ldc + n;
+                raw[q] = *reinterpret_cast<const Raw*>(static_cast<const char*>(e.C) + at * (DT == DT_F32 ? 4 : 2));
+            }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) c[q][k] = 0.0f;
-            if (!USE_C || r >= rows || have <= 0) continue;
-            const int64_t at = (r0 + 4 * (q0 + q)) * e.ldc + n;
-            if (vec) {
-                const float4 f = ld4(e.C, DT, at);
-                c[q][0] = f.x, c[q][1] = f.y, c[q][2] = f.z, c[q][3] = f.w;
-            } else {
+            for (int q = 0; q < 4; ++q) {
+                if constexpr (DT == DT_F32) {
+                    c[q][0] = __uint_as_float(raw[q].x), c[q][1] = __uint_as_float(raw[q].y);
+                    c[q][2] = __uint_as_float(raw[q].z), c[q][3] = __uint_as_float(raw[q].w);
+                } else {
+                    const uint32_t w[2] = {raw[q].x, raw[q].y};
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float2 f = DT == DT_BF16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]))
+                                                       : __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+                        c[q][2 * k] = f.x;
+                        c[q][2 * k + 1] = f.y;
+                    }
+                }
+            }
+        } else if (USE_C) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int r = 4 * (q0 + q) + lane / 8;
+                const int64_t at = (r0 + 4 * (q0 + q)) * e.ldc + n;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (k < have) c[q][k] = ld_elem(e.C, DT, at + k);
+                    if (r < rows && k < have) c[q][k] = ld_elem(e.C, DT, at + k);
             }
         }
 #pragma unroll
