@@ -16,7 +16,8 @@
 // All scores in 64 bits would take ten times the time: a 64-bit instruction of a warp
 // holds its unit for 16 cycles, and there is one unit an SM.
 // What bounds it is the number of instructions (some 800 a token of 256 experts) and
-// one token's chain of them: 4001 x 256 logits are 4 MB, 0.6 us.
+// one token's chain of them: 4001 x 256 logits are 4 MB, 0.6 us, and take 18 to 25 us with
+// bias and groups, 12.5 without; 16 x 8 tokens 3 us, one block.
 #include "common.cuh"
 #include "moe_params.h"
 

