@@ -26,7 +26,7 @@ extern "C" {
  * RN to nearest, ties to even (for amax / 127 < 2^-126 the factor is 2^126).  A row with a NaN
  * or an infinity gets a NaN scale and zero codes, so it shows in every product
  * it takes part in.  Q: row-major, GEMM_S8, any ld >= cols (gemm_run_s8 wants a
- * multiple of 16), as many matrices as X.  S: num * rows floats, matrix after
+ * multiple of 16), as many matrices as X; it must not overlap X.  S: num * rows floats, matrix after
  * matrix.  Weights [N, K] quantised like this are operand B: one scale per
  * output channel.
  */

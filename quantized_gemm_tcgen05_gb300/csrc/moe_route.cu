@@ -13,8 +13,8 @@
 //   2. where neighbours in that order are too near, a lane takes each of the
 //      candidates and compares 32-bit keys (a token in ten or twenty);
 //   3. ... and 64-bit scores (one in a thousand).
-// All scores in 64 bits would take ten times the time: a 64-bit instruction of a warp
-// holds its unit for 16 cycles, and there is one unit an SM.
+// All scores in 64 bits would take several times the time (16 tokens of 256 experts that
+// all need them 46 us, else 9): this GPU has little 64-bit arithmetic.
 // What bounds it is the number of instructions (some 800 a token of 256 experts) and
 // one token's chain of them: 4001 x 256 logits are 4 MB, 0.6 us, and take 18 to 25 us with
 // bias and groups, 12.5 without; 16 x 8 tokens 3 us, one block.

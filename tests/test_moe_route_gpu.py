@@ -141,6 +141,17 @@ def test_masked_experts_and_undefined_tokens(h, ws, tokens, biased, score):
         assert w.isnan().all() and int(off[-1]) == 0
 
 
+@pytest.mark.parametrize("tokens", [17, 40, 64])
+def test_one_block_without_a_workspace(h, ws, tokens):
+    l = normal(tokens, tokens, 40)
+    bias = (0.1 * torch.randn(40, generator=torch.Generator().manual_seed(3))).cuda()
+    for a, b in zip(check(h, None, l, 5, bias=bias), check(h, ws, l, 5, bias=bias)):
+        assert torch.equal(a, b)
+    bias.fill_(-torch.inf)  # nobody may be chosen
+    ids, w, rows, off = check(h, None, l, 5, bias=bias)
+    assert (ids == -1).all() and (w == 0).all() and (off == 0).all()
+
+
 def test_renormalised_weights_of_tiny_scores(h, ws):
     """A bias can choose experts whose scores underflow: their shares are still right."""
     l = torch.zeros(3, 8, device="cuda")
