@@ -128,8 +128,9 @@ def main():
         logits = torch.randn(a.tokens, a.experts, device="cuda")
         new = lambda *shape: torch.empty(*shape, dtype=torch.int32, device="cuda")  # noqa: E731
         ids, rows, offsets, weights = new(a.tokens, 1), new(a.tokens, 1), new(a.experts + 1), torch.empty(a.tokens, 1, device="cuda")
+        workspace = qg.Workspace()
         check(qg.gemm_moe_route(h, qg.gemm_route_t(topk=1, scale=1.0), qg.ptr(logits), qg.row_major(logits), qg.ptr(ids), qg.ptr(weights),
-                                qg.ptr(rows), qg.ptr(offsets), qg.Workspace().c, qg.current_stream()), "gemm_moe_route")
+                                qg.ptr(rows), qg.ptr(offsets), workspace.c, qg.current_stream()), "gemm_moe_route")
     b = Block(h, w, a.tokens, offsets)
     x = torch.randn(a.tokens, a.hidden, device="cuda").bfloat16()
     b.step(x)

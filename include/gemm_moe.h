@@ -53,7 +53,7 @@ typedef struct {
  * NULL.  With them, more than 64 tokens need workspace partials of
  * GEMM_ROUTE_SCRATCH(experts) bytes (GEMM_ERR_WORKSPACE); barriers are not used.
  */
-#define GEMM_ROUTE_SCRATCH(experts) ((size_t)304 * 4 * (size_t)(experts))
+#define GEMM_ROUTE_SCRATCH(experts) ((size_t)304 * 16 * (((size_t)(experts) + 7) / 8))
 int gemm_moe_route(gemm_handle_t h, const gemm_route_t* op, const void* L, const gemm_layout_t* Ldesc, int32_t* ids,
                    float* weights, int32_t* rows, int32_t* expert_offsets, const gemm_workspace_t* workspace,
                    gemm_stream_t stream);

@@ -349,7 +349,7 @@ def gemm_run_s8_grouped(h, op, alpha, A, Adesc, SA, B, Bdesc, SB, beta, C, Cdesc
 
 def gemm_route_scratch(experts) -> int:
     """Bytes of workspace partials that gemm_moe_route may need (GEMM_ROUTE_SCRATCH)."""
-    return 304 * 4 * int(experts)
+    return 304 * 16 * (-(-int(experts) // 8))
 
 
 def gemm_moe_route(h, op, L, Ldesc, ids, weights, rows, expert_offsets, workspace, stream):

@@ -15,7 +15,8 @@
 using namespace qg;
 
 static_assert((int)GEMM_ROUTE_SOFTMAX == (int)ROUTE_SOFTMAX && (int)GEMM_ROUTE_SIGMOID == (int)ROUTE_SIGMOID, "");
-static_assert(GEMM_ROUTE_SCRATCH(1) == sizeof(int32_t) * ROUTE_MAX_BLOCKS, "");
+// counts of a block: one per expert, in octets
+static_assert(GEMM_ROUTE_SCRATCH(1) == 8 * sizeof(uint16_t) * ROUTE_MAX_BLOCKS && GEMM_ROUTE_SCRATCH(9) == 2 * GEMM_ROUTE_SCRATCH(1), "");
 
 namespace {
 

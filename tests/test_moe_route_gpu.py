@@ -163,6 +163,19 @@ def test_renormalised_weights_of_tiny_scores(h, ws):
         assert ids.tolist() == [[2, 5]] * 3
 
 
+@pytest.mark.parametrize("tokens,experts", [(6000, 1), (6000, 2), (3000, 9), (4000, 257)])
+def test_workspace_of_the_stated_size(h, tokens, experts):
+    """Nothing past GEMM_ROUTE_SCRATCH bytes is written."""
+    n = qg.gemm_route_scratch(experts)
+    buf = torch.full((n + 65536,), 171, dtype=torch.uint8, device="cuda")
+
+    class Exact:
+        c = qg.gemm_workspace_t(None, 0, qg.ptr(buf), n)
+
+    check(h, Exact, normal(1, tokens, experts, x="bf16"), 1)
+    assert (buf[n:] == 171).all()
+
+
 def test_no_tokens(h, ws):
     l = torch.empty(0, 8, device="cuda")
     off = torch.full((9,), 5, dtype=torch.int32, device="cuda")
@@ -232,7 +245,7 @@ def test_refusals(h, ws):
                workspace=ws.c)
     lay = lambda **kw: qg.gemm_layout_t(**{**{f: getattr(arg["Ldesc"], f) for f, _ in qg.gemm_layout_t._fields_}, **kw})  # noqa: E731
     small = qg.gemm_workspace_t(None, 0, ws.c.partials, qg.gemm_route_scratch(16) - 1)
-    assert qg.gemm_route_scratch(16) == 304 * 4 * 16
+    assert qg.gemm_route_scratch(16) == 304 * 32 and qg.gemm_route_scratch(1) == 304 * 16
     cases = [
         (dict(score=2), {}, UNS), (dict(score=-1), {}, UNS), (dict(topk=0), {}, INV), (dict(topk=17), {}, INV), (dict(scale=float("nan")), {}, INV),
         (dict(scale=float("inf")), {}, INV), (dict(renormalize=2), {}, INV), (dict(groups=-1), {}, INV),
