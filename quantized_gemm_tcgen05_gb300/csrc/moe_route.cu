@@ -240,7 +240,13 @@ __device__ __noinline__ int choose_among(const RouteParams& p, int t, float top,
         // (all lanes take part in both exchanges)
         const float next_l = __shfl_down_sync(FULL, l, 1), next_b = __shfl_down_sync(FULL, b, 1);
         const bool same = l == next_l && b == next_b;
-        doubt = lane < p.topk && lane + 1 < n && !same && !(x - y > 2.0f * choice_error(err, fmaxf(fabsf(x), fabsf(y))));
+        const bool near = lane + 1 < n && !(x - y > 2.0f * choice_error(err, fmaxf(fabsf(x), fabsf(y))));
+        // The last slot's run goes on for as long as neighbours are near, equal ones among
+        // them: what stands in doubt anywhere in it may belong before it.  Behind a
+        // neighbour that is certainly smaller nothing can.
+        const unsigned run = __ballot_sync(FULL, near) >> (p.topk - 1);
+        const int end = p.topk - 1 + __ffs((int)~run) - 1;  // (lane 31 has no next one)
+        doubt = near && !same && lane < end;
     }
     if (__any_sync(FULL, doubt)) {
         double sum = 0.0;
