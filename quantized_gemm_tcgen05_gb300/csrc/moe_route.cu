@@ -140,12 +140,17 @@ __device__ __forceinline__ unsigned keep_groups(const RouteParams& p, const K (&
         better += other > mine || (other == mine && g < lane);
     }
     const bool kept = lane < p.groups && better < p.group_topk;
-    const K high = warp_max(!kept ? mine : (K)0);
-    if (err > 0.0f && high) {
-        // (all groups kept are live here) the best one left out against each one kept
-        const float x = (float)score, y = (float)number_of(high);
-        const float far = fmaxf(fabsf(x), fabsf(y));
-        if (__any_sync(FULL, kept && !(x - y > 2.0f * (2.0f * err + 2.4e-7f * far)))) sure = false;
+    if (err > 0.0f) {
+        // A group's score is off by what its one or two c are, each by its own size (they
+        // may cancel), and by the sum's rounding.  Every group kept against the best one
+        // left out, which may be any whose error reaches so high.
+        const bool both = two && m2;
+        const float size = fabsf((float)number_of(m1)) + (both ? fabsf((float)number_of(m2)) : 0.0f), x = (float)score;
+        const float off = m1 ? choice_error(both ? 2.0f * err : err, size + fabsf(x)) : 0.0f;
+        const K high = warp_max(!kept ? mine : (K)0);
+        const float most = __uint_as_float(warp_max(!kept && mine ? __float_as_uint(off) : 0u));
+        // (with a live one left out, all groups kept are live)
+        if (high && __any_sync(FULL, kept && !(x - (float)number_of(high) > off + most))) sure = false;
     }
     return __ballot_sync(FULL, kept);
 }
