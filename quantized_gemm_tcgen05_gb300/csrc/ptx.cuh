@@ -399,19 +399,26 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// The same with a release at the scope of this CTA: what this CTA's own tensor core
-// or threads read before the other CTA goes on from the barrier, as its half of a
-// pair's operands.  (The release at cluster scope cost 1000 cycles a K-step there.)
-__device__ __forceinline__ void mbar_arrive_remote_cta(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
 // The same without the release, for arrivals that publish no ordinary memory:
 // TMEM handed over (its accesses completed by tcgen05.wait and fenced by
 // tc_fence_before_sync), or shared memory that the caller has done with.  The
 // release at cluster scope costs about a microsecond per arrival.
 __device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// A release at cluster scope of what was written to this CTA's shared memory, and of
+// nothing else, then the arrival: what a CTA's threads hand to MMAs that a thread of
+// another CTA issues (it waits with mbar_try_wait_cluster).  The order, for the odd CTA's
+// half of a pair's operands: the writers' stores and their fence.proxy.async, the warp's
+// synchronisation, this fence and the relaxed arrival; the acquiring wait at cluster
+// scope, the MMA.  TMEM is handed over by the same arrival, between
+// tcgen05.fence::before_thread_sync and ::after_thread_sync.  A release that orders global
+// memory too waits for it: mbar_arrive_remote in this place took the int8 product of
+// 4096^3 from 116 us to 148.
+__device__ __forceinline__ void mbar_arrive_remote_smem(uint32_t cluster_addr) {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+    mbar_arrive_remote_relaxed(cluster_addr);
 }
 
 // try_wait with cluster-scope acquire, for phases completed by the peer CTA.

@@ -270,13 +270,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                 for (int j0 = 0; ok && j0 < nslots; j0 += SLOT_CHUNK, ++chunk) {
                     const uint32_t b = chunk & 1, d = tmem + TN * b;
                     const int n = nslots - j0 < SLOT_CHUNK ? nslots - j0 : SLOT_CHUNK;
-                    ok = __all_sync(0xFFFFFFFFu, wait_bar(&tempty[b], ((chunk >> 1) & 1) ^ 1, g, SITE_MMA_TMEM_EMPTY));
+                    ok = __all_sync(0xFFFFFFFFu, wait_bar_cluster(&tempty[b], ((chunk >> 1) & 1) ^ 1, g, SITE_MMA_TMEM_EMPTY));
                     // Two slots at a time: waiting and issuing take this warp some 500 cycles
                     // a turn, eight MMAs 768.
                     for (int j = 0; ok && j < n; j += 2) {
-                        // (this thread reads nothing that the other CTA wrote: its tensor core
-                        // does, there, so no acquire at cluster scope is needed)
-                        ok = __all_sync(0xFFFFFFFFu, wait_bar(&ready[slot / 2], ph, g, SITE_MMA_OPERAND));
+                        ok = __all_sync(0xFFFFFFFFu, wait_bar_cluster(&ready[slot / 2], ph, g, SITE_MMA_OPERAND));
                         if (!ok) break;
                         tc_fence_after_sync();
                         const uint64_t xd = xd0 + (uint64_t)((uint32_t)slot * (SLOT_BYTES / 16));
@@ -395,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     if (leader)
                         mbar_arrive(&ready[slot / 2]);
                     else
-                        mbar_arrive_remote_cta(l_ready);
+                        mbar_arrive_remote_smem(l_ready);
                 }
             }
         }
