@@ -60,8 +60,10 @@ int gemm_moe_route(gemm_handle_t h, const gemm_route_t* op, const void* L, const
 
 /*
  * Place row t of X at rows rows[t * topk + j] of Y, j < topk.  Y has X's type
- * (f32, f16, bf16, GEMM_S8, GEMM_E4M3, GEMM_E5M2; S is NULL), or is GEMM_S8 with X f32 / f16 / bf16: its
- * rows are quantised as gemm_s8_quantize does and S[row] is the scale.  Entries
+ * (f32, f16, bf16, GEMM_S8, GEMM_E4M3, GEMM_E5M2), or is GEMM_S8 with X f32 / f16 / bf16: its
+ * rows are quantised as gemm_s8_quantize does and S[row] is the scale.  Rows that are
+ * copied have no S: it is NULL (else GEMM_ERR_INVALID_ARG).  The scales of rows that are
+ * int8 already are placed by a second call, as f32 rows of one column.  Entries
  * outside 0 .. Y's rows - 1 are left out, rows of Y that no entry names keep
  * what they held.  No row may be named twice.  X and Y: row-major, any ld; they
  * must not overlap.

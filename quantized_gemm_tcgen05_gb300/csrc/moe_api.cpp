@@ -183,11 +183,13 @@ int gemm_moe_dispatch(gemm_handle_t h, const void* X, const gemm_layout_t* Xdesc
             bool q;
             gemm_layout_t x = *Xdesc;
             x.rows = 0;
-            return rows_params(h, X, &x, rows, 2, Y, Ydesc, S, &none, &q);
+            rc = rows_params(h, X, &x, rows, 2, Y, Ydesc, S, &none, &q);
+            return rc || q || !S ? rc : (int)GEMM_ERR_INVALID_ARG;
         }
         RowsParams p;
         bool quantise = false;
         if ((rc = rows_params(h, X, Xdesc, rows, topk, Y, Ydesc, S, &p, &quantise))) return rc;
+        if (!quantise && S) return (int)GEMM_ERR_INVALID_ARG;  // nothing would be written there
         const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
         return status_of(quantise ? launch_row_quantize(p, st) : launch_row_copy(p, st));
     });
