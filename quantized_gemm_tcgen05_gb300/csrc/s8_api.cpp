@@ -197,6 +197,7 @@ S8Choice choose(const S8GemmParams& p, int sm_count, int clusters, int forced_sp
     };
     for (int width : {32, 128}) {
         if (pinned && (forced.kernel != S8_TILE || forced.width != width)) continue;
+        if (!pinned && !s8_gemm_usable(width)) continue;  // the other serves the call
         const int rows = (int)(ceil_div(ceil_div(each, ceil_div(each, width)), 16) * 16);
         for (int splits : {1, 2, 4, 8}) {
             if (splits > steps || (forced_split && splits > forced_split)) continue;

@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(Cfg<TN>::THREADS, Cfg<TN>::CTAS)
 }
 
 template <int TN>
-cudaError_t launch_t(const S8Maps& m, const S8GemmParams& p, int grid, cudaStream_t st) {
+cudaError_t configure() {
     static std::atomic<uint64_t> configured{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -394,6 +394,13 @@ cudaError_t launch_t(const S8Maps& m, const S8GemmParams& p, int grid, cudaStrea
         if (e != cudaSuccess) return e;
         configured.fetch_or(bit);
     }
+    return cudaSuccess;
+}
+
+template <int TN>
+cudaError_t launch_t(const S8Maps& m, const S8GemmParams& p, int grid, cudaStream_t st) {
+    const cudaError_t e = configure<TN>();
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(Cfg<TN>::THREADS);
@@ -427,6 +434,12 @@ cudaError_t launch_s8_gemm(int width, const S8Maps& m, const S8GemmParams& p, in
         case 128: return launch_t<128>(m, p, grid, st);
         default: return cudaErrorInvalidValue;
     }
+}
+
+bool s8_gemm_usable(int width) {
+    if ((width == 32 ? configure<32>() : configure<128>()) == cudaSuccess) return true;
+    cudaGetLastError();
+    return false;
 }
 
 }  // namespace qg

@@ -45,6 +45,8 @@ int s8_gemv_slices(int64_t n, int64_t k, int64_t tiles, int sm_count);
 // The tensor-core kernel, one tile of 128 channels x up to `width` tokens per
 // cluster (width 32 or 128).
 cudaError_t launch_s8_gemm(int width, const S8Maps& m, const S8GemmParams& p, int grid, cudaStream_t st);
+// Whether the kernel was built with the registers that its warps share out.
+bool s8_gemm_usable(int width);
 
 // The CTA-pair kernel: 256 channels x up to S8_PAIR_TOKENS tokens, persistent
 // clusters of two.
