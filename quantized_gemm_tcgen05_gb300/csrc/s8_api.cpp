@@ -181,8 +181,13 @@ S8Choice choose(const S8GemmParams& p, int sm_count, int clusters, int forced_sp
     S8Choice forced{S8_GEMV, 0, 0, 1}, best{S8_TILE, 32, 16, 1};
     const bool pinned = forced_kernel(&forced);
     if (pinned ? forced.kernel == S8_GEMV : each <= 1 && !forced_split) {
-        best.kernel = S8_GEMV;  // 1x4096x14336 13.3 us, in tiles 15.4
-        best.rows = each <= 1 ? 1 : each <= 2 ? 2 : each <= 4 ? 4 : 8;
+        // One token: 1x4096x14336 13.3 us, in tiles 15.4.  By experts with a row each on
+        // average, popular ones first, each row reads its expert's weights: 8 rows by 32
+        // experts of 2048 x 4096 13.6 us, in tiles 20.9; 8 by 8 of 4096 x 14336 64, 73; 32 by
+        // 32 of 512 x 512 4.8, 6.1.  Tiles are quicker where many experts have several
+        // rows: 32 by 32 of 2048 x 4096 30, here 41; 64 by 64 50, 71; 256 by 256 168, 282.
+        best.kernel = S8_GEMV;
+        best.rows = 1;
         return best;
     }
     double best_us = -1.0;
@@ -239,9 +244,9 @@ int run_product(gemm_handle_t h, const gemm_op_t* op, S8GemmParams& p, cudaStrea
         if (tm > 65535) return GEMM_ERR_UNSUPPORTED;
         p.tiles_m = (int32_t)tm;
         p.kslices = s8_gemv_slices(N, p.K, tm, handle_sm_count(h));
-        snprintf(name, sizeof name, "s8%s_gemv%d/k%d", grouped, c.rows, p.kslices);
+        snprintf(name, sizeof name, "s8%s_gemv/k%d", grouped, p.kslices);
         handle_set_choice(h, name, M, N, p.K);
-        return status_of(launch_s8_gemv(p, handle_sm_count(h), st));
+        return status_of(launch_s8_gemv(p, st));
     }
     const bool pair = c.kernel == S8_PAIR;
     const int64_t tn = ceil_div(N, pair ? 256 : 128);

@@ -1,22 +1,21 @@
-// Streaming int8 product on the CUDA cores, for a few rows per expert: B's codes
-// are read once and are the work, four products an instruction (dp4a) into exact
-// 32-bit sums.
+// Streaming int8 product on the CUDA cores, one token at a time: B's codes are the
+// work, four products an instruction (dp4a) into exact 32-bit sums.
 //
 // A warp owns R = 4 rows of B and one of `kslices` contiguous slices of K; its lanes
-// take 16-byte chunks.  A block of 8 warps covers 8 / kslices row groups for one tile
-// of MT tokens.  Lanes' and slices' sums are integers: any order gives the same.
+// take U 16-byte chunks at a time.  A block of 8 warps covers 8 / kslices row groups for
+// one token.  Lanes' and slices' sums are integers: any order gives the same.
 //
 // Measured: 1x4096x14336 13.3 us (59 MB: 4.4 TB/s), launch and the last warps' sums a
-// third of it; with two tokens 18.5, where a tile on the tensor cores takes 15.6.
-#include <atomic>
-
+// third of it.  Two, four or eight tokens a warp were no quicker than the tensor cores
+// (2x4096x14336 18.5 us, there 15.6) and, by experts, no quicker than a token each (32
+// rows by 32 experts of 2048 x 4096: 40.7 us, with two 41.8, four 42.0, eight 48.9).
 #include "s8_epilogue.cuh"
 
 namespace qg {
 
 namespace {
 
-constexpr int R = 4, WARPS = 8;
+constexpr int R = 4, WARPS = 8, U = 2;
 
 // Chunk c of a row of K codes; past K zeros, and nothing is read there.
 __device__ __forceinline__ uint4 chunk_of(const int8_t* row, int64_t c, int64_t K) {
@@ -35,9 +34,8 @@ __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int s) {
     return __dp4a((int)a.w, (int)b.w, s);
 }
 
-template <int MT, int U>
-__global__ void __launch_bounds__(WARPS * 32, MT == 1 ? 4 : 2) s8_gemv_kernel(const __grid_constant__ S8GemmParams p) {
-    __shared__ int32_t red[WARPS][MT][R];
+__global__ void __launch_bounds__(WARPS * 32, 4) s8_gemv_kernel(const __grid_constant__ S8GemmParams p) {
+    __shared__ int32_t red[WARPS][R];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = p.kslices, per_block = WARPS / S;
     const int gi = warp / S, s = warp % S;
@@ -59,24 +57,16 @@ __global__ void __launch_bounds__(WARPS * 32, MT == 1 ? 4 : 2) s8_gemv_kernel(co
             }
     }
     griddep_wait();
-    int expert = 0, rows = 0;
-    int64_t m0 = 0, atom_row = 0;
-    if (p.offsets) {
-        if (!mx_expert_block(p.offsets, p.num_experts, p.epi.M, MT, blockIdx.y, lane, &expert, &m0, &rows, &atom_row)) return;
-    } else {
-        m0 = (int64_t)blockIdx.y * MT;
-        rows = (int)(p.epi.M - m0 < MT ? p.epi.M - m0 : MT);
-    }
+    int expert = 0, rows = 1;
+    int64_t row = blockIdx.y, atom_row = 0;
+    if (p.offsets && !mx_expert_block(p.offsets, p.num_experts, p.epi.M, 1, blockIdx.y, lane, &expert, &row, &rows, &atom_row)) return;
     if (rows <= 0) return;
+    const int8_t* A = p.A + row * p.lda;
     const int8_t* B = p.B + expert * p.b_bs;
     const EpiArith ar0 = epi_arith(p.epi);
     for (int64_t gbase = (int64_t)blockIdx.x * per_block; gbase < ngroups; gbase += (int64_t)gridDim.x * per_block) {
         const int64_t grp = gbase + gi;
-        int32_t acc[MT][R];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int r = 0; r < R; ++r) acc[m][r] = 0;
+        int32_t acc[R] = {};
         if (grp < ngroups) {
             const int8_t* brow[R];
 #pragma unroll
@@ -92,35 +82,29 @@ __global__ void __launch_bounds__(WARPS * 32, MT == 1 ? 4 : 2) s8_gemv_kernel(co
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (c + 32 * u >= cend) break;
+                    const uint4 a = chunk_of(A, c + 32 * u, K);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        if (m >= rows) break;
-                        const uint4 a = chunk_of(p.A + (m0 + m) * p.lda, c + 32 * u, K);
-#pragma unroll
-                        for (int r = 0; r < R; ++r) acc[m][r] = dot16(a, b[u][r], acc[m][r]);
-                    }
+                    for (int r = 0; r < R; ++r) acc[r] = dot16(a, b[u][r], acc[r]);
                 }
             }
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-                const int32_t v = __reduce_add_sync(0xFFFFFFFFu, acc[m][r]);
-                if (lane == 0) red[warp][m][r] = v;
-            }
+        for (int r = 0; r < R; ++r) {
+            const int32_t v = __reduce_add_sync(0xFFFFFFFFu, acc[r]);
+            if (lane == 0) red[warp][r] = v;
+        }
         __syncthreads();
         // a thread takes a pair of neighbouring columns
-        for (int t = threadIdx.x; t < per_block * MT * (R / 2); t += WARPS * 32) {
-            const int g2 = t / (MT * (R / 2)), m = t / (R / 2) % MT, r = t % (R / 2) * 2;
-            const int64_t n = (gbase + g2) * R + r, row = m0 + m;
-            if (m >= rows || n >= N) continue;
+        for (int t = threadIdx.x; t < per_block * (R / 2); t += WARPS * 32) {
+            const int g2 = t / (R / 2), r = t % (R / 2) * 2;
+            const int64_t n = (gbase + g2) * R + r;
+            if (n >= N) continue;
             const int have = N - n < 2 ? 1 : 2;
             if (!mx_block_in_bounds(p.epi, row, 1, n, have)) continue;
             int32_t s0 = 0, s1 = 0;
             for (int k = 0; k < S; ++k) {
-                s0 += red[g2 * S + k][m][r];
-                s1 += red[g2 * S + k][m][r + 1];
+                s0 += red[g2 * S + k][r];
+                s1 += red[g2 * S + k][r + 1];
             }
             EpiArith ar = ar0;
             ar.alpha = 1.0f;
@@ -143,8 +127,20 @@ __global__ void __launch_bounds__(WARPS * 32, MT == 1 ? 4 : 2) s8_gemv_kernel(co
     }
 }
 
-template <int MT, int U>
-cudaError_t launch_t(const S8GemmParams& p, int sm_count, cudaStream_t st) {
+}  // namespace
+
+int s8_gemv_slices(int64_t n, int64_t k, int64_t tokens, int sm_count) {
+    // as many slices as leave all warps resident at once and every lane a chunk
+    // (1x4096x14336: 13.3 us in four, 15.5 in eight, 17.8 in two; 1x14336x4096 14.2 us
+    // unsliced, 16 in two or four)
+    const int64_t groups = ceil_div(n, R), nchunk = ceil_div(k, 16), resident = (int64_t)sm_count * 32;
+    int s = 1;
+    while (s < WARPS && groups * tokens * 2 * s <= resident && nchunk / (2 * s) >= 32) s *= 2;
+    return s;
+}
+
+cudaError_t launch_s8_gemv(const S8GemmParams& p, cudaStream_t st) {
+    if (p.tiles_m < 1 || p.tiles_m > 65535 || p.tile_rows != 1) return cudaErrorInvalidValue;
     const int64_t groups = ceil_div(p.epi.N, R), blocks = ceil_div(groups, WARPS / p.kslices);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(blocks < 1 << 30 ? blocks : 1 << 30), (unsigned)p.tiles_m);
@@ -155,30 +151,7 @@ cudaError_t launch_t(const S8GemmParams& p, int sm_count, cudaStream_t st) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, s8_gemv_kernel<MT, U>, p);
-}
-
-}  // namespace
-
-int s8_gemv_slices(int64_t n, int64_t k, int64_t tiles, int sm_count) {
-    // as many slices as leave all warps resident at once and every lane a chunk
-    // (1x4096x14336: 13.3 us in four, 15.5 in eight, 17.8 in two; 1x14336x4096 14.2 us
-    // unsliced, 16 in two or four)
-    const int64_t groups = ceil_div(n, R), nchunk = ceil_div(k, 16), resident = (int64_t)sm_count * 32;
-    int s = 1;
-    while (s < WARPS && groups * tiles * 2 * s <= resident && nchunk / (2 * s) >= 32) s *= 2;
-    return s;
-}
-
-cudaError_t launch_s8_gemv(const S8GemmParams& p, int sm_count, cudaStream_t st) {
-    if (p.tiles_m < 1 || p.tiles_m > 65535) return cudaErrorInvalidValue;
-    switch (p.tile_rows) {
-        case 1: return launch_t<1, 2>(p, sm_count, st);
-        case 2: return launch_t<2, 2>(p, sm_count, st);
-        case 4: return launch_t<4, 1>(p, sm_count, st);
-        case 8: return launch_t<8, 1>(p, sm_count, st);
-        default: return cudaErrorInvalidValue;
-    }
+    return cudaLaunchKernelEx(&cfg, s8_gemv_kernel, p);
 }
 
 }  // namespace qg

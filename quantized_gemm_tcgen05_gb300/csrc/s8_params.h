@@ -37,10 +37,9 @@ struct S8Maps {
 constexpr int S8_KSTEP = 128;   // codes of one 128-byte swizzle row
 constexpr int S8_CHUNK = 8;     // K-steps whose sums fp32 holds exactly: 1024 products of at most 2^14
 
-// The streaming kernel on the CUDA cores: any M, meant for a few rows per expert.
-constexpr int S8_GEMV_ROWS = 8;  // tokens of a tile, at most
-cudaError_t launch_s8_gemv(const S8GemmParams& p, int sm_count, cudaStream_t st);
-int s8_gemv_slices(int64_t n, int64_t k, int64_t tiles, int sm_count);
+// The streaming kernel on the CUDA cores: a token a tile, up to 65535 of them.
+cudaError_t launch_s8_gemv(const S8GemmParams& p, cudaStream_t st);
+int s8_gemv_slices(int64_t n, int64_t k, int64_t tokens, int sm_count);
 
 // The tensor-core kernel, one tile of 128 channels x up to `width` tokens per
 // cluster (width 32 or 128).

@@ -14,3 +14,9 @@ def test_choice(h, m, n, k, want):  # noqa: F811
     p = Problem(m, n, k)
     p.run(h)
     assert qg.gemm_last_choice(h).startswith(want)
+
+
+def test_choice_by_experts(h):  # noqa: F811
+    for sizes, want in (([1, 0, 2, 0], "s8_grouped_gemv/"), ([20, 0, 30, 0], "s8_grouped_t")):
+        Problem(sum(sizes), 96, 160, sizes=sizes).check(h)
+        assert qg.gemm_last_choice(h).startswith(want)
