@@ -172,8 +172,9 @@ cudaError_t quantize_t(const RowsParams& p, cudaStream_t st) {
         return launch_pdl3(row_quantize_kernel<T, 2, false, 1024>, grid, threads(2), st, p);
     }
     if (!p.vec) return launch_pdl3(row_quantize_kernel<T, 1, false, 512>, grid, threads(1), st, p);
-    if (sizeof(T) == 2 && chunks >= 128 && p.rows >= 1024)
-        return launch_pdl3(row_quantize_kernel<T, 2, true, 256>, grid, threads(2), st, p);
+    if constexpr (sizeof(T) == 2) {
+        if (chunks >= 128 && p.rows >= 1024) return launch_pdl3(row_quantize_kernel<T, 2, true, 256>, grid, threads(2), st, p);
+    }
     return launch_pdl3(row_quantize_kernel<T, 1, true, 512>, grid, threads(1), st, p);
 }
 
