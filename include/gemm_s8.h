@@ -43,7 +43,9 @@ int gemm_s8_quantize(gemm_handle_t h, const void* X, const gemm_layout_t* Xdesc,
  * K need not be.  The sum is exact, as in 32-bit integers (K at most 131071, above it
  * GEMM_ERR_UNSUPPORTED); it is converted to fp32, multiplied by alpha * SA[i] and
  * by SB[j], and finished as in gemm_run: fp32 steps, one rounding to D's type.
- * Of op, epilogue / bias / bias_type apply (GELU as in gemm_run_mx); splitk
+ * Of op, epilogue / bias / bias_type apply; GELU is x Phi(x) as in gemm_run_mx: for an
+ * f32 D in gemm.h's form, off by up to 1.5 * 2^-22 |x| (at x = -5 some parts in a hundred
+ * of the result, which is small there), for a 16-bit D within 2e-5, relative; splitk
  * forces that many K slices (1, 2, 4 or 8, as far as K has 128-wide steps for
  * them; 0 chooses) where a kernel that slices K serves the call; dispatch is
  * accepted and the built-in choice used.  U / V groups, streamk = 1, zero points,

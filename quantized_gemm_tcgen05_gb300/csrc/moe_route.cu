@@ -15,9 +15,13 @@
 //   3. ... and 64-bit scores (one in a thousand).
 // All scores in 64 bits would take several times the time (16 tokens of 256 experts that
 // all need them 46 us, else 9): this GPU has little 64-bit arithmetic.
-// What bounds it is the number of instructions (some 800 a token of 256 experts) and
-// one token's chain of them: 4001 x 256 logits are 4 MB, 0.6 us, and take 18 to 25 us with
-// bias and groups, 12.5 without; 16 x 8 tokens 3 us, one block.
+// What bounds it: 4001 x 256 logits are 4 MB, 0.6 us, and take 18.7 to 25.7 us with bias and
+// groups, 12.5 without.  With them the choice takes half of that: some 1900
+// instructions a token of 256 experts, which the schedulers issue in 58% of their cycles;
+// the rest is latency, above all the block's wait for its longest token (the stall
+// sampled most is the barrier behind the loop).  The rows take the other half: a launch
+// whose schedulers issue in 29% of the cycles, waiting for counts and for one warp a
+// block that places its pairs.  16 x 8 tokens 3 us, one block.
 #include "common.cuh"
 #include "moe_params.h"
 

@@ -275,9 +275,11 @@ __device__ __forceinline__ void mx_store_block(const EpiParams& e, bool vec32, f
         mx_store_block_dt<DT_F32>(e, vec32, alpha, m0, rows, n0, v, stage, lane);
 }
 
-// Warp-wide: block b (of `bm` rows, a multiple of 128) of rows sorted by
-// expert -> expert, its first row, its rows (those below M, the rows there are),
-// and the scale atom row it starts on.  Returns false past the last block.
+// Warp-wide: block b (of `bm` rows) of rows sorted by expert -> expert, its first
+// row, its rows (those below M, the rows there are; 0 or fewer: none), and, for a bm
+// that is a multiple of 128, the scale atom row it starts on.  Returns false past the
+// last block.  Offsets that are no partition of the rows may give any expert and row
+// (the sums of their blocks may wrap), but none outside 0 .. M - 1.
 __device__ __forceinline__ bool mx_expert_block(const int32_t* off, int32_t E, int64_t M, int bm, int64_t b, int lane,
                                                 int* expert, int64_t* row0, int* rows, int64_t* atom_row) {
     int64_t blocks = 0, tiles = 0;

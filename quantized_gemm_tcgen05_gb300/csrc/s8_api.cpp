@@ -149,12 +149,12 @@ bool forced_kernel(S8Choice* c) {
 // launches, cold operands:
 //   one tile, up to 32 tokens    5 us for set-up, first data and epilogue; a K-step of
 //     128 0.40 us, 0.50 where two CTAs share an SM, 0.08 more with 32 tokens than with 16;
-//     K slices 3 us (8x4096x4096 9.2 us in eight, 16x4096x14336 16.0 in eight, 22 in four,
-//     256x4096x4096 24.7, 512x4096x4096 47.8)
+//     K slices 3 us (8x4096x4096 9.3 us in eight, 16x4096x14336 16.1 in eight, 22 in four,
+//     256x4096x4096 24.5, 512x4096x4096 47.5)
 //   one tile, up to 128 tokens   7.5 us; a K-step 0.36 us and 0.0025 a token
-//     (77x11002x4104 26.6, 128x14336x4096 28.8, 256x4096x4096 22.2 in two slices)
+//     (77x11002x4104 26.0, 128x14336x4096 28.7, 256x4096x4096 22.0 in two slices)
 //   CTA pair                     9 us once; a K-step of a wave of tiles 0.51 us with 96
-//     tokens, 0.53 with 128, 0.61 with 160, 0.65 with 192 (4096^3: 168, 129, 126, 114 us)
+//     tokens, 0.53 with 128, 0.61 with 160, 0.65 with 192 (4096^3: 169, 132, 129, 116 us)
 double estimate(const S8GemmParams& p, int sm_count, int clusters, const S8Choice& c) {
     const double n = (double)p.epi.N, k = (double)p.K;
     const int64_t steps = ceil_div(p.K, S8_KSTEP);

@@ -16,8 +16,9 @@
 //   then 4 or 8 warps of sums, 8 or 16 of operands (up to 32 tokens two CTAs share an
 //   SM, each with half as many); the epilogue is all warps'
 // Measured (back-to-back launches, cold operands): up to 32 tokens 16x4096x14336 16 us,
-// 32 rows by 8 experts of 14336 x 4096 83 us (5.7 TB/s); up to 128 tokens
-// 128x14336x4096 29 us, 512x4096x4096 29. A K-step is a chain of waits of half a microsecond
+// 32 rows by 8 experts of 14336 x 4096 83 us (5.7 TB/s); up to 128 tokens 256x4096x4096
+// 22.0 us in two K slices, 128x14336x4096 28.7 and 512x4096x4096 28.4 (the CTA pair, which is
+// chosen for these two, 27.5 and 26.3). A K-step is a chain of waits of half a microsecond
 // (without conversion and MMAs 77x11002x4104 took 23 us of 29), set-up, first data and
 // end of a CTA 5 to 7.5 us.
 #include <atomic>

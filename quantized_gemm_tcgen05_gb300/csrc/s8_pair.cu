@@ -11,10 +11,10 @@
 //   warps 0-3    TMA producer, (leader) MMAs, two without work
 //   warps 4-11   sums and epilogue: a 32-lane quarter and half of the columns each
 //   warps 12-27  f16 operands
-// Measured (back-to-back launches, cold operands): 4096^3 111 to 115 us by the card (1.2
-// PFLOP/s; the MMAs alone would take 68), with C 133, with GELU 128; 4096 x 14336 x 4096
-// 350 to 365 us, 1.35 PFLOP/s; 4096 rows by 8 experts 407. A slot takes 0.33 us of which
-// its MMAs are 0.20; the rest is the chain from the slot's release to its next MMAs.
+// Measured (back-to-back launches, cold operands): 4096^3 116 us (1.18 PFLOP/s; the MMAs
+// alone would take 68), with C 134, with GELU 130; 4096 x 14336 x 4096 370 us, 1.30
+// PFLOP/s; 4096 rows by 8 experts 419. A slot takes 0.33 us of which its MMAs are 0.20; the
+// rest is the chain from the slot's release to its next MMAs.
 #include <atomic>
 
 #include "mx_rows.h"
